@@ -533,6 +533,156 @@ int tdp_pixel_plan_sizes(const tdp_pixel_plan* plan, int64_t* tile_elems, int64_
  * it fails. */
 int tdp_pixel_blend(const tdp_pixel_plan* plan, const void* tiles, void* out, void* stream);
 
+/* ---- the tile's attention: rotation, norms, attention, gradients ---------- */
+
+/* What a denoising transformer computes on the buffers that tdp_extract
+ * fills: queries and keys are turned by the tile's three-axis positions
+ * (TDP docs, "Position normalization": they are handed to the model per
+ * tile), usually after a norm of each head, and every token attends the used
+ * rows of its tile's slot, the kept conditioning tokens among them.  The
+ * calls below take (rows, heads, head_dim) tensors that follow the slots,
+ * for all tiles at once, and each has its gradient.
+ *
+ * Rows come in sequences.  Sequence s owns the rows [row_range[2 s],
+ * row_range[2 s + 1]) (uniformly max_rows each, one after another, when
+ * row_range is NULL) and uses the first len of them, len = seq_len[s /
+ * len_group] (all of them when seq_len is NULL).  tdp_plan_sequences gives a
+ * plan's ranges, and tile_count is its seq_len with len_group = B.  Unused
+ * rows may hold anything, NaN included, in every input; outputs there are 0.
+ * Rows outside every range are left alone.  Both arrays are read on the
+ * device: a range outside [0, total_rows], an end below its start or a length
+ * outside the sequence is clamped.  Ranges of written tensors must not
+ * overlap. */
+typedef struct {
+  int32_t num_seqs;          /* S >= 1                                          */
+  int32_t max_rows;          /* rows of the longest sequence, 1 .. 2^24; rows   */
+                             /* of a sequence past it are left alone            */
+  int64_t total_rows;        /* rows of the tensors (S * max_rows when          */
+                             /* row_range is NULL), < 2^31                      */
+  const int64_t* row_range;  /* device, (S, 2) [start, end), or NULL            */
+  const int32_t* seq_len;    /* device, used rows, entry s / len_group, or NULL */
+  int32_t len_group;         /* >= 1 sequences that share an entry of seq_len   */
+} tdp_seqs;
+
+/* A (rows, heads, head_dim) tensor: element strides, head_dim contiguous.
+ * Row i of sequence s starts at (row_range[2 s] + i) * row_stride, or at
+ * s * seq_stride + i * row_stride when row_range is NULL.  data is 16-byte
+ * aligned and every stride a multiple of 16 bytes, so slices of a packed
+ * projection and head-major tensors pass as they are. */
+typedef struct {
+  void* data;
+  int64_t seq_stride, row_stride, head_stride;
+  int32_t heads;
+} tdp_heads;
+
+/* The row ranges of a plan's sequences, slot by slot and batch element by
+ * batch element: 2 * num_slots * batch host int64 entries, rows of tile_lat.
+ * TDP_EINVAL for a null argument. */
+int tdp_plan_sequences(const tdp_plan* plan, int64_t* row_range);
+
+/* Rotation by several position axes (host only).  The head's first
+ * rot_dim[0] dims turn with the time position, the next rot_dim[1] with
+ * height, the next rot_dim[2] with width, the rest pass unchanged.  Pair i of
+ * an axis turns by freqs[i] radians per position unit (rot_dim / 2 values per
+ * axis, the axes one after another).  A pair is dims (2i, 2i + 1) of its
+ * section (TDP_PAIR_INTERLEAVED) or (i, i + rot_dim / 2) (TDP_PAIR_HALVES):
+ *   y0 = x0 cos(a) - x1 sin(a),  y1 = x0 sin(a) + x1 cos(a),  a = f * p
+ * with p the middle of the token's [start, end) interval (TDP_POINT_MIDDLE)
+ * or its start (TDP_POINT_START).  Angles are reduced as two-float turns, so
+ * positions far from the origin lose nothing against 64 bits that an fp32
+ * result could hold. */
+#define TDP_PAIR_INTERLEAVED 0
+#define TDP_PAIR_HALVES 1
+#define TDP_POINT_MIDDLE 0
+#define TDP_POINT_START 1
+#define TDP_MAX_ROPE_DIM 256      /* head_dim of the rotation and the norms     */
+#define TDP_MAX_ATTENTION_DIM 128 /* head_dim of the attention                  */
+typedef struct tdp_rope tdp_rope; /* opaque host object owned by the library    */
+typedef struct {
+  int32_t head_dim;   /* a multiple of 8, at most TDP_MAX_ROPE_DIM              */
+  int32_t rot_dim[3]; /* even, >= 0, together at most head_dim                  */
+  int32_t pairing;    /* TDP_PAIR_*                                             */
+  int32_t point;      /* TDP_POINT_*                                            */
+} tdp_rope_config;
+/* TDP_EINVAL for a null argument (freqs may be NULL when nothing turns), an
+ * unknown pairing or point or a frequency that is not finite or above 1e6;
+ * TDP_ESHAPE for dims out of range. */
+int tdp_rope_create(const tdp_rope_config* cfg, const double* freqs, tdp_rope** out);
+void tdp_rope_destroy(tdp_rope* rope);
+
+/* y = x turned by its positions (inverse != 0: by their negatives, which is
+ * also the gradient).  pos holds, per sequence, three planes of
+ * as many [start, end) float pairs as its range has rows, from float 6 times
+ * the range's start on: tile_pos as it is (8-byte aligned).  dtype (TDP_F32 or TDP_BF16) is
+ * that of x and y; the arithmetic is fp32, rounded once.  y may be x (same
+ * strides); otherwise they must not overlap.  One launch.
+ * Errors of this and the next four calls, nothing enqueued: TDP_EINVAL for
+ * null or misaligned pointers, bad counts, dtypes or strides; TDP_ESHAPE for
+ * sizes out of range or a launch past 2^32 - 1 work-items.  TDP_EHIP when a
+ * launch fails. */
+int tdp_rope_apply(const tdp_rope* rope, const tdp_seqs* seqs, const float* pos, const tdp_heads* x,
+                   const tdp_heads* y, int32_t dtype, int32_t inverse, void* stream);
+
+/* Per-head norm of queries and keys and their rotation in one pass:
+ *   y = turn(x * r * w),  r = 1 / sqrt(mean(x^2) + eps)
+ * per row and head, w (head_dim) fp32, one for queries and one for keys
+ * (NULL: ones).  q_out may be q and k_out k (same strides).  One launch. */
+int tdp_qk_norm_rope(const tdp_rope* rope, const tdp_seqs* seqs, const float* pos, const tdp_heads* q,
+                     const tdp_heads* k, const float* q_weight, const float* k_weight, const tdp_heads* q_out,
+                     const tdp_heads* k_out, float eps, int32_t dtype, void* stream);
+
+/* Its gradient, from the inputs and the outputs' gradients (r is computed
+ * again, nothing is saved): with n = turn^-1(dy) and g = n * w,
+ *   dx = r * (g - x * r^2 * mean(g * x)),  dw = sum over rows and heads of n * x * r.
+ * dq may be dq_out and dk dk_out (same strides).  dq_weight and dk_weight
+ * (head_dim) fp32 are written, not added to (NULL: not wanted).  The sums run
+ * in a fixed order, so results repeat bit for bit.  workspace: device, 16-byte
+ * aligned, of tdp_qk_norm_rope_workspace bytes (0 for bad arguments); its
+ * contents mean nothing between calls, and calls that share it must not
+ * overlap. */
+int64_t tdp_qk_norm_rope_workspace(const tdp_rope* rope, const tdp_seqs* seqs, int32_t q_heads, int32_t k_heads);
+int tdp_qk_norm_rope_backward(const tdp_rope* rope, const tdp_seqs* seqs, const float* pos, const tdp_heads* q,
+                              const tdp_heads* k, const float* q_weight, const float* k_weight,
+                              const tdp_heads* dq_out, const tdp_heads* dk_out, const tdp_heads* dq,
+                              const tdp_heads* dk, float* dq_weight, float* dk_weight, float eps, int32_t dtype,
+                              void* workspace, void* stream);
+
+/* Attention of each sequence's queries over the keys and values of the same
+ * sequence of k_seqs (the tile's own rows, or a prompt's):
+ *   s_ij = scale * q_i . k_j + key_bias_j,  out_i = sum_j softmax_j(s_ij) v_j
+ * q.heads is a multiple of k.heads; query head h reads key head
+ * h / (q.heads / k.heads).  key_bias (NULL: none) is one fp32 per key row
+ * (k_seqs.total_rows), shared by all heads; a key whose bias is -infinity takes
+ * no part, whatever its rows hold.  A query with no key left gives 0.  lse
+ * (NULL: not wanted) receives log(sum_j exp(s_ij)) as fp32 (q.heads,
+ * q_seqs.total_rows), -infinity where no key is left or the row is unused.
+ * Scores, softmax and sums are fp32; for TDP_BF16 the softmax's weights are
+ * rounded to bf16 for the product with v, as its matrix instructions take
+ * them.  out overlaps no input.  head_dim is a multiple of 8, at most
+ * TDP_MAX_ATTENTION_DIM; scale is finite and > 0.  workspace as above, of
+ * tdp_attention_workspace bytes (0: NULL allowed): where few query rows meet
+ * long keys, the keys are split over workgroups and joined from there. */
+int64_t tdp_attention_workspace(const tdp_seqs* q_seqs, const tdp_seqs* k_seqs, int32_t q_heads, int32_t k_heads,
+                                int32_t head_dim);
+int tdp_attention(const tdp_seqs* q_seqs, const tdp_seqs* k_seqs, const tdp_heads* q, const tdp_heads* k,
+                  const tdp_heads* v, const float* key_bias, const tdp_heads* out, float* lse, float scale,
+                  int32_t head_dim, int32_t dtype, void* workspace, void* stream);
+
+/* Its gradients, the probabilities computed again from lse: with
+ * p = exp(s - lse) and delta_i = dout_i . out_i,
+ *   ds = p * (dout_i . v_j - delta_i),  dq = scale * sum_j ds k_j,
+ *   dk = scale * sum_i ds q_i,  dv = sum_i p dout_i,
+ * dk and dv summed over the query heads that share a key head.  out and lse
+ * come from tdp_attention on the same arguments.  No atomics: results repeat
+ * bit for bit.  key_bias takes no gradient.  workspace as above, of
+ * tdp_attention_backward_workspace bytes. */
+int64_t tdp_attention_backward_workspace(const tdp_seqs* q_seqs, const tdp_seqs* k_seqs, int32_t q_heads,
+                                         int32_t k_heads, int32_t head_dim);
+int tdp_attention_backward(const tdp_seqs* q_seqs, const tdp_seqs* k_seqs, const tdp_heads* q, const tdp_heads* k,
+                           const tdp_heads* v, const float* key_bias, const tdp_heads* out, const float* lse,
+                           const tdp_heads* dout, const tdp_heads* dq, const tdp_heads* dk, const tdp_heads* dv,
+                           float scale, int32_t head_dim, int32_t dtype, void* workspace, void* stream);
+
 /* ---- errors ------------------------------------------------------------ */
 /* Errors are reported, never produced silently, and a guard violation names
  * the axis and the largest overlap it allows (mold #673, "A bug found while

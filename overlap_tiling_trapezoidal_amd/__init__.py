@@ -22,7 +22,8 @@ DEFAULT_LIB_PATH = os.path.join(_HERE, "libtdp.so")
 LIB_PATH = os.environ.get("TDP_LIBRARY") or DEFAULT_LIB_PATH
 DEVICE_FUNCTIONS = ("tdp_extract", "tdp_extract_noalloc", "tdp_set_lookback_polls", "tdp_pipeline_step",
                     "tdp_extract_positions", "tdp_extract_latent", "tdp_pipeline_latent_step", "tdp_blend",
-                    "tdp_blend_tile", "tdp_blend_finish", "tdp_pixel_blend")
+                    "tdp_blend_tile", "tdp_blend_finish", "tdp_pixel_blend", "tdp_rope_apply", "tdp_qk_norm_rope",
+                    "tdp_qk_norm_rope_backward", "tdp_attention", "tdp_attention_backward")
 HEADER_PATH = os.path.join(os.path.dirname(_HERE), "include", "tdp.h")
 
 # ---- constants (mirror include/tdp.h) --------------------------------------
@@ -37,6 +38,12 @@ TDP_NORMALIZE_POSITIONS = 0x1
 TDP_UNGUARDED = 0x2
 TDP_MAX_TILES_PER_AXIS = 32
 TDP_STATIC_SCRATCH_BYTES = 1 << 20
+TDP_PAIR_INTERLEAVED = 0
+TDP_PAIR_HALVES = 1
+TDP_POINT_MIDDLE = 0
+TDP_POINT_START = 1
+TDP_MAX_ROPE_DIM = 256
+TDP_MAX_ATTENTION_DIM = 128
 
 _DTYPES = {"f32": TDP_F32, "float32": TDP_F32, "bf16": TDP_BF16, "bfloat16": TDP_BF16}
 
@@ -125,6 +132,36 @@ class tdp_quality(ctypes.Structure):
     ]
 
 
+class tdp_seqs(ctypes.Structure):
+    _fields_ = [
+        ("num_seqs", ctypes.c_int32),
+        ("max_rows", ctypes.c_int32),
+        ("total_rows", ctypes.c_int64),
+        ("row_range", ctypes.c_void_p),
+        ("seq_len", ctypes.c_void_p),
+        ("len_group", ctypes.c_int32),
+    ]
+
+
+class tdp_heads(ctypes.Structure):
+    _fields_ = [
+        ("data", ctypes.c_void_p),
+        ("seq_stride", ctypes.c_int64),
+        ("row_stride", ctypes.c_int64),
+        ("head_stride", ctypes.c_int64),
+        ("heads", ctypes.c_int32),
+    ]
+
+
+class tdp_rope_config(ctypes.Structure):
+    _fields_ = [
+        ("head_dim", ctypes.c_int32),
+        ("rot_dim", ctypes.c_int32 * 3),
+        ("pairing", ctypes.c_int32),
+        ("point", ctypes.c_int32),
+    ]
+
+
 class TdpError(RuntimeError):
     def __init__(self, status: int, message: str):
         super().__init__(f"{message} [{status}]")
@@ -145,6 +182,7 @@ def load_library(path: str = LIB_PATH):
                           "(python overlap_tiling_trapezoidal_amd/build.py)")
     lib = ctypes.CDLL(path)
     vp, i32, i32p = ctypes.c_void_p, ctypes.c_int32, ctypes.POINTER(ctypes.c_int32)
+    f32, sq, hd = ctypes.c_float, ctypes.POINTER(tdp_seqs), ctypes.POINTER(tdp_heads)
     sig = {
         "tdp_plan_create": (ctypes.c_int, [ctypes.POINTER(tdp_config), ctypes.POINTER(vp)]),
         "tdp_plan_create_rank": (ctypes.c_int, [ctypes.POINTER(tdp_config), i32, i32, ctypes.POINTER(vp)]),
@@ -176,6 +214,20 @@ def load_library(path: str = LIB_PATH):
         "tdp_pixel_plan_sizes": (ctypes.c_int, [vp, ctypes.POINTER(ctypes.c_int64), ctypes.POINTER(ctypes.c_int64),
                                                 i32p]),
         "tdp_pixel_blend": (ctypes.c_int, [vp] * 4),
+        "tdp_plan_sequences": (ctypes.c_int, [vp, ctypes.POINTER(ctypes.c_int64)]),
+        "tdp_rope_create": (ctypes.c_int, [ctypes.POINTER(tdp_rope_config), ctypes.POINTER(ctypes.c_double),
+                                           ctypes.POINTER(vp)]),
+        "tdp_rope_destroy": (None, [vp]),
+        "tdp_rope_apply": (ctypes.c_int, [vp, sq, vp, hd, hd, i32, i32, vp]),
+        "tdp_qk_norm_rope": (ctypes.c_int, [vp, sq, vp, hd, hd, vp, vp, hd, hd, f32, i32, vp]),
+        "tdp_qk_norm_rope_workspace": (ctypes.c_int64, [vp, sq, i32, i32]),
+        "tdp_qk_norm_rope_backward": (ctypes.c_int, [vp, sq, vp, hd, hd, vp, vp, hd, hd, hd, hd, vp, vp, f32, i32, vp,
+                                                     vp]),
+        "tdp_attention_workspace": (ctypes.c_int64, [sq, sq, i32, i32, i32]),
+        "tdp_attention": (ctypes.c_int, [sq, sq, hd, hd, hd, vp, hd, vp, f32, i32, i32, vp, vp]),
+        "tdp_attention_backward_workspace": (ctypes.c_int64, [sq, sq, i32, i32, i32]),
+        "tdp_attention_backward": (ctypes.c_int, [sq, sq, hd, hd, hd, vp, hd, vp, hd, hd, hd, hd, f32, i32, i32, vp,
+                                                  vp]),
         "tdp_status_string": (ctypes.c_char_p, [ctypes.c_int]),
         "tdp_last_error": (ctypes.c_char_p, []),
     }
@@ -712,3 +764,284 @@ def tdp_pixel_blend(plan: PixelPlan, tiles, out, stream=None):
     _check(load_library().tdp_pixel_blend(plan.handle, _ptr(tiles, "tiles", _torch_dtype(c.in_dtype), tile_elems, dev),
                                           _ptr(out, "out", _torch_dtype(c.out_dtype), out_elems, dev),
                                           _stream_handle(stream, dev)))
+
+
+# ---------------------------------------------------------------------------
+# The tile's attention: rotation, norms, attention and their gradients
+# ---------------------------------------------------------------------------
+
+class Sequences:
+    """How the rows of (rows, heads, head_dim) tensors fall into sequences.
+
+    ``num_seqs`` sequences of ``max_rows`` rows each, one after another; or
+    sequence s owns rows [row_start[s], row_start[s + 1]) (``row_start``: S + 1
+    int64, ascending) or row_range[s] (``row_range``: (S, 2) int64), none longer
+    than ``max_rows``.  ``seq_len`` (int32) holds the used rows, entry
+    s // len_group.  The tensors live on the GPU and are kept alive here.
+    """
+
+    def __init__(self, num_seqs, max_rows, row_start=None, row_range=None, total_rows=None, seq_len=None,
+                 len_group=1):
+        import torch
+        if row_start is not None:
+            if row_range is not None:
+                raise ValueError("row_start and row_range are two forms of the same: give one")
+            if row_start.numel() != num_seqs + 1:
+                raise ValueError(f"row_start holds {row_start.numel()} entries, needs {num_seqs + 1}")
+            row_range = torch.stack([row_start[:-1], row_start[1:]], dim=1)
+        if row_range is None:
+            rows = num_seqs * max_rows
+            if total_rows not in (None, rows):
+                raise ValueError(f"{num_seqs} sequences of {max_rows} rows span {rows} rows, not {total_rows}")
+            total_rows = rows
+        elif total_rows is None:
+            raise ValueError("total_rows is required with row_start or row_range")
+        if len_group < 1:
+            raise ValueError("len_group must be >= 1")
+        s = tdp_seqs()
+        s.num_seqs, s.max_rows, s.total_rows, s.len_group = num_seqs, max_rows, total_rows, len_group
+        dev = None
+        if row_range is not None:
+            row_range = row_range.contiguous()
+            s.row_range = _ptr(row_range, "row_range", torch.int64, 2 * num_seqs, None)
+            dev = row_range.device
+        if seq_len is not None:
+            s.seq_len = _ptr(seq_len, "seq_len", torch.int32, (num_seqs + len_group - 1) // len_group, dev)
+            dev = seq_len.device
+        self.c, self.device = s, dev
+        self._keep = (row_range, seq_len)
+
+    num_seqs = property(lambda self: self.c.num_seqs)
+    max_rows = property(lambda self: self.c.max_rows)
+    total_rows = property(lambda self: self.c.total_rows)
+
+
+def tdp_plan_sequences(plan: Plan) -> list[tuple[int, int]]:
+    """[start, end) rows of tile_lat per sequence: slot by slot, batch element by batch element."""
+    n = tdp_plan_sizes(plan).num_slots * plan.cfg.batch
+    buf = (ctypes.c_int64 * max(1, 2 * n))()
+    _check(load_library().tdp_plan_sequences(plan.handle, buf))
+    return [(buf[2 * i], buf[2 * i + 1]) for i in range(n)]
+
+
+def plan_sequences(plan: Plan, tile_count=None, device="cuda") -> Sequences:
+    """The Sequences of a plan's slots; ``tile_count`` (tdp_extract's) gives the
+    used rows, otherwise every row of a slot counts as used."""
+    import torch
+    ranges = tdp_plan_sequences(plan)
+    if not ranges:
+        raise ValueError("the plan holds no tiles")
+    rows = tdp_plan_sizes(plan).tile_pos_floats // 6
+    return Sequences(len(ranges), max(b - a for a, b in ranges),
+                     row_range=torch.tensor(ranges, dtype=torch.int64, device=torch.device(device)),
+                     total_rows=rows, seq_len=tile_count, len_group=plan.cfg.batch)
+
+
+class RopeConfig:
+    """tdp_rope_config with its frequencies (see make_rope_config)."""
+
+    def __init__(self, cfg: tdp_rope_config, freqs):
+        self.cfg, self.freqs = cfg, freqs
+
+
+def make_rope_config(head_dim, rot_dims, theta=10000.0, scale=(1.0, 1.0, 1.0), freqs=None, pairing="interleaved",
+                     point="middle") -> RopeConfig:
+    """Fill a tdp_rope_config.  ``rot_dims``: dims turned by (time, height, width).
+    Pair i of an axis turns by scale * theta ** (-2 i / rot_dim) radians per
+    position unit, or by freqs[axis][i]."""
+    cfg = tdp_rope_config()
+    cfg.head_dim = head_dim
+    for a in range(3):
+        cfg.rot_dim[a] = rot_dims[a]
+    cfg.pairing = {"interleaved": TDP_PAIR_INTERLEAVED, "halves": TDP_PAIR_HALVES}.get(pairing, pairing)
+    cfg.point = {"middle": TDP_POINT_MIDDLE, "start": TDP_POINT_START}.get(point, point)
+    if freqs is None:
+        freqs = [[scale[a] * theta ** (-2.0 * i / r) for i in range(r // 2)] for a, r in enumerate(rot_dims)]
+    for a in range(3):
+        if len(freqs[a]) != max(rot_dims[a], 0) // 2:
+            raise ValueError(f"axis {a}: {len(freqs[a])} frequencies for {rot_dims[a]} dims")
+    return RopeConfig(cfg, [float(f) for axis in freqs for f in axis])
+
+
+class Rope:
+    """Owns a tdp_rope handle (host memory only)."""
+
+    def __init__(self, handle: int, cfg: tdp_rope_config):
+        self.handle, self.cfg = ctypes.c_void_p(handle), cfg
+
+    def __del__(self):
+        if getattr(self, "handle", None) and _lib is not None:
+            _lib.tdp_rope_destroy(self.handle)
+            self.handle = None
+
+
+def tdp_rope_create(config: RopeConfig) -> Rope:
+    h = ctypes.c_void_p()
+    freqs = (ctypes.c_double * max(1, len(config.freqs)))(*config.freqs)
+    _check(load_library().tdp_rope_create(ctypes.byref(config.cfg), freqs, ctypes.byref(h)))
+    return Rope(h.value, config.cfg)
+
+
+def _dtype_code(t, name):
+    import torch
+    if t.dtype == torch.bfloat16:
+        return TDP_BF16
+    if t.dtype == torch.float32:
+        return TDP_F32
+    raise ValueError(f"{name} must be torch.float32 or torch.bfloat16, got {t.dtype}")
+
+
+def _heads(t, name, seqs: Sequences, head_dim, like, written=False):
+    """tdp_heads of a (total_rows, heads, head_dim) tensor, or of a
+    (num_seqs, max_rows, heads, head_dim) one for uniform sequences."""
+    if t is None:
+        raise ValueError(f"{name} is required")
+    if not t.is_cuda or t.device != like.device:
+        raise ValueError(f"{name} must be on {like.device if like.is_cuda else 'a GPU'}, got {t.device}")
+    if seqs.device is not None and seqs.device != t.device:
+        raise ValueError(f"{name} is on {t.device}, its sequences on {seqs.device}")
+    if t.dtype != like.dtype:
+        raise ValueError(f"{name} must be {like.dtype}, got {t.dtype}")
+    h = tdp_heads()
+    if t.dim() == 4 and not seqs.c.row_range:
+        if t.shape[0] != seqs.num_seqs or t.shape[1] != seqs.max_rows:
+            raise ValueError(f"{name} is {tuple(t.shape)}, needs ({seqs.num_seqs}, {seqs.max_rows}, heads, {head_dim})")
+        h.seq_stride, h.row_stride, h.head_stride = t.stride()[:3]
+    elif t.dim() == 3:
+        if t.shape[0] != seqs.total_rows:
+            raise ValueError(f"{name} holds {t.shape[0]} rows, needs {seqs.total_rows}")
+        h.row_stride, h.head_stride = t.stride()[:2]
+        h.seq_stride = seqs.max_rows * h.row_stride
+    else:
+        raise ValueError(f"{name} must be (rows, heads, head_dim), or (sequences, rows, heads, head_dim) without row "
+                         f"ranges; got {tuple(t.shape)}")
+    if t.shape[-1] != head_dim or (head_dim > 1 and t.stride(-1) != 1):
+        raise ValueError(f"{name} needs {head_dim} contiguous elements per head, got {tuple(t.shape)} with strides "
+                         f"{t.stride()}")
+    if written:   # every element its own place
+        dims = sorted((st, n) for st, n in zip(t.stride(), t.shape) if n > 1)
+        reach = 1
+        for st, n in dims:
+            if st < reach:
+                raise ValueError(f"{name} is written and must not overlap itself (strides {t.stride()})")
+            reach = st * (n - 1) + reach
+    # a dimension of one element is never stepped over: torch may report any stride for it
+    sizes = t.shape[:-1] if t.dim() == 4 else (1,) + tuple(t.shape[:-1])
+    if sizes[-1] == 1:
+        h.head_stride = 0
+    if sizes[-2] == 1:
+        h.row_stride = 0
+    if t.dim() == 4 and sizes[0] == 1 or seqs.num_seqs == 1:
+        h.seq_stride = 0
+    h.data, h.heads = t.data_ptr(), t.shape[-2]
+    return h
+
+
+def _vec(t, name, dtype, numel, device):
+    return ctypes.c_void_p(None) if t is None else _ptr(t, name, dtype, numel, device)
+
+
+def _pos_ptr(rope: Rope, seqs: Sequences, pos, device):
+    import torch
+    if not any(rope.cfg.rot_dim):
+        return ctypes.c_void_p(None)
+    return _ptr(pos, "pos", torch.float32, 6 * seqs.total_rows, device)
+
+
+def tdp_rope_apply(rope: Rope, seqs: Sequences, pos, x, y, inverse=False, stream=None):
+    """Enqueue y = x turned by the positions ``pos`` (tile_pos, or (S, 3, rows, 2));
+    ``inverse`` turns back, which is also the gradient.  y may be x."""
+    ref = ctypes.byref
+    D = rope.cfg.head_dim
+    _check(load_library().tdp_rope_apply(
+        rope.handle, ref(seqs.c), _pos_ptr(rope, seqs, pos, x.device), ref(_heads(x, "x", seqs, D, x)),
+        ref(_heads(y, "y", seqs, D, x, True)), _dtype_code(x, "x"), int(bool(inverse)),
+        _stream_handle(stream, x.device)))
+
+
+def tdp_qk_norm_rope(rope: Rope, seqs: Sequences, pos, q, k, q_weight, k_weight, q_out, k_out, eps=1e-6, stream=None):
+    """Enqueue the norm of every query and key head (times fp32 weights, None: ones) and its rotation."""
+    import torch
+    ref, D, dev = ctypes.byref, rope.cfg.head_dim, q.device
+    _check(load_library().tdp_qk_norm_rope(
+        rope.handle, ref(seqs.c), _pos_ptr(rope, seqs, pos, dev), ref(_heads(q, "q", seqs, D, q)),
+        ref(_heads(k, "k", seqs, D, q)), _vec(q_weight, "q_weight", torch.float32, D, dev),
+        _vec(k_weight, "k_weight", torch.float32, D, dev), ref(_heads(q_out, "q_out", seqs, D, q, True)),
+        ref(_heads(k_out, "k_out", seqs, D, q, True)), eps, _dtype_code(q, "q"), _stream_handle(stream, dev)))
+
+
+def allocate_qk_norm_rope_workspace(rope: Rope, seqs: Sequences, q_heads: int, k_heads: int, device="cuda"):
+    import torch
+    n = load_library().tdp_qk_norm_rope_workspace(rope.handle, ctypes.byref(seqs.c), q_heads, k_heads)
+    if n <= 0:
+        raise TdpError(TDP_EINVAL, tdp_last_error())
+    return torch.empty(n, dtype=torch.uint8, device=torch.device(device))
+
+
+def tdp_qk_norm_rope_backward(rope: Rope, seqs: Sequences, pos, q, k, q_weight, k_weight, dq_out, dk_out, dq, dk,
+                              dq_weight, dk_weight, workspace, eps=1e-6, stream=None):
+    """Enqueue the gradients of tdp_qk_norm_rope (dq may be dq_out, dk may be dk_out)."""
+    import torch
+    ref, D, dev = ctypes.byref, rope.cfg.head_dim, q.device
+    sq, sk = _heads(q, "q", seqs, D, q), _heads(k, "k", seqs, D, q)
+    need = load_library().tdp_qk_norm_rope_workspace(rope.handle, ref(seqs.c), sq.heads, sk.heads)
+    _check(load_library().tdp_qk_norm_rope_backward(
+        rope.handle, ref(seqs.c), _pos_ptr(rope, seqs, pos, dev), ref(sq), ref(sk),
+        _vec(q_weight, "q_weight", torch.float32, D, dev), _vec(k_weight, "k_weight", torch.float32, D, dev),
+        ref(_heads(dq_out, "dq_out", seqs, D, q)), ref(_heads(dk_out, "dk_out", seqs, D, q)),
+        ref(_heads(dq, "dq", seqs, D, q, True)), ref(_heads(dk, "dk", seqs, D, q, True)),
+        _vec(dq_weight, "dq_weight", torch.float32, D, dev), _vec(dk_weight, "dk_weight", torch.float32, D, dev),
+        eps, _dtype_code(q, "q"), _ptr(workspace, "workspace", torch.uint8, need, dev), _stream_handle(stream, dev)))
+
+
+def allocate_attention_workspace(q_seqs: Sequences, k_seqs: Sequences, q_heads: int, k_heads: int, head_dim: int,
+                                 device="cuda"):
+    """Workspace of tdp_attention, or None where it needs none."""
+    import torch
+    n = load_library().tdp_attention_workspace(ctypes.byref(q_seqs.c), ctypes.byref(k_seqs.c), q_heads, k_heads,
+                                               head_dim)
+    return torch.empty(n, dtype=torch.uint8, device=torch.device(device)) if n else None
+
+
+def allocate_attention_backward_workspace(q_seqs: Sequences, k_seqs: Sequences, q_heads: int, k_heads: int,
+                                          head_dim: int, device="cuda"):
+    import torch
+    n = load_library().tdp_attention_backward_workspace(ctypes.byref(q_seqs.c), ctypes.byref(k_seqs.c), q_heads,
+                                                        k_heads, head_dim)
+    if n <= 0:
+        raise TdpError(TDP_EINVAL, tdp_last_error())
+    return torch.empty(n, dtype=torch.uint8, device=torch.device(device))
+
+
+def tdp_attention(q_seqs: Sequences, k_seqs: Sequences, q, k, v, out, lse=None, key_bias=None, scale=None,
+                  workspace=None, stream=None):
+    """Enqueue attention of each sequence's queries over its keys (scale: 1 / sqrt(head_dim)
+    by default).  ``lse`` (heads, rows) fp32 is wanted by the backward."""
+    import torch
+    ref, D, dev = ctypes.byref, q.shape[-1], q.device
+    sq, sk = _heads(q, "q", q_seqs, D, q), _heads(k, "k", k_seqs, D, q)
+    need = load_library().tdp_attention_workspace(ref(q_seqs.c), ref(k_seqs.c), sq.heads, sk.heads, D)
+    _check(load_library().tdp_attention(
+        ref(q_seqs.c), ref(k_seqs.c), ref(sq), ref(sk), ref(_heads(v, "v", k_seqs, D, q)),
+        _vec(key_bias, "key_bias", torch.float32, k_seqs.total_rows, dev),
+        ref(_heads(out, "out", q_seqs, D, q, True)),
+        _vec(lse, "lse", torch.float32, sq.heads * q_seqs.total_rows, dev), D ** -0.5 if scale is None else scale, D,
+        _dtype_code(q, "q"), _ptr(workspace, "workspace", torch.uint8, need, dev) if need else ctypes.c_void_p(None),
+        _stream_handle(stream, dev)))
+
+
+def tdp_attention_backward(q_seqs: Sequences, k_seqs: Sequences, q, k, v, out, lse, dout, dq, dk, dv, workspace,
+                           key_bias=None, scale=None, stream=None):
+    """Enqueue the gradients of tdp_attention; ``out`` and ``lse`` are its results."""
+    import torch
+    ref, D, dev = ctypes.byref, q.shape[-1], q.device
+    sq, sk = _heads(q, "q", q_seqs, D, q), _heads(k, "k", k_seqs, D, q)
+    need = load_library().tdp_attention_backward_workspace(ref(q_seqs.c), ref(k_seqs.c), sq.heads, sk.heads, D)
+    _check(load_library().tdp_attention_backward(
+        ref(q_seqs.c), ref(k_seqs.c), ref(sq), ref(sk), ref(_heads(v, "v", k_seqs, D, q)),
+        _vec(key_bias, "key_bias", torch.float32, k_seqs.total_rows, dev), ref(_heads(out, "out", q_seqs, D, q)),
+        _ptr(lse, "lse", torch.float32, sq.heads * q_seqs.total_rows, dev),
+        ref(_heads(dout, "dout", q_seqs, D, q)), ref(_heads(dq, "dq", q_seqs, D, q, True)),
+        ref(_heads(dk, "dk", k_seqs, D, q, True)), ref(_heads(dv, "dv", k_seqs, D, q, True)),
+        D ** -0.5 if scale is None else scale, D, _dtype_code(q, "q"),
+        _ptr(workspace, "workspace", torch.uint8, need, dev), _stream_handle(stream, dev)))

@@ -9,7 +9,7 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 LIB = os.path.join(HERE, "libtdp.so")
 SOURCES = [os.path.join(HERE, "csrc", n) for n in (
-    "plan.cpp", "quality.cpp", "pixel_plan.cpp", "kernels.hip", "pixel.hip")]
+    "plan.cpp", "quality.cpp", "pixel_plan.cpp", "tokens.cpp", "kernels.hip", "pixel.hip", "rope.hip", "attention.hip")]
 # memory-system ceilings for the measurement script (not the hot path)
 CEILING_LIB = os.path.join(HERE, "libtdp_ceiling.so")
 CEILING_SOURCES = [os.path.join(HERE, "csrc", "ceiling.hip")]
@@ -17,7 +17,8 @@ CEILING_SOURCES = [os.path.join(HERE, "csrc", "ceiling.hip")]
 # the host planner alone, built with a host compiler under address and
 # undefined-behaviour sanitizers (CPU tests only; no device entry points)
 HOST_SAN_LIB = os.path.join(HERE, "libtdp_host_san.so")
-HOST_SAN_SOURCES = [os.path.join(HERE, "csrc", n) for n in ("plan.cpp", "quality.cpp", "pixel_plan.cpp")]
+HOST_SAN_SOURCES = [os.path.join(HERE, "csrc", n) for n in ("plan.cpp", "quality.cpp", "pixel_plan.cpp",
+                                                              "tokens.cpp")]
 HOST_SAN_FLAGS = ["-std=c++17", "-O1", "-g", "-fno-omit-frame-pointer", "-fsanitize=address,undefined",
                   "-fno-sanitize-recover=all", "-fPIC", "-shared", "-Wall", "-I" + os.path.join(ROOT, "include")]
 

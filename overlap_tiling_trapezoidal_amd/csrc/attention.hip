@@ -1,0 +1,832 @@
+// Attention of a tile's rows and its gradients (gfx950 matrix instructions).
+//
+//   s_ij = scale * q_i . k_j + bias_j,  p_ij = exp(s_ij - lse_i),
+//   o_i = sum_j p_ij v_j
+//   delta_i = do_i . o_i,  ds_ij = p_ij (do_i . v_j - delta_i)
+//   dq_i = scale sum_j ds_ij k_j,  dk_j = scale sum_i ds_ij q_i,  dv_j = sum_i p_ij do_i
+//
+// The scores are never stored: the forward keeps a running maximum and sum
+// per query while it walks the keys, the backward computes them again from
+// lse.  All products run as 32 x 32 tiles of the matrix instructions with
+// fp32 accumulators.
+//
+// Layouts.  A product C = A B of 32 x 32 with a contraction of 16 takes from
+// lane l (h = l / 32) the elements A[l % 32][8h .. 8h+7] and B[8h .. 8h+7][l % 32]
+// and leaves C[8 (r / 4) + 4h + r % 4][l % 32] in its register r.  The score
+// tile is computed so that the axis the next product keeps lies on the
+// columns (keys x queries for o and dq, queries x keys for dk and dv): each
+// lane then holds one column, the softmax needs one exchange between the two
+// halves of the wave, and registers 8s .. 8s+7 are, as they stand, the B
+// operand of the next product's step s with its contraction in the order
+//   16s + {4h, .., 4h+3, 8+4h, .., 8+4h+3}.
+// The A operand of that product is read in the same order, down the columns
+// of the LDS tile (bf16: the transposing 64-bit LDS read, four rows of 16
+// columns per 16 lanes).
+//
+// fp32 tensors run the same code on fp32 matrix instructions, eight
+// contractions of 2 for one of 16.
+#include <hip/hip_runtime.h>
+#include <math.h>
+#include <stdint.h>
+
+#include "token_device.h"
+
+namespace tdp {
+namespace {
+
+constexpr int kTok = 256;
+constexpr float kLog2e = 1.4426950408889634f;
+// A bias at or below this (-infinity, the lowest values of fp32 and bf16) takes
+// the key out.
+constexpr float kBiasOut = -1.0e30f;
+// The running maximum is moved only when a block exceeds it by this many
+// powers of two: weights stay below 2^8, where fp32 sums and bf16 weights lose
+// nothing, and most blocks skip the rescaling of the sums.
+constexpr float kSlack = 8.0f;
+
+typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef float f32x8 __attribute__((ext_vector_type(8)));
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+#define TDP_LDS __attribute__((address_space(3)))
+
+template <int T>
+struct Mat;
+template <>
+struct Mat<TDP_BF16> {
+  typedef bf16x8 Frag;
+  static constexpr int kBytes = 2;
+  __device__ static inline f32x16 mma(const Frag& a, const Frag& b, const f32x16& c) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
+  }
+  __device__ static inline Frag pack(const float* x) {
+    return __builtin_convertvector(f32x8{x[0], x[1], x[2], x[3], x[4], x[5], x[6], x[7]}, bf16x8);
+  }
+};
+template <>
+struct Mat<TDP_F32> {
+  typedef f32x8 Frag;
+  static constexpr int kBytes = 4;
+  __device__ static inline f32x16 mma(const Frag& a, const Frag& b, f32x16 c) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) c = __builtin_amdgcn_mfma_f32_32x32x2f32(a[e], b[e], c, 0, 0, 0);
+    return c;
+  }
+  __device__ static inline Frag pack(const float* x) { return f32x8{x[0], x[1], x[2], x[3], x[4], x[5], x[6], x[7]}; }
+};
+
+// A tile of rows in LDS: DP elements per row in 16-byte chunks, chunk c of row
+// r at c ^ swizzle(r), so that neither 16-byte reads of one column chunk over
+// eight rows nor the transposing reads of four rows meet in a bank.
+template <int T, int DP>
+struct Tile {
+  typedef typename Mat<T>::Frag Frag;
+  static constexpr int kRow = DP * Mat<T>::kBytes;  // bytes
+  static constexpr int kChunks = kRow / 16;
+  __device__ static inline int at(int r, int c) {
+    const int sw = kChunks == 8 ? ((r >> 1) & 3) << 1 : (r & 7) << 1;
+    return r * kRow + ((c ^ sw) << 4);
+  }
+  // A[r][16 kk + 8h .. +7]
+  __device__ static inline Frag row_frag(const char* lds, int r, int kk, int h) {
+    if constexpr (T == TDP_BF16) {
+      return *reinterpret_cast<const bf16x8*>(lds + at(r, 2 * kk + h));
+    } else {
+      const f32x4 a = *reinterpret_cast<const f32x4*>(lds + at(r, 4 * kk + 2 * h));
+      const f32x4 b = *reinterpret_cast<const f32x4*>(lds + at(r, 4 * kk + 2 * h + 1));
+      return f32x8{a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
+    }
+  }
+  // rows r0 + {4h .. 4h+3, 8+4h .. 8+4h+3} of column c0 + l % 32
+  __device__ static inline Frag col_frag(char* lds, int r0, int c0, int lane) {
+    const int h = lane >> 5;
+    if constexpr (T == TDP_BF16) {
+      const int r = r0 + 4 * h + ((lane & 15) >> 2);
+      const int c = c0 + (lane & 16) + 4 * (lane & 3);
+      const int off = (c & 7) * 2;
+      typedef TDP_LDS bf16x4* P;
+      const bf16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4bf16((P)(TDP_LDS char*)(lds + at(r, c >> 3) + off));
+      const bf16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4bf16((P)(TDP_LDS char*)(lds + at(r + 8, c >> 3) + off));
+      return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
+    } else {
+      const int c = c0 + (lane & 31);
+      f32x8 v;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const int r = r0 + 4 * h + (e & 3) + 8 * (e >> 2);
+        v[e] = *reinterpret_cast<const float*>(lds + at(r, c >> 2) + (c & 3) * 4);
+      }
+      return v;
+    }
+  }
+};
+
+struct AttnArgs {
+  SeqsDev qs, ks;
+  HeadsDev q, k, v, o, dout, dq, dk, dv;
+  const float* bias;
+  float* lse;
+  float* delta;
+  float* ws;
+  float scale;
+  int32_t D, group, splits, m_max;  // m_max: query entries of the longest sequence
+  FastDiv by_group;
+  uint32_t blocks, tiles;  // row blocks per (sequence, key head); all work items
+};
+
+// Workgroups are dealt round-robin to the eight XCDs; each gets a contiguous
+// range of the work items, which are ordered so that neighbours walk the same
+// keys, and these then stay in that XCD's L2.
+__device__ inline uint32_t xcd_item(uint32_t tiles) {
+  const uint32_t per = (tiles + 7) / 8;
+  return (blockIdx.x & 7) * per + (blockIdx.x >> 3);
+}
+inline uint32_t xcd_grid(uint32_t tiles) { return (tiles + 7) / 8 * 8; }
+
+__device__ inline float other_half_max(float x) {
+  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
+__device__ inline float other_half_sum(float x) {
+  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+}
+
+// Rows [r0, r0 + ROWS) of a tensor through registers into LDS; rows at and past
+// `len`, and chunks past head_dim, are zero.
+template <int T, int DP, int ROWS>
+struct Stage {
+  typedef Tile<T, DP> L;
+  static constexpr int N = ROWS * L::kChunks / kTok;
+  u32x4 v[N];
+  // keys and values: base points at row 0 of the head
+  __device__ inline void load_rows(const char* base, int64_t row_bytes, int r0, int len, int d_bytes,
+                                   const float* bias) {
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+      const int i = threadIdx.x + n * kTok, r = r0 + i / L::kChunks, c = i % L::kChunks;
+      v[n] = u32x4{0, 0, 0, 0};
+      if (r < len && c * 16 < d_bytes && !(bias && bias[r] <= kBiasOut))
+        v[n] = *reinterpret_cast<const u32x4*>(base + r * row_bytes + c * 16);
+    }
+  }
+  // query entries m: row m / group, head m % group
+  __device__ inline void load_entries(const char* base, int64_t row_bytes, int64_t head_bytes, const AttnArgs& A,
+                                      int m0, int len, int d_bytes) {
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+      const int i = threadIdx.x + n * kTok, m = m0 + i / L::kChunks, c = i % L::kChunks;
+      v[n] = u32x4{0, 0, 0, 0};
+      if (m < len && c * 16 < d_bytes) {
+        const int row = (int)fastdiv((uint32_t)m, A.by_group);
+        v[n] = *reinterpret_cast<const u32x4*>(base + row * row_bytes + (m - row * A.group) * head_bytes + c * 16);
+      }
+    }
+  }
+  __device__ inline void put(char* lds) const {
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+      const int i = threadIdx.x + n * kTok;
+      *reinterpret_cast<u32x4*>(lds + L::at(i / L::kChunks, i % L::kChunks)) = v[n];
+    }
+  }
+};
+
+// The B operand of a product over head_dim, from global memory: element
+// 16 kk + 8h + e of the lane's row (null: zero).
+template <int T, int DP>
+__device__ inline void load_frags(const char* row, int h, int D, typename Mat<T>::Frag* f) {
+#pragma unroll
+  for (int kk = 0; kk < DP / 16; ++kk) {
+    const int d = 16 * kk + 8 * h;
+    float x[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+    if constexpr (T == TDP_BF16) {
+      u32x4 v = {0, 0, 0, 0};
+      if (row && d < D) v = *reinterpret_cast<const u32x4*>(row + 2 * d);
+      f[kk] = __builtin_bit_cast(bf16x8, v);
+    } else {
+      if (row && d < D) load8<TDP_F32>(row, d, x);
+      f[kk] = Mat<T>::pack(x);
+    }
+  }
+}
+
+// One lane's column of an accumulator (rows = head_dim) times `f`, as the output dtype.
+template <int T, int ND>
+__device__ inline void store_column(char* row, int h, int D, const f32x16* acc, float f) {
+#pragma unroll
+  for (int nd = 0; nd < ND; ++nd)
+#pragma unroll
+    for (int r4 = 0; r4 < 4; ++r4) {
+      const int d = nd * 32 + r4 * 8 + h * 4;
+      if (d >= D) continue;
+      float x[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) x[e] = acc[nd][r4 * 4 + e] * f;
+      if constexpr (T == TDP_BF16) {
+        uint2 v;
+        v.x = pack_bf16x2(x[0], x[1]);
+        v.y = pack_bf16x2(x[2], x[3]);
+        *reinterpret_cast<uint2*>(row + 2 * d) = v;
+      } else {
+        *reinterpret_cast<f32x4*>(row + 4 * d) = f32x4{x[0], x[1], x[2], x[3]};
+      }
+    }
+}
+
+__device__ inline f32x16 zero16() {
+  f32x16 z;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) z[i] = 0.0f;
+  return z;
+}
+
+// A work item's place: sequence, key head, block of query entries or keys, split.
+struct Place {
+  int s, hk, blk, split;
+};
+__device__ inline Place place(const AttnArgs& A, uint32_t item) {
+  Place p;
+  const uint32_t sh = item / (A.blocks * A.splits), rest = item - sh * (A.blocks * A.splits);
+  p.split = rest / A.blocks;
+  p.blk = rest - p.split * A.blocks;
+  p.s = sh / A.k.heads;
+  p.hk = sh - p.s * A.k.heads;
+  return p;
+}
+
+// Forward: 128 query entries of one key head per workgroup, 32 per wave; K and
+// V blocks of 64 keys pass through LDS.
+template <int T, int DP, bool BIAS>
+__global__ __launch_bounds__(kTok, T == TDP_BF16 ? 2 : 1) void attn_forward_kernel(const AttnArgs A) {
+  typedef Tile<T, DP> L;
+  typedef typename Mat<T>::Frag Frag;
+  constexpr int KD = DP / 16, ND = DP / 32, KT = kAttnBlockK / 32;
+  __shared__ __align__(16) char kl[kAttnBlockK * L::kRow];
+  __shared__ __align__(16) char vl[kAttnBlockK * L::kRow];
+  __shared__ __align__(16) float bl[BIAS ? kAttnBlockK : 4];
+  const uint32_t item = xcd_item(A.tiles);
+  if (item >= A.tiles) return;
+  const Place pl = place(A, item);
+  const SeqRows qr = seq_rows(A.qs, pl.s), kr = seq_rows(A.ks, pl.s);
+  const int M = qr.cap * A.group, mlen = qr.len * A.group;
+  const int m0 = pl.blk * kAttnBlockQ;
+  if (m0 >= M) return;
+  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, h = lane >> 5;
+  const int m = m0 + wave * 32 + (lane & 31);
+  const int row = (int)fastdiv((uint32_t)m, A.by_group), head = pl.hk * A.group + (m - row * A.group);
+  constexpr int eb = Mat<T>::kBytes;
+
+  Frag qf[KD];
+  load_frags<T, DP>(m < mlen ? A.q.data + eb * (seq_base(A.qs, A.q, pl.s, qr) + row * A.q.row_stride +
+                                               head * A.q.head_stride)
+                             : nullptr,
+                    h, A.D, qf);
+  f32x16 o[ND];
+#pragma unroll
+  for (int nd = 0; nd < ND; ++nd) o[nd] = zero16();
+  float mx = -INFINITY, l = 0.0f;
+  const float c = BIAS ? kLog2e : A.scale * kLog2e;
+
+  const char* kb = A.k.data + eb * (seq_base(A.ks, A.k, pl.s, kr) + pl.hk * A.k.head_stride);
+  const char* vb = A.v.data + eb * (seq_base(A.ks, A.v, pl.s, kr) + pl.hk * A.v.head_stride);
+  const int64_t krow = eb * A.k.row_stride, vrow = eb * A.v.row_stride;
+  const float* bias = BIAS ? A.bias + kr.row0 : nullptr;
+  const int nb = (kr.len + kAttnBlockK - 1) / kAttnBlockK;
+  const int per = (nb + A.splits - 1) / A.splits;
+  const int b0 = pl.split * per;
+  int b1 = b0 + per < nb ? b0 + per : nb;
+  if (m0 >= mlen) b1 = b0;
+
+  Stage<T, DP, kAttnBlockK> ks, vs;
+  float bs = 0.0f;
+  auto fetch = [&](int b) {
+    ks.load_rows(kb, krow, b * kAttnBlockK, kr.len, A.D * eb, bias);
+    vs.load_rows(vb, vrow, b * kAttnBlockK, kr.len, A.D * eb, bias);
+    if constexpr (BIAS) {
+      const int j = b * kAttnBlockK + (int)threadIdx.x;
+      if (threadIdx.x < kAttnBlockK) {
+        bs = j < kr.len ? bias[j] : -INFINITY;
+        bs = bs <= kBiasOut ? -INFINITY : bs;
+      }
+    }
+  };
+  if (b0 < b1) fetch(b0);
+  for (int b = b0; b < b1; ++b) {
+    __syncthreads();
+    ks.put(kl);
+    vs.put(vl);
+    if (BIAS && threadIdx.x < kAttnBlockK) bl[threadIdx.x] = bs;
+    __syncthreads();
+    if (b + 1 < b1) fetch(b + 1);
+
+    f32x16 st[KT];
+#pragma unroll
+    for (int kt = 0; kt < KT; ++kt) {
+      st[kt] = zero16();
+#pragma unroll
+      for (int kk = 0; kk < KD; ++kk)
+        st[kt] = Mat<T>::mma(L::row_frag(kl, kt * 32 + (lane & 31), kk, h), qf[kk], st[kt]);
+    }
+    if constexpr (BIAS) {
+#pragma unroll
+      for (int kt = 0; kt < KT; ++kt)
+#pragma unroll
+        for (int r = 0; r < 16; ++r)
+          st[kt][r] = fmaf(st[kt][r], A.scale, bl[kt * 32 + 8 * (r >> 2) + 4 * h + (r & 3)]);
+    } else if ((b + 1) * kAttnBlockK > kr.len) {
+#pragma unroll
+      for (int kt = 0; kt < KT; ++kt)
+#pragma unroll
+        for (int r = 0; r < 16; ++r)
+          if (b * kAttnBlockK + kt * 32 + 8 * (r >> 2) + 4 * h + (r & 3) >= kr.len) st[kt][r] = -INFINITY;
+    }
+    float bm = -INFINITY;
+#pragma unroll
+    for (int kt = 0; kt < KT; ++kt)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) bm = fmaxf(bm, st[kt][r]);
+    bm = other_half_max(bm);
+    if (__any((bm - mx) * c > kSlack)) {
+      const float nm = fmaxf(mx, bm);
+      const float f = mx == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f((mx - nm) * c);
+      mx = nm;
+      l *= f;
+#pragma unroll
+      for (int nd = 0; nd < ND; ++nd) o[nd] *= f;
+    }
+    const float mu = mx == -INFINITY ? 0.0f : mx;
+    const float mc = mu * c;
+#pragma unroll
+    for (int kt = 0; kt < KT; ++kt) {
+      float p[16];
+#pragma unroll
+      for (int r = 0; r < 16; ++r) {
+        p[r] = __builtin_amdgcn_exp2f(BIAS ? (st[kt][r] - mu) * c : fmaf(st[kt][r], c, -mc));
+        l += p[r];
+      }
+#pragma unroll
+      for (int s = 0; s < 2; ++s) {
+        const Frag pf = Mat<T>::pack(p + 8 * s);
+#pragma unroll
+        for (int nd = 0; nd < ND; ++nd)
+          o[nd] = Mat<T>::mma(L::col_frag(vl, kt * 32 + 16 * s, nd * 32, lane), pf, o[nd]);
+      }
+    }
+  }
+  l = other_half_sum(l);
+  if (m >= M) return;
+  if (A.splits > 1) {
+    const int64_t e = (((int64_t)pl.split * A.qs.S + pl.s) * A.k.heads + pl.hk) * A.m_max + m;
+    const int64_t n = (int64_t)A.splits * A.qs.S * A.k.heads * A.m_max;
+    store_column<TDP_F32, ND>(reinterpret_cast<char*>(A.ws + e * DP), h, DP, o, 1.0f);
+    if (h == 0) *reinterpret_cast<f32x2*>(A.ws + n * DP + 2 * e) = f32x2{mx, l};
+    return;
+  }
+  const bool live = m < mlen;
+  char* op = A.o.data + eb * (seq_base(A.qs, A.o, pl.s, qr) + row * A.o.row_stride + head * A.o.head_stride);
+  if (!live || l == 0.0f) {
+#pragma unroll
+    for (int nd = 0; nd < ND; ++nd) o[nd] = zero16();
+  }
+  store_column<T, ND>(op, h, A.D, o, live && l != 0.0f ? 1.0f / l : 0.0f);
+  if (A.lse && h == 0)
+    A.lse[(int64_t)head * A.qs.total + qr.row0 + row] =
+        live && l != 0.0f ? mx * (BIAS ? 1.0f : A.scale) + logf(l) : -INFINITY;
+}
+
+// Join the splits of one query entry per wave: weights 2^(c (m_i - max)).
+template <int T, int DP>
+__global__ __launch_bounds__(kTok) void attn_join_kernel(const AttnArgs A, float c, float unit) {
+  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+  const int64_t g = (int64_t)blockIdx.x * 4 + wave;  // ((s, hk), m)
+  const int64_t n1 = (int64_t)A.qs.S * A.k.heads * A.m_max;
+  if (g >= n1) return;
+  const int64_t sh = g / A.m_max;
+  const int m = (int)(g - sh * A.m_max), s = (int)(sh / A.k.heads), hk = (int)(sh - (int64_t)s * A.k.heads);
+  const SeqRows qr = seq_rows(A.qs, s);
+  if (m >= qr.cap * A.group) return;
+  const f32x2* ml = reinterpret_cast<const f32x2*>(A.ws + n1 * A.splits * DP);
+  float mx = -INFINITY;
+  for (int i = 0; i < A.splits; ++i) mx = fmaxf(mx, ml[i * n1 + g].x);
+  float l = 0.0f, x[DP / 64];
+#pragma unroll
+  for (int e = 0; e < DP / 64; ++e) x[e] = 0.0f;
+  for (int i = 0; i < A.splits; ++i) {
+    const f32x2 v = ml[i * n1 + g];
+    if (v.y == 0.0f) continue;  // no key in this part
+    const float f = v.x == mx ? 1.0f : __builtin_amdgcn_exp2f((v.x - mx) * c);
+    l = fmaf(v.y, f, l);
+#pragma unroll
+    for (int e = 0; e < DP / 64; ++e) x[e] = fmaf(A.ws[(i * n1 + g) * DP + e * 64 + lane], f, x[e]);
+  }
+  const int row = (int)fastdiv((uint32_t)m, A.by_group), head = hk * A.group + (m - row * A.group);
+  const bool live = row < qr.len && l != 0.0f;
+  char* op = A.o.data + Mat<T>::kBytes * (seq_base(A.qs, A.o, s, qr) + row * A.o.row_stride + head * A.o.head_stride);
+#pragma unroll
+  for (int e = 0; e < DP / 64; ++e) {
+    const int d = e * 64 + lane;
+    if (d >= A.D) continue;
+    const float y = live ? x[e] / l : 0.0f;
+    if constexpr (T == TDP_BF16)
+      reinterpret_cast<__bf16*>(op)[d] = (__bf16)y;
+    else
+      reinterpret_cast<float*>(op)[d] = y;
+  }
+  if (A.lse && lane == 0)
+    A.lse[(int64_t)head * A.qs.total + qr.row0 + row] = live ? mx * unit + logf(l) : -INFINITY;
+}
+
+// delta = dout . out per query head and row: 16 lanes per head, a wave per row.
+template <int T>
+__global__ __launch_bounds__(kTok) void attn_delta_kernel(const AttnArgs A, uint32_t blocks) {
+  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+  const int s = blockIdx.x / blocks;
+  const int i = (blockIdx.x - s * blocks) * 4 + wave;
+  const SeqRows qr = seq_rows(A.qs, s);
+  if (i >= qr.len) return;
+  const int chunk = lane & 15;
+  const int64_t gb = seq_base(A.qs, A.dout, s, qr) + i * A.dout.row_stride + chunk * 8;
+  const int64_t ob = seq_base(A.qs, A.o, s, qr) + i * A.o.row_stride + chunk * 8;
+  for (int hd = lane >> 4; hd < A.q.heads; hd += 4) {
+    float v = 0.0f;
+    if (chunk * 8 < A.D) {
+      float a[8], b[8];
+      load8<T>(A.dout.data, gb + hd * A.dout.head_stride, a);
+      load8<T>(A.o.data, ob + hd * A.o.head_stride, b);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v = fmaf(a[e], b[e], v);
+    }
+#pragma unroll
+    for (int x = 1; x < 16; x <<= 1) v += __shfl_xor(v, x);
+    if (chunk == 0) A.delta[(int64_t)hd * A.qs.total + qr.row0 + i] = v;
+  }
+}
+
+// A weight again from its score: exp(s - lse).  `nl` is -lse in the exponent's
+// unit (log2 without a bias, natural with one); -infinity for rows without keys.
+template <bool BIAS>
+__device__ inline float weight(float s, float scale, float c, float bias, float nl) {
+  if constexpr (BIAS) return __builtin_amdgcn_exp2f((fmaf(s, scale, bias) + nl) * kLog2e);
+  return __builtin_amdgcn_exp2f(fmaf(s, c, nl));
+}
+template <bool BIAS>
+__device__ inline float neg_lse(float lse) {
+  return lse == -INFINITY ? -INFINITY : (BIAS ? -lse : -lse * kLog2e);
+}
+
+// dq: the forward's walk over the keys with a third product.
+template <int T, int DP, bool BIAS>
+__global__ __launch_bounds__(kTok, T == TDP_BF16 && !(BIAS && DP == 128) ? 2 : 1) void attn_dq_kernel(const AttnArgs A) {
+  typedef Tile<T, DP> L;
+  typedef typename Mat<T>::Frag Frag;
+  constexpr int KD = DP / 16, ND = DP / 32, KT = kAttnBlockK / 32;
+  __shared__ __align__(16) char kl[kAttnBlockK * L::kRow];
+  __shared__ __align__(16) char vl[kAttnBlockK * L::kRow];
+  __shared__ __align__(16) float bl[BIAS ? kAttnBlockK : 4];
+  const uint32_t item = xcd_item(A.tiles);
+  if (item >= A.tiles) return;
+  const Place pl = place(A, item);
+  const SeqRows qr = seq_rows(A.qs, pl.s), kr = seq_rows(A.ks, pl.s);
+  const int M = qr.cap * A.group, mlen = qr.len * A.group;
+  const int m0 = pl.blk * kAttnBlockQ;
+  if (m0 >= M) return;
+  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, h = lane >> 5;
+  const int m = m0 + wave * 32 + (lane & 31);
+  const bool live = m < mlen;
+  const int row = (int)fastdiv((uint32_t)m, A.by_group), head = pl.hk * A.group + (m - row * A.group);
+  constexpr int eb = Mat<T>::kBytes;
+
+  Frag qf[KD], gf[KD];
+  load_frags<T, DP>(live ? A.q.data + eb * (seq_base(A.qs, A.q, pl.s, qr) + row * A.q.row_stride +
+                                            head * A.q.head_stride) : nullptr, h, A.D, qf);
+  load_frags<T, DP>(live ? A.dout.data + eb * (seq_base(A.qs, A.dout, pl.s, qr) + row * A.dout.row_stride +
+                                               head * A.dout.head_stride) : nullptr, h, A.D, gf);
+  const int64_t stat = (int64_t)head * A.qs.total + qr.row0 + row;
+  const float nl = live ? neg_lse<BIAS>(A.lse[stat]) : -INFINITY;
+  const float delta = live ? A.delta[stat] : 0.0f;
+  const float c = A.scale * kLog2e;
+  f32x16 dq[ND];
+#pragma unroll
+  for (int nd = 0; nd < ND; ++nd) dq[nd] = zero16();
+
+  const char* kb = A.k.data + eb * (seq_base(A.ks, A.k, pl.s, kr) + pl.hk * A.k.head_stride);
+  const char* vb = A.v.data + eb * (seq_base(A.ks, A.v, pl.s, kr) + pl.hk * A.v.head_stride);
+  const int64_t krow = eb * A.k.row_stride, vrow = eb * A.v.row_stride;
+  const float* bias = BIAS ? A.bias + kr.row0 : nullptr;
+  const int nb = m0 >= mlen ? 0 : (kr.len + kAttnBlockK - 1) / kAttnBlockK;
+
+  Stage<T, DP, kAttnBlockK> ks, vs;
+  float bs = 0.0f;
+  auto fetch = [&](int b) {
+    ks.load_rows(kb, krow, b * kAttnBlockK, kr.len, A.D * eb, bias);
+    vs.load_rows(vb, vrow, b * kAttnBlockK, kr.len, A.D * eb, bias);
+    if constexpr (BIAS) {
+      const int j = b * kAttnBlockK + (int)threadIdx.x;
+      if (threadIdx.x < kAttnBlockK) {
+        bs = j < kr.len ? bias[j] : -INFINITY;
+        bs = bs <= kBiasOut ? -INFINITY : bs;
+      }
+    }
+  };
+  if (nb) fetch(0);
+  for (int b = 0; b < nb; ++b) {
+    __syncthreads();
+    ks.put(kl);
+    vs.put(vl);
+    if (BIAS && threadIdx.x < kAttnBlockK) bl[threadIdx.x] = bs;
+    __syncthreads();
+    if (b + 1 < nb) fetch(b + 1);
+#pragma unroll
+    for (int kt = 0; kt < KT; ++kt) {
+      f32x16 st = zero16(), dp = zero16();
+#pragma unroll
+      for (int kk = 0; kk < KD; ++kk) {
+        st = Mat<T>::mma(L::row_frag(kl, kt * 32 + (lane & 31), kk, h), qf[kk], st);
+        dp = Mat<T>::mma(L::row_frag(vl, kt * 32 + (lane & 31), kk, h), gf[kk], dp);
+      }
+      float ds[16];
+#pragma unroll
+      for (int r = 0; r < 16; ++r) {
+        // keys past the end have zero rows in LDS: they add nothing to dq
+        const float bi = BIAS ? bl[kt * 32 + 8 * (r >> 2) + 4 * h + (r & 3)] : 0.0f;
+        ds[r] = weight<BIAS>(st[r], A.scale, c, bi, nl) * (dp[r] - delta);
+      }
+#pragma unroll
+      for (int s = 0; s < 2; ++s) {
+        const Frag f = Mat<T>::pack(ds + 8 * s);
+#pragma unroll
+        for (int nd = 0; nd < ND; ++nd)
+          dq[nd] = Mat<T>::mma(L::col_frag(kl, kt * 32 + 16 * s, nd * 32, lane), f, dq[nd]);
+      }
+    }
+  }
+  if (m >= M) return;
+  char* op = A.dq.data + eb * (seq_base(A.qs, A.dq, pl.s, qr) + row * A.dq.row_stride + head * A.dq.head_stride);
+  if (!live) {
+#pragma unroll
+    for (int nd = 0; nd < ND; ++nd) dq[nd] = zero16();
+  }
+  store_column<T, ND>(op, h, A.D, dq, A.scale);
+}
+
+// dk and dv: 128 keys of one key head per workgroup, 32 per wave, their K and V
+// in registers; blocks of 32 query entries (all heads of the group) pass
+// through LDS with their dout, lse and delta.
+constexpr int kBlockM = 32;
+template <int T, int DP, bool BIAS>
+__global__ __launch_bounds__(kTok, 1) void attn_dkv_kernel(const AttnArgs A) {
+  typedef Tile<T, DP> L;
+  typedef typename Mat<T>::Frag Frag;
+  constexpr int KD = DP / 16, ND = DP / 32;
+  __shared__ __align__(16) char ql[kBlockM * L::kRow];
+  __shared__ __align__(16) char gl[kBlockM * L::kRow];
+  __shared__ __align__(16) float nll[kBlockM], del[kBlockM];
+  const uint32_t item = xcd_item(A.tiles);
+  if (item >= A.tiles) return;
+  const Place pl = place(A, item);
+  const SeqRows qr = seq_rows(A.qs, pl.s), kr = seq_rows(A.ks, pl.s);
+  const int j0 = pl.blk * 128;
+  if (j0 >= kr.cap) return;
+  const int mlen = j0 < kr.len ? qr.len * A.group : 0;
+  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, h = lane >> 5;
+  const int j = j0 + wave * 32 + (lane & 31);
+  constexpr int eb = Mat<T>::kBytes;
+  float bi = 0.0f;
+  bool live = j < kr.len;
+  if constexpr (BIAS) {
+    bi = live ? A.bias[kr.row0 + j] : -INFINITY;
+    bi = bi <= kBiasOut ? -INFINITY : bi;
+    live = live && bi != -INFINITY;
+  }
+  Frag kf[KD], vf[KD];
+  load_frags<T, DP>(live ? A.k.data + eb * (seq_base(A.ks, A.k, pl.s, kr) + j * A.k.row_stride +
+                                            pl.hk * A.k.head_stride) : nullptr, h, A.D, kf);
+  load_frags<T, DP>(live ? A.v.data + eb * (seq_base(A.ks, A.v, pl.s, kr) + j * A.v.row_stride +
+                                            pl.hk * A.v.head_stride) : nullptr, h, A.D, vf);
+  f32x16 dk[ND], dv[ND];
+#pragma unroll
+  for (int nd = 0; nd < ND; ++nd) dk[nd] = dv[nd] = zero16();
+  const float c = A.scale * kLog2e;
+  const int64_t hq0 = (int64_t)pl.hk * A.group;
+  const char* qb = A.q.data + eb * (seq_base(A.qs, A.q, pl.s, qr) + hq0 * A.q.head_stride);
+  const char* gb = A.dout.data + eb * (seq_base(A.qs, A.dout, pl.s, qr) + hq0 * A.dout.head_stride);
+
+  Stage<T, DP, kBlockM> qs, gs;
+  float nls = 0.0f, des = 0.0f;
+  auto fetch = [&](int m0) {
+    qs.load_entries(qb, eb * A.q.row_stride, eb * A.q.head_stride, A, m0, mlen, A.D * eb);
+    gs.load_entries(gb, eb * A.dout.row_stride, eb * A.dout.head_stride, A, m0, mlen, A.D * eb);
+    if (threadIdx.x < kBlockM) {
+      const int m = m0 + (int)threadIdx.x;
+      nls = -INFINITY;
+      des = 0.0f;
+      if (m < mlen) {
+        const int row = (int)fastdiv((uint32_t)m, A.by_group);
+        const int64_t stat = (hq0 + m - row * A.group) * A.qs.total + qr.row0 + row;
+        nls = neg_lse<BIAS>(A.lse[stat]);
+        des = A.delta[stat];
+      }
+    }
+  };
+  if (mlen) fetch(0);
+  for (int m0 = 0; m0 < mlen; m0 += kBlockM) {
+    __syncthreads();
+    qs.put(ql);
+    gs.put(gl);
+    if (threadIdx.x < kBlockM) {
+      nll[threadIdx.x] = nls;
+      del[threadIdx.x] = des;
+    }
+    __syncthreads();
+    if (m0 + kBlockM < mlen) fetch(m0 + kBlockM);
+    f32x16 st = zero16(), dp = zero16();
+#pragma unroll
+    for (int kk = 0; kk < KD; ++kk) {
+      st = Mat<T>::mma(L::row_frag(ql, lane & 31, kk, h), kf[kk], st);
+      dp = Mat<T>::mma(L::row_frag(gl, lane & 31, kk, h), vf[kk], dp);
+    }
+    float p[16], ds[16];
+#pragma unroll
+    for (int r4 = 0; r4 < 4; ++r4) {
+      const f32x4 nl = *reinterpret_cast<const f32x4*>(nll + 8 * r4 + 4 * h);
+      const f32x4 de = *reinterpret_cast<const f32x4*>(del + 8 * r4 + 4 * h);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int r = 4 * r4 + e;
+        p[r] = weight<BIAS>(st[r], A.scale, c, bi, nl[e]);
+        ds[r] = p[r] * (dp[r] - de[e]);
+      }
+    }
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+      const Frag pf = Mat<T>::pack(p + 8 * s), df = Mat<T>::pack(ds + 8 * s);
+#pragma unroll
+      for (int nd = 0; nd < ND; ++nd) {
+        dv[nd] = Mat<T>::mma(L::col_frag(gl, 16 * s, nd * 32, lane), pf, dv[nd]);
+        dk[nd] = Mat<T>::mma(L::col_frag(ql, 16 * s, nd * 32, lane), df, dk[nd]);
+      }
+    }
+  }
+  if (j >= kr.cap) return;
+  if (!live) {
+#pragma unroll
+    for (int nd = 0; nd < ND; ++nd) dk[nd] = dv[nd] = zero16();
+  }
+  store_column<T, ND>(A.dk.data + eb * (seq_base(A.ks, A.dk, pl.s, kr) + j * A.dk.row_stride +
+                                        pl.hk * A.dk.head_stride), h, A.D, dk, A.scale);
+  store_column<T, ND>(A.dv.data + eb * (seq_base(A.ks, A.dv, pl.s, kr) + j * A.dv.row_stride +
+                                        pl.hk * A.dv.head_stride), h, A.D, dv, 1.0f);
+}
+
+template <int T, int DP, bool BIAS>
+void launch_forward(const AttnArgs& A, hipStream_t st) {
+  hipLaunchKernelGGL((attn_forward_kernel<T, DP, BIAS>), dim3(xcd_grid(A.tiles)), dim3(kTok), 0, st, A);
+  if (A.splits > 1) {
+    const int64_t n = (int64_t)A.qs.S * A.k.heads * A.m_max;
+    hipLaunchKernelGGL((attn_join_kernel<T, DP>), dim3((unsigned)((n + 3) / 4)), dim3(kTok), 0, st, A,
+                       BIAS ? kLog2e : A.scale * kLog2e, BIAS ? 1.0f : A.scale);
+  }
+}
+
+template <int T, int DP, bool BIAS>
+void launch_backward(AttnArgs A, uint32_t q_rows, uint32_t k_rows, hipStream_t st) {
+  const uint32_t db = (q_rows + 3) / 4;
+  hipLaunchKernelGGL((attn_delta_kernel<T>), dim3(A.qs.S * db), dim3(kTok), 0, st, A, db);
+  hipLaunchKernelGGL((attn_dq_kernel<T, DP, BIAS>), dim3(xcd_grid(A.tiles)), dim3(kTok), 0, st, A);
+  A.blocks = (k_rows + 127) / 128;
+  A.tiles = A.blocks * (uint32_t)A.ks.S * (uint32_t)A.k.heads;
+  hipLaunchKernelGGL((attn_dkv_kernel<T, DP, BIAS>), dim3(xcd_grid(A.tiles)), dim3(kTok), 0, st, A);
+}
+
+// Checks shared by both calls.
+int begin(const char* fn, const tdp_seqs* q_seqs, const tdp_seqs* k_seqs, const tdp_heads* q, const tdp_heads* k,
+          const tdp_heads* v, const float* bias, const tdp_heads* out, const float* lse, float scale,
+          int32_t head_dim, int32_t dtype, AttnArgs* A) {
+  if (!dtype_bytes(dtype)) return fail(TDP_EINVAL, "%s: dtype must be TDP_F32 or TDP_BF16 (got %d)", fn, dtype);
+  if (head_dim < 8 || head_dim % 8 != 0 || head_dim > TDP_MAX_ATTENTION_DIM)
+    return fail(TDP_ESHAPE, "%s: head_dim must be a multiple of 8 in [8, %d] (got %d)", fn, TDP_MAX_ATTENTION_DIM,
+                head_dim);
+  if (!(scale > 0.0f) || scale > 3.0e38f) return fail(TDP_EINVAL, "%s: scale must be finite and > 0", fn);
+  int st = check_seqs(fn, "q_seqs", q_seqs, &A->qs);
+  if (st == TDP_OK) st = check_seqs(fn, "k_seqs", k_seqs, &A->ks);
+  if (st != TDP_OK) return st;
+  if (q_seqs->num_seqs != k_seqs->num_seqs)
+    return fail(TDP_EINVAL, "%s: %d query sequences meet %d key sequences", fn, q_seqs->num_seqs, k_seqs->num_seqs);
+  st = check_heads(fn, "q", q, q_seqs, head_dim, dtype, &A->q);
+  if (st == TDP_OK) st = check_heads(fn, "k", k, k_seqs, head_dim, dtype, &A->k);
+  if (st == TDP_OK) st = check_heads(fn, "v", v, k_seqs, head_dim, dtype, &A->v);
+  if (st == TDP_OK) st = check_heads(fn, "out", out, q_seqs, head_dim, dtype, &A->o);
+  if (st != TDP_OK) return st;
+  if (k->heads != v->heads || q->heads != out->heads || q->heads % k->heads != 0)
+    return fail(TDP_EINVAL, "%s: out needs q's heads, v k's, and q's must be a multiple of k's (q %d, k %d, v %d, out %d)",
+                fn, q->heads, k->heads, v->heads, out->heads);
+  if ((reinterpret_cast<uintptr_t>(bias) | reinterpret_cast<uintptr_t>(lse)) & 3)
+    return fail(TDP_EINVAL, "%s: key_bias and lse must be 4-byte aligned", fn);
+  A->bias = bias;
+  A->lse = const_cast<float*>(lse);
+  A->scale = scale;
+  A->D = head_dim;
+  A->group = q->heads / k->heads;
+  A->by_group = make_fastdiv((uint32_t)A->group);
+  const int64_t m = (int64_t)q_seqs->max_rows * A->group;
+  if (m > (1 << 30)) return fail(TDP_ESHAPE, "%s: %lld rows times heads of one key head exceed 2^30", fn, (long long)m);
+  A->m_max = (int32_t)m;
+  A->blocks = (uint32_t)((m + kAttnBlockQ - 1) / kAttnBlockQ);
+  A->splits = 1;
+  return TDP_OK;
+}
+
+int check_items(const char* fn, int64_t workgroups) {
+  if (workgroups * kTok > 0xffffffffLL - 8 * kTok)
+    return fail(TDP_ESHAPE, "%s: %lld workgroups, more work-items than one HIP launch holds", fn, (long long)workgroups);
+  return TDP_OK;
+}
+
+}  // namespace
+}  // namespace tdp
+
+using namespace tdp;
+
+#define TDP_ATTN_DISPATCH(call)                                     \
+  do {                                                              \
+    if (dtype == TDP_BF16) {                                        \
+      if (head_dim <= 64) {                                         \
+        if (key_bias) call(TDP_BF16, 64, true);                     \
+        else call(TDP_BF16, 64, false);                             \
+      } else {                                                      \
+        if (key_bias) call(TDP_BF16, 128, true);                    \
+        else call(TDP_BF16, 128, false);                            \
+      }                                                             \
+    } else {                                                        \
+      if (head_dim <= 64) {                                         \
+        if (key_bias) call(TDP_F32, 64, true);                      \
+        else call(TDP_F32, 64, false);                              \
+      } else {                                                      \
+        if (key_bias) call(TDP_F32, 128, true);                     \
+        else call(TDP_F32, 128, false);                             \
+      }                                                             \
+    }                                                               \
+  } while (0)
+
+extern "C" {
+
+int tdp_attention(const tdp_seqs* q_seqs, const tdp_seqs* k_seqs, const tdp_heads* q, const tdp_heads* k,
+                  const tdp_heads* v, const float* key_bias, const tdp_heads* out, float* lse, float scale,
+                  int32_t head_dim, int32_t dtype, void* workspace, void* stream) {
+  const char* fn = "tdp_attention";
+  AttnArgs A = {};
+  int st = begin(fn, q_seqs, k_seqs, q, k, v, key_bias, out, lse, scale, head_dim, dtype, &A);
+  if (st != TDP_OK) return st;
+  A.splits = attention_splits(*q_seqs, *k_seqs, q->heads, k->heads);
+  if (A.splits > 1 && (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 15)))
+    return fail(TDP_EINVAL, "%s: workspace must be a 16-byte aligned device pointer (tdp_attention_workspace)", fn);
+  A.ws = static_cast<float*>(workspace);
+  const int64_t tiles = (int64_t)A.blocks * q_seqs->num_seqs * k->heads * A.splits;
+  const int64_t join = A.splits > 1 ? ((int64_t)q_seqs->num_seqs * k->heads * A.m_max + 3) / 4 : 0;
+  st = check_items(fn, tiles > join ? tiles : join);
+  if (st != TDP_OK) return st;
+  A.tiles = (uint32_t)tiles;
+  hipStream_t hs = reinterpret_cast<hipStream_t>(stream);
+#define CALL(T, DP, B) launch_forward<T, DP, B>(A, hs)
+  TDP_ATTN_DISPATCH(CALL);
+#undef CALL
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return fail(TDP_EHIP, "%s: kernel launch failed: %s", fn, hipGetErrorString(e));
+  return TDP_OK;
+}
+
+int tdp_attention_backward(const tdp_seqs* q_seqs, const tdp_seqs* k_seqs, const tdp_heads* q, const tdp_heads* k,
+                           const tdp_heads* v, const float* key_bias, const tdp_heads* out, const float* lse,
+                           const tdp_heads* dout, const tdp_heads* dq, const tdp_heads* dk, const tdp_heads* dv,
+                           float scale, int32_t head_dim, int32_t dtype, void* workspace, void* stream) {
+  const char* fn = "tdp_attention_backward";
+  AttnArgs A = {};
+  int st = begin(fn, q_seqs, k_seqs, q, k, v, key_bias, out, lse, scale, head_dim, dtype, &A);
+  if (st == TDP_OK) st = check_heads(fn, "dout", dout, q_seqs, head_dim, dtype, &A.dout);
+  if (st == TDP_OK) st = check_heads(fn, "dq", dq, q_seqs, head_dim, dtype, &A.dq);
+  if (st == TDP_OK) st = check_heads(fn, "dk", dk, k_seqs, head_dim, dtype, &A.dk);
+  if (st == TDP_OK) st = check_heads(fn, "dv", dv, k_seqs, head_dim, dtype, &A.dv);
+  if (st != TDP_OK) return st;
+  if (dout->heads != q->heads || dq->heads != q->heads || dk->heads != k->heads || dv->heads != k->heads)
+    return fail(TDP_EINVAL, "%s: dout and dq need q's heads, dk and dv k's", fn);
+  if (!lse) return fail(TDP_EINVAL, "%s: null lse", fn);
+  if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 15))
+    return fail(TDP_EINVAL, "%s: workspace must be a 16-byte aligned device pointer", fn);
+  A.delta = static_cast<float*>(workspace);
+  const int64_t sh = (int64_t)q_seqs->num_seqs * k->heads;
+  const int64_t qt = A.blocks * sh, kt = ((int64_t)k_seqs->max_rows + 127) / 128 * sh;
+  const int64_t db = seq_blocks(*q_seqs, 4);
+  st = check_items(fn, qt > kt ? (qt > db ? qt : db) : (kt > db ? kt : db));
+  if (st != TDP_OK) return st;
+  A.tiles = (uint32_t)qt;
+  hipStream_t hs = reinterpret_cast<hipStream_t>(stream);
+#define CALL(T, DP, B) launch_backward<T, DP, B>(A, (uint32_t)q_seqs->max_rows, (uint32_t)k_seqs->max_rows, hs)
+  TDP_ATTN_DISPATCH(CALL);
+#undef CALL
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return fail(TDP_EHIP, "%s: kernel launch failed: %s", fn, hipGetErrorString(e));
+  return TDP_OK;
+}
+
+}  // extern "C"
