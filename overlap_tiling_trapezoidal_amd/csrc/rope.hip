@@ -5,14 +5,17 @@
 // "Position normalization" (each tile hands the model its own zero-based
 // [start, end) intervals on time, height and width).
 //
-// All three kernels are bound by HBM bandwidth: a few operations per element
-// read and written once.  A wave owns one row (token) at a time, all its heads:
-// its lanes compute the row's angles once, one pair each, into LDS, and every
-// head reuses them, so no table of cosines is stored or read (24 bytes of
-// positions per row instead of 4 * head_dim).  A lane moves eight elements of
-// a head (16 bytes of bf16), G lanes share a head (G = the power of two at or
-// above head_dim / 8) and 64 / G heads go through the wave at once; the norm's
-// sums run over the G lanes by cross-lane moves.
+// All kernels are bound by HBM bandwidth: a few operations per element read
+// and written once.  A wave owns one row (token) at a time, all its heads: its
+// lanes compute the row's angles once, one pair each, into LDS, and every head
+// reuses them, so no table of cosines is stored or read (24 bytes of positions
+// per row instead of 4 * head_dim).  A lane moves eight elements of a head in
+// 16-byte pieces, G lanes share a head (G = the power of two at or above
+// head_dim / 8) and 64 / G heads go through the wave at once; the norm's sums
+// run over the G lanes by DPP moves.  A batch of U such passes is loaded ahead
+// of the one being worked on, across rows too: a workgroup takes several
+// consecutive blocks of four rows, so what does not depend on the row (weights,
+// frequencies, partners) is set up once.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -42,10 +45,10 @@ __device__ inline void turn(float a, float b, bool middle, float hi, float lo, f
 
 __device__ inline int pair_axis(const RopeDev& r, int p) { return (p >= r.pair_end[0]) + (p >= r.pair_end[1]); }
 
-// One wave's cos/sin of a row: pair p at [p], and (1, 0) for the unturned dims
-// at [pairs] and up (to pair 128).
+// One wave's row of angles, per dim: the factor of the dim itself and of its
+// partner, y[d] = x[d] c[d] + x[partner] s[d] (s carries the pair's sign).
 struct Angles {
-  float c[kMaxPairs + 1], s[kMaxPairs + 1];
+  float c[TDP_MAX_ROPE_DIM], s[TDP_MAX_ROPE_DIM];
 };
 
 __device__ inline void wave_lds_fence() {
@@ -55,94 +58,192 @@ __device__ inline void wave_lds_fence() {
   __builtin_amdgcn_wave_barrier();
 }
 
-__device__ inline void fill_angles(const RopeDev& r, const float* pos, const SeqRows& sr, int i, int lane, Angles* a) {
-  const f32x2* base = reinterpret_cast<const f32x2*>(pos) + 3 * sr.row0 + i;
-  for (int p = lane; p < r.D / 2 + 1; p += 64) {
-    float c = 1.0f, s = 0.0f;
-    if (p < r.pairs) {
-      const f32x2 iv = base[(int64_t)pair_axis(r, p) * sr.span];
-      turn(iv.x, iv.y, r.point == TDP_POINT_MIDDLE, r.hi[p], r.lo[p], &c, &s);
+// A lane's pairs of a row: p = lane and lane + 64 (head_dim > 128).
+template <bool HALVES, int G>
+struct LaneTurns {
+  static constexpr int N = G > 16 ? 2 : 1;
+  float hi[N], lo[N];
+  int axis[N], d0[N], d1[N];
+  bool on[N];
+  __device__ inline LaneTurns(const RopeDev& r, int lane) {
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+      const int p = lane + 64 * n;
+      on[n] = p < r.pairs;
+      axis[n] = on[n] ? pair_axis(r, p) : 0;
+      hi[n] = on[n] ? r.hi[p] : 0.0f;
+      lo[n] = on[n] ? r.lo[p] : 0.0f;
+      d0[n] = 2 * p;
+      d1[n] = 2 * p + 1;
+      if (HALVES && on[n]) {
+        d0[n] = p + (axis[n] == 0 ? 0 : r.pair_end[axis[n] - 1]);
+        d1[n] = d0[n] + r.half[axis[n]];
+      }
     }
-    a->c[p] = c;
-    a->s[p] = s;
   }
+  // the dims that do not turn follow the pairs; once per wave
+  __device__ inline void clear(int D, int lane, Angles* a) const {
+    for (int d = lane; d < D; d += 64) {
+      a->c[d] = 1.0f;
+      a->s[d] = 0.0f;
+    }
+  }
+  __device__ inline void load(const float* pos, const SeqRows& sr, int i, f32x2* iv) const {
+    const f32x2* base = reinterpret_cast<const f32x2*>(pos) + 3 * sr.row0 + i;
+#pragma unroll
+    for (int n = 0; n < N; ++n)
+      if (on[n]) iv[n] = base[(int64_t)axis[n] * sr.span];
+  }
+  __device__ inline void fill(const f32x2* iv, bool middle, float dir, Angles* a) const {
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+      if (!on[n]) continue;
+      float c, s;
+      turn(iv[n].x, iv[n].y, middle, hi[n], lo[n], &c, &s);
+      s *= dir;
+      a->c[d0[n]] = a->c[d1[n]] = c;
+      a->s[d0[n]] = -s;
+      a->s[d1[n]] = s;
+    }
+  }
+};
+
+// The dims of a lane: bf16, eight in a row; fp32, four in each half of the
+// head, so that each 16-byte access of neighbouring lanes is contiguous.
+template <int T>
+__device__ inline int lane_dim(int D, int chunk, int e) {
+  return T == TDP_BF16 ? chunk * 8 + e : chunk * 4 + (e & 3) + (e >> 2) * (D / 2);
+}
+// Inverse of it: the slot e * 64 + chunk of dim d in a wave's exchange buffer.
+template <int T>
+__device__ inline int dim_slot(int D, int d) {
+  if (T == TDP_BF16) return (d & 7) * 64 + (d >> 3);
+  const int up = d >= D / 2, q = d - up * (D / 2);
+  return ((q & 3) + 4 * up) * 64 + (q >> 2);
 }
 
-// Which angle and which partner each of a lane's eight dims uses.
-template <bool HALVES>
-struct LanePairs {
-  int pair[HALVES ? 8 : 4];
-  int src[HALVES ? 8 : 1];     // slot of the partner in the wave's exchange buffer
-  float sign[HALVES ? 8 : 1];  // -1 on the first half of a section
-  __device__ inline LanePairs(const RopeDev& r, int chunk, int group_lane0) {
-    if constexpr (!HALVES) {
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int p = chunk * 4 + e;
-        pair[e] = p < r.D / 2 ? p : r.D / 2;  // entries past `pairs` hold (1, 0)
-      }
+template <int T>
+struct Raw {
+  u32x4 v[T == TDP_BF16 ? 1 : 2];
+  // p: the lane's first dim; half: bytes from the first quad to the second (fp32)
+  __device__ inline void load(const char* p, int half, bool on) {
+    v[0] = u32x4{0, 0, 0, 0};
+    if constexpr (T == TDP_F32) v[1] = u32x4{0, 0, 0, 0};
+    if (on) {
+      v[0] = ld_nt(reinterpret_cast<const u32x4*>(p));
+      if constexpr (T == TDP_F32) v[1] = ld_nt(reinterpret_cast<const u32x4*>(p + half));
+    }
+  }
+  __device__ inline void unpack(float* x) const {
+    InVec<T>::unpack(v[0], x);
+    if constexpr (T == TDP_F32) InVec<T>::unpack(v[1], x + 4);
+  }
+  __device__ static inline void store(char* p, int half, const float* x) {
+    if constexpr (T == TDP_BF16) {
+      store_out<TDP_BF16, 8>(p, 0, x);
     } else {
+      st_nt(reinterpret_cast<f32x4*>(p), f32x4{x[0], x[1], x[2], x[3]});
+      st_nt(reinterpret_cast<f32x4*>(p + half), f32x4{x[4], x[5], x[6], x[7]});
+    }
+  }
+};
+
+// Where the partners of a lane's dims pass through a wave's exchange buffer
+// (half-split pairs; the other pairs lie in one lane).
+template <int T, bool HALVES>
+struct Partners {
+  int src[HALVES ? 8 : 1];
+  __device__ inline Partners(const RopeDev& r, int chunk, int group_lane0) {
+    if constexpr (HALVES) {
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        const int d = chunk * 8 + e;
-        pair[e] = r.D / 2;
+        const int d = lane_dim<T>(r.D, chunk, e);
         src[e] = e * 64 + group_lane0 + chunk;
-        sign[e] = 0.0f;
-        if (d < 2 * r.pairs) {
+        if (chunk * 8 < r.D && d < 2 * r.pairs) {
           const int ax = pair_axis(r, d / 2);
-          const int first = ax == 0 ? 0 : r.pair_end[ax - 1];
-          const int j = d - 2 * first, h = r.half[ax];
-          const bool lower = j < h;
-          const int dp = lower ? d + h : d - h;
-          pair[e] = first + (lower ? j : j - h);
-          src[e] = (dp & 7) * 64 + group_lane0 + (dp >> 3);
-          sign[e] = lower ? -1.0f : 1.0f;
+          const int j = d - (ax == 0 ? 0 : 2 * r.pair_end[ax - 1]);
+          src[e] = dim_slot<T>(r.D, j < r.half[ax] ? d + r.half[ax] : d - r.half[ax]) + group_lane0;
         }
       }
     }
   }
 };
 
-// The cos and signed sin of a lane's dims for one row.
-template <bool HALVES>
+// The factors of a lane's dims for one row; a pair inside the lane needs them
+// once.
+template <int T, bool HALVES>
 struct LaneAngles {
-  float c[HALVES ? 8 : 4], s[HALVES ? 8 : 4];
-  __device__ inline LaneAngles(const LanePairs<HALVES>& lp, const Angles* a, float dir) {
+  static constexpr int N = HALVES ? 8 : 4;
+  float c[N], s[N];
+  __device__ inline void read(int D, int chunk, bool on, const Angles* a) {
+    const int d0 = on ? lane_dim<T>(D, chunk, 0) : 0, d1 = on ? lane_dim<T>(D, chunk, 4) : 0;
+    float cc[8], ss[8];
 #pragma unroll
-    for (int e = 0; e < (HALVES ? 8 : 4); ++e) {
-      c[e] = a->c[lp.pair[e]];
-      s[e] = a->s[lp.pair[e]] * dir;
-      if constexpr (HALVES) s[e] *= lp.sign[e];
+    for (int e = 0; e < 4; ++e) {
+      cc[e] = a->c[d0 + e];
+      cc[4 + e] = a->c[d1 + e];
+      ss[e] = a->s[d0 + e];
+      ss[4 + e] = a->s[d1 + e];
+    }
+#pragma unroll
+    for (int e = 0; e < N; ++e) {
+      c[e] = cc[HALVES ? e : 2 * e];
+      s[e] = ss[HALVES ? e : 2 * e + 1];
     }
   }
 };
 
-template <bool HALVES>
-__device__ inline void rotate8(const LanePairs<HALVES>& lp, const LaneAngles<HALVES>& la, float* ex, int lane,
-                               float* x) {
+// Turn the first n of U vectors.  Half-split partners sit in other lanes: they
+// pass through LDS, element e of lane l at e * 64 + l, so writes and reads touch
+// consecutive banks; all vectors are written before the first is read.
+template <int T, bool HALVES, int U>
+__device__ inline void rotate(const Partners<T, HALVES>& pt, const LaneAngles<T, HALVES>& la, float* ex, int lane, int n,
+                              float (*x)[8]) {
   if constexpr (!HALVES) {
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const float a = x[2 * e], b = x[2 * e + 1];
-      x[2 * e] = fmaf(a, la.c[e], -b * la.s[e]);
-      x[2 * e + 1] = fmaf(b, la.c[e], a * la.s[e]);
+    for (int u = 0; u < U; ++u) {
+      if (u >= n) break;
+#pragma unroll
+      for (int e = 0; e < 8; e += 2) {
+        const float a = x[u][e], b = x[u][e + 1];
+        x[u][e] = fmaf(a, la.c[e / 2], -b * la.s[e / 2]);
+        x[u][e + 1] = fmaf(b, la.c[e / 2], a * la.s[e / 2]);
+      }
     }
   } else {
-    // partners sit in other lanes: element e of lane l at e * 64 + l, so
-    // writes and reads touch consecutive banks
     wave_lds_fence();
 #pragma unroll
-    for (int e = 0; e < 8; ++e) ex[e * 64 + lane] = x[e];
+    for (int u = 0; u < U; ++u) {
+      if (u >= n) break;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) ex[u * 512 + e * 64 + lane] = x[u][e];
+    }
     wave_lds_fence();
 #pragma unroll
-    for (int e = 0; e < 8; ++e) x[e] = fmaf(x[e], la.c[e], ex[lp.src[e]] * la.s[e]);
+    for (int u = 0; u < U; ++u) {
+      if (u >= n) break;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) x[u][e] = fmaf(x[u][e], la.c[e], ex[u * 512 + pt.src[e]] * la.s[e]);
+    }
   }
 }
 
+template <int CTRL>
+__device__ inline float dpp(float v) {
+  return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), CTRL, 0xf, 0xf, true));
+}
+// Sum over aligned groups of G lanes: quads by permutes, then mirrors of 8 and
+// 16 lanes, then the swap of neighbouring rows of 16.
 template <int G>
 __device__ inline float group_sum(float v) {
-#pragma unroll
-  for (int o = 1; o < G; o <<= 1) v += __shfl_xor(v, o);
+  if constexpr (G >= 2) v += dpp<0xB1>(v);
+  if constexpr (G >= 4) v += dpp<0x4E>(v);
+  if constexpr (G >= 8) v += dpp<0x141>(v);
+  if constexpr (G >= 16) v += dpp<0x140>(v);
+  if constexpr (G >= 32) {
+    const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    v = __uint_as_float(r[0]) + __uint_as_float(r[1]);
+  }
   return v;
 }
 
@@ -156,206 +257,316 @@ struct RopeArgs {
   float* parts;            // backward: partial weight gradients
   float eps, dir;          // dir -1: inverse rotation
   uint32_t blocks;         // row blocks per sequence
+  uint32_t per_wg;         // forward: row blocks per workgroup
+  uint32_t q_wgs;          // backward: workgroups on queries, the others take keys
 };
 
-// One row (sequence s, row i) per wave; workgroups cover every row once.
-template <int T, int G, bool HALVES, bool NORM>
-__global__ __launch_bounds__(kTok) void rope_kernel(const RopeArgs A) {
-  __shared__ Angles ang[kWaves];
-  __shared__ float exch[HALVES ? kWaves : 1][HALVES ? 512 : 1];
-  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
-  const int s = blockIdx.x / A.blocks;
-  const int i = (blockIdx.x - s * A.blocks) * kWaves + wave;
-  const SeqRows sr = seq_rows(A.seqs, s);
-  if (i >= sr.cap) return;
-  const int chunk = lane % G, grp = lane / G;
-  const bool on = chunk * 8 < A.rope.D;
-  const int nq = A.in[0].heads, H = nq + A.in[1].heads;
-  constexpr int kPer = 64 / G;
-  int64_t ib[2], ob[2];
-#pragma unroll
-  for (int t = 0; t < 2; ++t) {
-    ib[t] = seq_base(A.seqs, A.in[t], s, sr) + i * A.in[t].row_stride + chunk * 8;
-    ob[t] = seq_base(A.seqs, A.out[t], s, sr) + i * A.out[t].row_stride + chunk * 8;
+// The rows of one wave: block blk of the launch is rows 4 k .. 4 k + 3 of a
+// sequence, one per wave of the workgroup.
+struct RowAt {
+  uint32_t blk;
+  int s, i;
+  SeqRows sr;
+  __device__ inline void seek(const SeqsDev& q, uint32_t blocks, uint32_t b, int wave) {
+    blk = b;
+    s = b / blocks;
+    i = (b - s * blocks) * kWaves + wave;
+    sr = seq_rows(q, s);
   }
-  if (i >= sr.len) {
-    const float z[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-    for (int h = grp; h < H; h += kPer) {
-      const int t = h >= nq, hh = t ? h - nq : h;
-      if (on) store8<T>(A.out[t].data, ob[t] + hh * A.out[t].head_stride, z);
+  __device__ inline void next(const SeqsDev& q, uint32_t blocks, int wave) {
+    ++blk;
+    i += kWaves;
+    if (blk == (uint32_t)(s + 1) * blocks) {
+      ++s;
+      i = wave;
+      sr = seq_rows(q, s);
     }
-    return;
   }
-  fill_angles(A.rope, A.pos, sr, i, lane, &ang[wave]);
-  const LanePairs<HALVES> lp(A.rope, chunk, lane - chunk);
-  wave_lds_fence();
-  const LaneAngles<HALVES> la(lp, &ang[wave], A.dir);
-  float w[2][8];
+  __device__ inline bool owned() const { return i < sr.cap; }
+  __device__ inline bool live() const { return i < sr.len; }
+};
+
+// A tensor as a wave sees it: the lane's share of a head, and the row's base
+// (the same for the whole wave).
+template <int T, int G>
+struct Lanes {
+  static constexpr int eb = T == TDP_BF16 ? 2 : 4, kPer = 64 / G;
+  char* lane0;
+  int64_t row_step, head_step, seq_step;
+  int heads;
+  __device__ inline Lanes(const HeadsDev& t, int chunk, int grp)
+      : lane0(t.data + eb * (grp * t.head_stride + chunk * (T == TDP_BF16 ? 8 : 4))),
+        row_step(t.row_stride * eb), head_step(t.head_stride * eb), seq_step(t.seq_stride * eb), heads(t.heads) {}
+  __device__ inline char* at(const SeqsDev& q, const RowAt& r, int head) const {
+    const int64_t base = q.range ? (r.sr.row0 + r.i) * row_step : r.s * seq_step + r.i * row_step;
+    return lane0 + (base + head * head_step);
+  }
+  __device__ inline void zero(const SeqsDev& q, const RowAt& r, int half, int grp, bool on) const {
+    const float z[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+    for (int h = 0; h < heads; h += kPer)
+      if (on && h + grp < heads) Raw<T>::store(at(q, r, h), half, z);
+  }
+};
+
+template <int T, int G, bool HALVES, bool NORM, int U>
+__global__ __launch_bounds__(kTok, U == 2 ? 4 : 3) void rope_kernel(const RopeArgs A) {
+  constexpr int kPer = 64 / G;
+  __shared__ Angles ang[kWaves];
+  __shared__ float exch[HALVES ? kWaves : 1][HALVES ? U * 512 : 1];
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+  const int chunk = lane % G, grp = lane / G, half = A.rope.D * 2;
+  const bool on = chunk * 8 < A.rope.D;
+  const uint32_t nblk = A.blocks * (uint32_t)A.seqs.S;
+  const uint32_t b0 = blockIdx.x * A.per_wg, b1 = b0 + A.per_wg < nblk ? b0 + A.per_wg : nblk;
+  const Lanes<T, G> iq(A.in[0], chunk, grp), ik(A.in[1], chunk, grp), oq(A.out[0], chunk, grp), ok(A.out[1], chunk, grp);
+  const int nq = (iq.heads + kPer * U - 1) / (kPer * U), nk = (ik.heads + kPer * U - 1) / (kPer * U);
+  const LaneTurns<HALVES, G> turns(A.rope, lane);
+  const Partners<T, HALVES> pt(A.rope, chunk, lane - chunk);
+  turns.clear(A.rope.D, lane, &ang[wave]);
+  const float inv_d = 1.0f / (float)A.rope.D;
+  float wq[8], wk[8];
   if constexpr (NORM) {
 #pragma unroll
-    for (int t = 0; t < 2; ++t)
-#pragma unroll
-      for (int e = 0; e < 8; ++e) w[t][e] = A.w[t] && on ? A.w[t][chunk * 8 + e] : 1.0f;
-  }
-  constexpr int U = 4;  // heads in flight per lane
-  for (int h0 = 0; h0 < H; h0 += kPer * U) {
-    float x[U][8];
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int h = h0 + u * kPer + grp;
-      const int t = h >= nq, hh = t ? h - nq : h;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) x[u][e] = 0.0f;
-      if (on && h < H) load8<T>(A.in[t].data, ib[t] + hh * A.in[t].head_stride, x[u]);
+    for (int e = 0; e < 8; ++e) {
+      const int d = lane_dim<T>(A.rope.D, chunk, e);
+      wq[e] = A.w[0] && on ? A.w[0][d] : 1.0f;
+      wk[e] = A.w[1] && on ? A.w[1][d] : 1.0f;
     }
+  }
+  RowAt nx;
+  Raw<T> raw[U];
+  f32x2 iv[LaneTurns<HALVES, G>::N];
+  auto fetch = [&](const RowAt& r, int b) {
+    const bool k = b >= nq;  // the same for the whole wave
+    const int h0 = (k ? b - nq : b) * kPer * U, heads = k ? ik.heads : iq.heads;
+    const char* p = k ? ik.at(A.seqs, r, h0) : iq.at(A.seqs, r, h0);
+    const int64_t step = (k ? ik.head_step : iq.head_step) * kPer;
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int h = h0 + u * kPer + grp;
-      const int t = h >= nq, hh = t ? h - nq : h;
-      if constexpr (NORM) {
-        float ss = 0.0f;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) ss = fmaf(x[u][e], x[u][e], ss);
-        ss = group_sum<G>(ss);
-        const float r = 1.0f / sqrtf(ss / (float)A.rope.D + A.eps);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) x[u][e] *= r * (t ? w[1][e] : w[0][e]);
+    for (int u = 0; u < U; ++u) raw[u].load(p + u * step, half, on && h0 + u * kPer + grp < heads);
+  };
+  auto begin_row = [&]() {
+    if (nx.live()) {
+      fetch(nx, 0);
+      turns.load(A.pos, nx.sr, nx.i, iv);
+    }
+  };
+  nx.seek(A.seqs, A.blocks, b0, wave);
+  begin_row();
+  for (uint32_t blk = b0; blk < b1; ++blk) {
+    const RowAt at = nx;
+    if (!at.live()) {
+      if (at.owned()) {
+        oq.zero(A.seqs, at, half, grp, on);
+        ok.zero(A.seqs, at, half, grp, on);
       }
-      rotate8<HALVES>(lp, la, exch[HALVES ? wave : 0], lane, x[u]);
-      if (on && h < H) store8<T>(A.out[t].data, ob[t] + hh * A.out[t].head_stride, x[u]);
+      if (blk + 1 < b1) {
+        nx.next(A.seqs, A.blocks, wave);
+        begin_row();
+      }
+      continue;
+    }
+    wave_lds_fence();
+    turns.fill(iv, A.rope.point == TDP_POINT_MIDDLE, A.dir, &ang[wave]);
+    wave_lds_fence();
+    LaneAngles<T, HALVES> la;
+    la.read(A.rope.D, chunk, on, &ang[wave]);
+    for (int b = 0; b < nq + nk; ++b) {
+      const bool k = b >= nq;
+      const int heads = k ? ik.heads : iq.heads;
+      const int hb = (k ? b - nq : b) * kPer * U;
+      const int n = (heads - hb + kPer - 1) / kPer;  // passes with a head left, the same for the whole wave
+      float x[U][8];
+#pragma unroll
+      for (int u = 0; u < U; ++u) raw[u].unpack(x[u]);
+      if (b + 1 < nq + nk) {
+        fetch(at, b + 1);
+      } else if (blk + 1 < b1) {
+        nx.next(A.seqs, A.blocks, wave);
+        begin_row();
+      }
+      if constexpr (NORM) {
+        float w[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) w[e] = k ? wk[e] : wq[e];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          if (u >= n) break;
+          float ss = 0.0f;
+#pragma unroll
+          for (int e = 0; e < 8; ++e) ss = fmaf(x[u][e], x[u][e], ss);
+          const float r = __builtin_amdgcn_rsqf(fmaf(group_sum<G>(ss), inv_d, A.eps));
+#pragma unroll
+          for (int e = 0; e < 8; ++e) x[u][e] *= r * w[e];
+        }
+      }
+      rotate<T, HALVES, U>(pt, la, exch[HALVES ? wave : 0], lane, n, x);
+      char* p = k ? ok.at(A.seqs, at, hb) : oq.at(A.seqs, at, hb);
+      const int64_t step = (k ? ok.head_step : oq.head_step) * kPer;
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        if (on && hb + u * kPer + grp < heads) Raw<T>::store(p + u * step, half, x[u]);
     }
   }
 }
 
 // Gradient of the norm and rotation: dx per row, and each workgroup's sums of
-// the weights' gradients over its rows, in a fixed order.
+// the weight's gradient over its rows, in a fixed order.  A workgroup takes
+// queries or keys (the first q_wgs take queries), which keeps one tensor's sums
+// and weights in registers.
 template <int T, int G, bool HALVES>
-__global__ __launch_bounds__(kTok) void norm_backward_kernel(const RopeArgs A) {
+__global__ __launch_bounds__(kTok, 3) void norm_backward_kernel(const RopeArgs A) {
+  constexpr int kPer = 64 / G, U = 2;
   __shared__ Angles ang[kWaves];
-  __shared__ float exch[HALVES ? kWaves : 1][HALVES ? 512 : 1];
-  __shared__ float red[kWaves][2][TDP_MAX_ROPE_DIM];
-  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
-  const int chunk = lane % G, grp = lane / G;
+  __shared__ float exch[HALVES ? kWaves : 1][HALVES ? U * 512 : 1];
+  __shared__ float red[kWaves][TDP_MAX_ROPE_DIM];
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+  const int chunk = lane % G, grp = lane / G, half = A.rope.D * 2;
   const bool on = chunk * 8 < A.rope.D;
-  const int nq = A.in[0].heads, H = nq + A.in[1].heads;
-  constexpr int kPer = 64 / G;
-  const LanePairs<HALVES> lp(A.rope, chunk, lane - chunk);
-  float w[2][8], dw[2][8];
-#pragma unroll
-  for (int t = 0; t < 2; ++t)
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      w[t][e] = A.w[t] && on ? A.w[t][chunk * 8 + e] : 1.0f;
-      dw[t][e] = 0.0f;
-    }
+  const bool keys = blockIdx.x >= A.q_wgs;
+  const Lanes<T, G> in(keys ? A.in[1] : A.in[0], chunk, grp), gr(keys ? A.grad[1] : A.grad[0], chunk, grp),
+      out(keys ? A.out[1] : A.out[0], chunk, grp);
+  const float* wp = keys ? A.w[1] : A.w[0];
   const uint32_t nblk = A.blocks * (uint32_t)A.seqs.S;
-  for (uint32_t blk = blockIdx.x; blk < nblk; blk += gridDim.x) {
-    const int s = blk / A.blocks;
-    const int i = (blk - s * A.blocks) * kWaves + wave;
-    const SeqRows sr = seq_rows(A.seqs, s);
-    if (i >= sr.cap) continue;
-    int64_t ib[2], gb[2], ob[2];
+  const uint32_t wg = keys ? blockIdx.x - A.q_wgs : blockIdx.x, wgs = keys ? gridDim.x - A.q_wgs : A.q_wgs;
+  const uint32_t b0 = (uint32_t)((uint64_t)nblk * wg / wgs), b1 = (uint32_t)((uint64_t)nblk * (wg + 1) / wgs);
+  const int nb = (in.heads + kPer * U - 1) / (kPer * U);
+  const LaneTurns<HALVES, G> turns(A.rope, lane);
+  const Partners<T, HALVES> pt(A.rope, chunk, lane - chunk);
+  turns.clear(A.rope.D, lane, &ang[wave]);
+  const float inv_d = 1.0f / (float)A.rope.D;
+  float w[8], dw[8];
 #pragma unroll
-    for (int t = 0; t < 2; ++t) {
-      ib[t] = seq_base(A.seqs, A.in[t], s, sr) + i * A.in[t].row_stride + chunk * 8;
-      gb[t] = seq_base(A.seqs, A.grad[t], s, sr) + i * A.grad[t].row_stride + chunk * 8;
-      ob[t] = seq_base(A.seqs, A.out[t], s, sr) + i * A.out[t].row_stride + chunk * 8;
+  for (int e = 0; e < 8; ++e) {
+    w[e] = wp && on ? wp[lane_dim<T>(A.rope.D, chunk, e)] : 1.0f;
+    dw[e] = 0.0f;
+  }
+  RowAt nx;
+  Raw<T> rx[U], rg[U];
+  f32x2 iv[LaneTurns<HALVES, G>::N];
+  auto fetch = [&](const RowAt& r, int b) {
+    const int h0 = b * kPer * U;
+    const char *ip = in.at(A.seqs, r, h0), *gp = gr.at(A.seqs, r, h0);
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const bool ld = on && h0 + u * kPer + grp < in.heads;
+      rx[u].load(ip + u * kPer * in.head_step, half, ld);
+      rg[u].load(gp + u * kPer * gr.head_step, half, ld);
     }
-    if (i >= sr.len) {
-      const float z[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-      for (int h = grp; h < H; h += kPer) {
-        const int t = h >= nq, hh = t ? h - nq : h;
-        if (on) store8<T>(A.out[t].data, ob[t] + hh * A.out[t].head_stride, z);
+  };
+  auto begin_row = [&]() {
+    if (nx.live()) {
+      fetch(nx, 0);
+      turns.load(A.pos, nx.sr, nx.i, iv);
+    }
+  };
+  if (b0 < b1) {
+    nx.seek(A.seqs, A.blocks, b0, wave);
+    begin_row();
+  }
+  for (uint32_t blk = b0; blk < b1; ++blk) {
+    const RowAt at = nx;
+    if (!at.live()) {
+      if (at.owned()) out.zero(A.seqs, at, half, grp, on);
+      if (blk + 1 < b1) {
+        nx.next(A.seqs, A.blocks, wave);
+        begin_row();
       }
       continue;
     }
     wave_lds_fence();
-    fill_angles(A.rope, A.pos, sr, i, lane, &ang[wave]);
+    turns.fill(iv, A.rope.point == TDP_POINT_MIDDLE, -1.0f, &ang[wave]);
     wave_lds_fence();
-    const LaneAngles<HALVES> la(lp, &ang[wave], -1.0f);
-    constexpr int U = 2;
-    for (int h0 = 0; h0 < H; h0 += kPer * U) {
+    LaneAngles<T, HALVES> la;
+    la.read(A.rope.D, chunk, on, &ang[wave]);
+    for (int b = 0; b < nb; ++b) {
+      const int hb = b * kPer * U;
+      const int n = (in.heads - hb + kPer - 1) / kPer;
       float x[U][8], g[U][8];
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        const int h = h0 + u * kPer + grp;
-        const int t = h >= nq, hh = t ? h - nq : h;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) x[u][e] = g[u][e] = 0.0f;
-        if (on && h < H) {
-          load8<T>(A.in[t].data, ib[t] + hh * A.in[t].head_stride, x[u]);
-          load8<T>(A.grad[t].data, gb[t] + hh * A.grad[t].head_stride, g[u]);
-        }
+        rx[u].unpack(x[u]);
+        rg[u].unpack(g[u]);
       }
+      if (b + 1 < nb) {
+        fetch(at, b + 1);
+      } else if (blk + 1 < b1) {
+        nx.next(A.seqs, A.blocks, wave);
+        begin_row();
+      }
+      rotate<T, HALVES, U>(pt, la, exch[HALVES ? wave : 0], lane, n, g);
+      char* op = out.at(A.seqs, at, hb);
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        const int h = h0 + u * kPer + grp;
-        const int t = h >= nq, hh = t ? h - nq : h;
-        rotate8<HALVES>(lp, la, exch[HALVES ? wave : 0], lane, g[u]);
+        if (u >= n) break;
         float ss = 0.0f, gx = 0.0f;
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
           ss = fmaf(x[u][e], x[u][e], ss);
-          gx = fmaf(g[u][e] * (t ? w[1][e] : w[0][e]), x[u][e], gx);
+          gx = fmaf(g[u][e] * w[e], x[u][e], gx);
         }
-        ss = group_sum<G>(ss);
-        gx = group_sum<G>(gx);
-        const float inv = 1.0f / (float)A.rope.D;
-        const float r = 1.0f / sqrtf(ss * inv + A.eps);
-        const float m = gx * inv * r * r;
+        const float r = __builtin_amdgcn_rsqf(fmaf(group_sum<G>(ss), inv_d, A.eps));
+        const float m = group_sum<G>(gx) * inv_d * r * r;
         float y[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-          const float nx = g[u][e] * (x[u][e] * r);
-          dw[0][e] += t ? 0.0f : nx;
-          dw[1][e] += t ? nx : 0.0f;
-          y[e] = r * fmaf(g[u][e], t ? w[1][e] : w[0][e], -x[u][e] * m);
+          dw[e] = fmaf(g[u][e], x[u][e] * r, dw[e]);
+          y[e] = r * fmaf(g[u][e], w[e], -x[u][e] * m);
         }
-        if (on && h < H) store8<T>(A.out[t].data, ob[t] + hh * A.out[t].head_stride, y);
+        if (on && hb + u * kPer + grp < in.heads) Raw<T>::store(op + u * kPer * out.head_step, half, y);
       }
     }
   }
   // the wave's groups, then its four waves
 #pragma unroll
-  for (int t = 0; t < 2; ++t)
+  for (int e = 0; e < 8; ++e) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-#pragma unroll
-      for (int o = G; o < 64; o <<= 1) dw[t][e] += __shfl_xor(dw[t][e], o);
-      if (grp == 0 && on) red[wave][t][chunk * 8 + e] = dw[t][e];
-    }
-  __syncthreads();
-  for (int c = threadIdx.x; c < 2 * A.rope.D; c += kTok) {
-    const int t = c >= A.rope.D, d = t ? c - A.rope.D : c;
-    A.parts[(int64_t)blockIdx.x * 2 * A.rope.D + c] = (red[0][t][d] + red[1][t][d]) + (red[2][t][d] + red[3][t][d]);
+    for (int o = G; o < 64; o <<= 1) dw[e] += __shfl_xor(dw[e], o);
+    if (grp == 0 && on) red[wave][lane_dim<T>(A.rope.D, chunk, e)] = dw[e];
   }
+  __syncthreads();
+  for (int d = threadIdx.x; d < A.rope.D; d += kTok)
+    A.parts[(int64_t)blockIdx.x * A.rope.D + d] = (red[0][d] + red[1][d]) + (red[2][d] + red[3][d]);
 }
 
 // Sum the workgroups' partial rows: 16 columns per workgroup, 16 strided row
-// sums per column joined in order.
-__global__ __launch_bounds__(kTok) void norm_weights_kernel(const float* parts, int n, int D, float* dwq, float* dwk) {
+// sums per column joined in order; the first workgroups take queries.
+__global__ __launch_bounds__(kTok) void norm_weights_kernel(const float* parts, int nq, int n, int D, float* dwq,
+                                                            float* dwk) {
   __shared__ float red[16][17];
+  const int per = (D + 15) / 16;
+  const bool keys = (int)blockIdx.x >= per;
   const int col = threadIdx.x & 15, row = threadIdx.x >> 4;
-  const int c = blockIdx.x * 16 + col;
+  const int c = (keys ? blockIdx.x - per : blockIdx.x) * 16 + col;
+  float* out = keys ? dwk : dwq;
   float v = 0.0f;
-  if (c < 2 * D)
-    for (int r = row; r < n; r += 16) v += parts[(int64_t)r * 2 * D + c];
+  if (c < D)
+    for (int r = (keys ? nq : 0) + row; r < (keys ? n : nq); r += 16) v += parts[(int64_t)r * D + c];
   red[row][col] = v;
   __syncthreads();
-  if (row == 0 && c < 2 * D) {
+  if (row == 0 && c < D && out) {
     float sum = 0.0f;
     for (int r = 0; r < 16; ++r) sum += red[r][col];
-    float* out = c < D ? dwq : dwk;
-    if (out) out[c < D ? c : c - D] = sum;
+    out[c] = sum;
   }
 }
 
+// Four passes of the wave ahead where a tensor's heads fill them, two where
+// they would not: on 16 bf16 heads of 128 dims (4 passes) four took 329 us for
+// 2.0 GB against 354, on 8 and 4 fp32 heads of 64 dims (one pass each) two took
+// 182 us for 0.8 GB against 208, registers and exchange buffers being smaller.
+template <int T, int G, bool NORM, bool HALVES>
+void launch_forward(const RopeArgs& a, uint32_t grid, hipStream_t st) {
+  if (a.in[0].heads >= 4 * (64 / G))
+    hipLaunchKernelGGL((rope_kernel<T, G, HALVES, NORM, 4>), dim3(grid), dim3(kTok), 0, st, a);
+  else
+    hipLaunchKernelGGL((rope_kernel<T, G, HALVES, NORM, 2>), dim3(grid), dim3(kTok), 0, st, a);
+}
 template <int T, int G, bool NORM>
 void launch_forward(const RopeArgs& a, uint32_t grid, hipStream_t st) {
   if (a.rope.pairing == TDP_PAIR_HALVES)
-    hipLaunchKernelGGL((rope_kernel<T, G, true, NORM>), dim3(grid), dim3(kTok), 0, st, a);
+    launch_forward<T, G, NORM, true>(a, grid, st);
   else
-    hipLaunchKernelGGL((rope_kernel<T, G, false, NORM>), dim3(grid), dim3(kTok), 0, st, a);
+    launch_forward<T, G, NORM, false>(a, grid, st);
 }
 template <int T, int G>
 void launch_backward(const RopeArgs& a, uint32_t grid, hipStream_t st) {
@@ -401,6 +612,18 @@ int begin(const char* fn, const tdp_rope* rope, const tdp_seqs* seqs, const floa
   return TDP_OK;
 }
 
+// Row blocks per workgroup of a forward launch: rows of fewer than 4 passes of
+// 64 lanes are taken 32 passes at a time, so that the wave's setup is shared,
+// as long as 4096 workgroups (16 per CU) remain.
+uint32_t forward_grid(const tdp_seqs& s, RopeArgs* a) {
+  const int64_t nblk = seq_blocks(s, kWaves);
+  const int64_t lanes = (int64_t)(a->in[0].heads + a->in[1].heads) * ((a->rope.D + 7) / 8);
+  int64_t per = lanes < 4 * 64 ? 32 * 64 / lanes : 1;
+  if (per > nblk / 4096) per = nblk / 4096;
+  a->per_wg = (uint32_t)(per < 1 ? 1 : per);
+  return (uint32_t)((nblk + a->per_wg - 1) / a->per_wg);
+}
+
 int check_in_place(const char* fn, const char* out_name, const tdp_heads* in, const tdp_heads* out) {
   if (in->heads != out->heads)
     return fail(TDP_EINVAL, "%s: %s has %d heads, its input %d", fn, out_name, out->heads, in->heads);
@@ -444,7 +667,8 @@ int tdp_rope_apply(const tdp_rope* rope, const tdp_seqs* seqs, const float* pos,
   if (st == TDP_OK) st = check_pair(fn, "x", "y", x, y, seqs, rope->cfg.head_dim, dtype, &a.in[0], &a.out[0]);
   if (st != TDP_OK) return st;
   a.dir = inverse ? -1.0f : 1.0f;
-  return run(fn, Mode::kRope, a, dtype, (uint32_t)seq_blocks(*seqs, kWaves), stream);
+  const uint32_t grid = forward_grid(*seqs, &a);
+  return run(fn, Mode::kRope, a, dtype, grid, stream);
 }
 
 static int check_norm(const char* fn, float eps, const float* wq, const float* wk) {
@@ -468,7 +692,8 @@ int tdp_qk_norm_rope(const tdp_rope* rope, const tdp_seqs* seqs, const float* po
   a.w[1] = k_weight;
   a.eps = eps;
   a.dir = 1.0f;
-  return run(fn, Mode::kNorm, a, dtype, (uint32_t)seq_blocks(*seqs, kWaves), stream);
+  const uint32_t grid = forward_grid(*seqs, &a);
+  return run(fn, Mode::kNorm, a, dtype, grid, stream);
 }
 
 int tdp_qk_norm_rope_backward(const tdp_rope* rope, const tdp_seqs* seqs, const float* pos, const tdp_heads* q,
@@ -495,11 +720,12 @@ int tdp_qk_norm_rope_backward(const tdp_rope* rope, const tdp_seqs* seqs, const 
   a.w[1] = k_weight;
   a.eps = eps;
   a.parts = static_cast<float*>(workspace);
-  const int parts = norm_parts(*seqs);
-  st = run(fn, Mode::kBackward, a, dtype, (uint32_t)parts, stream);
+  const NormParts n = norm_parts(*seqs, q->heads, k->heads);
+  a.q_wgs = (uint32_t)n.q;
+  st = run(fn, Mode::kBackward, a, dtype, (uint32_t)(n.q + n.k), stream);
   if (st != TDP_OK || (!dq_weight && !dk_weight)) return st;
-  hipLaunchKernelGGL(norm_weights_kernel, dim3((2 * D + 15) / 16), dim3(kTok), 0,
-                     reinterpret_cast<hipStream_t>(stream), a.parts, parts, D, dq_weight, dk_weight);
+  hipLaunchKernelGGL(norm_weights_kernel, dim3(2 * ((D + 15) / 16)), dim3(kTok), 0,
+                     reinterpret_cast<hipStream_t>(stream), a.parts, n.q, n.q + n.k, D, dq_weight, dk_weight);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return fail(TDP_EHIP, "%s: kernel launch failed: %s", fn, hipGetErrorString(e));
   return TDP_OK;

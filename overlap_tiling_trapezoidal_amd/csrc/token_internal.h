@@ -46,13 +46,20 @@ inline int64_t seq_blocks(const tdp_seqs& s, int rows) {
   return (int64_t)s.num_seqs * ((s.max_rows + rows - 1) / rows);
 }
 
-// Partial sums of the norm weights' gradients: one row of 2 * head_dim floats
-// per workgroup of the backward launch, at most kNormParts workgroups.
-constexpr int kNormParts = 1024;
+// Partial sums of the norm weights' gradients: one row of head_dim floats per
+// workgroup of the backward launch.  A workgroup takes queries or keys; they
+// share at most kNormParts workgroups in proportion to their heads.
+constexpr int kNormParts = 768;
 constexpr int kNormRowsPerWg = 4;  // one row per wave
-inline int norm_parts(const tdp_seqs& s) {
+struct NormParts {
+  int q, k;
+};
+inline NormParts norm_parts(const tdp_seqs& s, int32_t q_heads, int32_t k_heads) {
   const int64_t b = seq_blocks(s, kNormRowsPerWg);
-  return (int)(b < kNormParts ? b : kNormParts);
+  int64_t q = (int64_t)kNormParts * q_heads / ((int64_t)q_heads + k_heads);
+  q = q < 1 ? 1 : (q > kNormParts - 1 ? kNormParts - 1 : q);
+  const int64_t k = kNormParts - q;
+  return {(int)(b < q ? b : q), (int)(b < k ? b : k)};
 }
 
 // Attention blocks.  The query axis of a key head is its group's query heads

@@ -127,7 +127,8 @@ void tdp_rope_destroy(tdp_rope* rope) { delete rope; }
 int64_t tdp_qk_norm_rope_workspace(const tdp_rope* rope, const tdp_seqs* seqs, int32_t q_heads, int32_t k_heads) {
   if (!rope || q_heads < 1 || k_heads < 1 || check_seqs("tdp_qk_norm_rope_workspace", "seqs", seqs, nullptr) != TDP_OK)
     return 0;
-  return align256((int64_t)norm_parts(*seqs) * 2 * rope->cfg.head_dim * 4);
+  const NormParts n = norm_parts(*seqs, q_heads, k_heads);
+  return align256((int64_t)(n.q + n.k) * rope->cfg.head_dim * 4);
 }
 
 int64_t tdp_attention_workspace(const tdp_seqs* q_seqs, const tdp_seqs* k_seqs, int32_t q_heads, int32_t k_heads,
