@@ -652,8 +652,9 @@ int tdp_qk_norm_rope_backward(const tdp_rope* rope, const tdp_seqs* seqs, const 
  *   s_ij = scale * q_i . k_j + key_bias_j,  out_i = sum_j softmax_j(s_ij) v_j
  * q.heads is a multiple of k.heads; query head h reads key head
  * h / (q.heads / k.heads).  key_bias (NULL: none) is one fp32 per key row
- * (k_seqs.total_rows), shared by all heads; a key whose bias is -infinity takes
- * no part, whatever its rows hold.  A query with no key left gives 0.  lse
+ * (k_seqs.total_rows), shared by all heads and at most 1e30; a key whose bias is
+ * -1e30 or less (-infinity, the lowest values of fp32 and bf16) takes no part,
+ * whatever its rows hold.  A query with no key left gives 0.  lse
  * (NULL: not wanted) receives log(sum_j exp(s_ij)) as fp32 (q.heads,
  * q_seqs.total_rows), -infinity where no key is left or the row is unused.
  * Scores, softmax and sums are fp32; for TDP_BF16 the softmax's weights are

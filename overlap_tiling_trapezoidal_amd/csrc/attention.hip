@@ -29,6 +29,8 @@
 #include <math.h>
 #include <stdint.h>
 
+#include <initializer_list>
+
 #include "token_device.h"
 
 namespace tdp {
@@ -36,6 +38,7 @@ namespace {
 
 constexpr int kTok = 256;
 constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
 // A bias at or below this (-infinity, the lowest values of fp32 and bf16) takes
 // the key out.
 constexpr float kBiasOut = -1.0e30f;
@@ -84,8 +87,11 @@ struct Tile {
   static constexpr int kRow = DP * Mat<T>::kBytes;  // bytes
   static constexpr int kChunks = kRow / 16;
   __device__ static inline int at(int r, int c) {
-    const int sw = kChunks == 8 ? ((r >> 1) & 3) << 1 : (r & 7) << 1;
-    return r * kRow + ((c ^ sw) << 4);
+    return r * kRow + (chunk_at(r, c) << 4);
+  }
+  // the chunk held by slot c of row r
+  __device__ static inline int chunk_at(int r, int c) {
+    return c ^ (kChunks == 8 ? ((r >> 1) & 3) << 1 : (r & 7) << 1);
   }
   // A[r][16 kk + 8h .. +7]
   __device__ static inline Frag row_frag(const char* lds, int r, int kk, int h) {
@@ -192,6 +198,56 @@ struct Stage {
   }
 };
 
+// Rows [r0, r0 + ROWS) of a head straight into a tile in LDS: a wave's 64 lanes
+// fill 64 neighbouring 16-byte slots, each lane fetching the chunk that the
+// swizzle puts there.  Rows at and past `len` and chunks past head_dim lie
+// outside the buffer descriptor's range, which makes them zero.
+template <int T, int DP, int ROWS>
+struct Direct {
+  typedef Tile<T, DP> L;
+  static constexpr int N = ROWS * L::kChunks / kTok;
+  uint32_t off[N];
+  __device__ inline void init(uint32_t row_bytes, int d_bytes) {
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+      const int i = threadIdx.x + n * kTok, r = i / L::kChunks, c = L::chunk_at(r, i % L::kChunks);
+      off[n] = c * 16 < d_bytes ? r * row_bytes + c * 16 : 0xfffffff0u;
+    }
+  }
+  __device__ inline void load(const char* head, int64_t row_bytes, int d_bytes, int r0, int len, int wave,
+                              char* lds) const {
+    const int left = len - r0 < ROWS ? len - r0 : ROWS;
+    const uint32_t span = left > 0 ? (uint32_t)(left - 1) * (uint32_t)row_bytes + d_bytes : 0;
+#ifdef __HIP_DEVICE_COMPILE__  // the descriptor type exists on the device only
+    const __amdgpu_buffer_rsrc_t rs = __builtin_amdgcn_make_buffer_rsrc(
+        const_cast<char*>(head + r0 * row_bytes), 0, __builtin_amdgcn_readfirstlane(span), 0x00020000);
+#pragma unroll
+    for (int n = 0; n < N; ++n)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (TDP_LDS void*)(lds + (n * kTok + wave * 64) * 16), 16, off[n], 0,
+                                               0, 0);
+#endif
+  }
+  // Clear what this lane has loaded of block b's keys that take no part: their
+  // rows may hold anything, and a weight of zero would not remove a NaN.
+  __device__ inline void clear(const float* bias, int b, int len, char* lds) const {
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+      const int i = threadIdx.x + n * kTok, j = b * ROWS + i / L::kChunks;
+      if (j < len && bias[j] <= kBiasOut) *reinterpret_cast<u32x4*>(lds + i * 16) = u32x4{0, 0, 0, 0};
+    }
+  }
+};
+// Block b's biases in powers of two, -infinity where a key takes no part or
+// lies past the end.
+__device__ inline void put_bias(const float* bias, int b, int len, float* bl) {
+  if (threadIdx.x < kAttnBlockK) {
+    const int j = b * kAttnBlockK + (int)threadIdx.x;
+    const float x = j < len ? bias[j] : -INFINITY;
+    bl[threadIdx.x] = x <= kBiasOut ? -INFINITY : x * kLog2e;
+  }
+}
+__device__ inline void wait_loads() { __builtin_amdgcn_s_waitcnt(0x0f70); }  // vmcnt(0)
+
 // The B operand of a product over head_dim, from global memory: element
 // 16 kk + 8h + e of the lane's row (null: zero).
 template <int T, int DP>
@@ -255,16 +311,37 @@ __device__ inline Place place(const AttnArgs& A, uint32_t item) {
   return p;
 }
 
-// Forward: 128 query entries of one key head per workgroup, 32 per wave; K and
-// V blocks of 64 keys pass through LDS.
+// A block's scores as the softmax takes them: with a bias in powers of two
+// (scaled and biased, the bias -infinity where a key takes no part), otherwise
+// raw, and -infinity for keys past the end.
+template <bool BIAS>
+__device__ inline void mask_scores(f32x16& st, const float* bl, float c, int j0, int len, int h) {
+#pragma unroll
+  for (int r = 0; r < 16; ++r) {
+    const int j = 8 * (r >> 2) + 4 * h + (r & 3);
+    if constexpr (BIAS)
+      st[r] = fmaf(st[r], c, bl[j]);
+    else if (j0 + j >= len)
+      st[r] = -INFINITY;
+  }
+}
+
+// Forward: 128 query entries of one key head per workgroup, 32 per wave.  K and
+// V blocks of 64 keys come through two LDS buffers each, loaded one step ahead.
+// A step multiplies block b's scores while the softmax and the product with V
+// of block b - 1 run, so that matrix and vector instructions of one wave have
+// each other to overlap with; two workgroups share a CU.
 template <int T, int DP, bool BIAS>
 __global__ __launch_bounds__(kTok, T == TDP_BF16 ? 2 : 1) void attn_forward_kernel(const AttnArgs A) {
   typedef Tile<T, DP> L;
   typedef typename Mat<T>::Frag Frag;
-  constexpr int KD = DP / 16, ND = DP / 32, KT = kAttnBlockK / 32;
-  __shared__ __align__(16) char kl[kAttnBlockK * L::kRow];
-  __shared__ __align__(16) char vl[kAttnBlockK * L::kRow];
-  __shared__ __align__(16) float bl[BIAS ? kAttnBlockK : 4];
+  constexpr int KD = DP / 16, ND = DP / 32, KT = kAttnBlockK / 32, kTile = kAttnBlockK * L::kRow;
+  // separate arrays, so that reads of one are not held back by loads into another
+  __shared__ __align__(16) char k0[kTile];
+  __shared__ __align__(16) char k1[kTile];
+  __shared__ __align__(16) char v0[kTile];
+  __shared__ __align__(16) char v1[kTile];
+  __shared__ __align__(16) float bl[2][BIAS ? kAttnBlockK : 4];
   const uint32_t item = xcd_item(A.tiles);
   if (item >= A.tiles) return;
   const Place pl = place(A, item);
@@ -272,7 +349,7 @@ __global__ __launch_bounds__(kTok, T == TDP_BF16 ? 2 : 1) void attn_forward_kern
   const int M = qr.cap * A.group, mlen = qr.len * A.group;
   const int m0 = pl.blk * kAttnBlockQ;
   if (m0 >= M) return;
-  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, h = lane >> 5;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, h = lane >> 5;
   const int m = m0 + wave * 32 + (lane & 31);
   const int row = (int)fastdiv((uint32_t)m, A.by_group), head = pl.hk * A.group + (m - row * A.group);
   constexpr int eb = Mat<T>::kBytes;
@@ -282,87 +359,44 @@ __global__ __launch_bounds__(kTok, T == TDP_BF16 ? 2 : 1) void attn_forward_kern
                                                head * A.q.head_stride)
                              : nullptr,
                     h, A.D, qf);
-  f32x16 o[ND];
+  f32x16 o[ND], st[KT];
 #pragma unroll
   for (int nd = 0; nd < ND; ++nd) o[nd] = zero16();
-  float mx = -INFINITY, l = 0.0f;
-  const float c = BIAS ? kLog2e : A.scale * kLog2e;
+  float mx = -INFINITY, l = 0.0f;  // mx in the scores' unit
+  const float c = A.scale * kLog2e, unit = BIAS ? 1.0f : c;
 
   const char* kb = A.k.data + eb * (seq_base(A.ks, A.k, pl.s, kr) + pl.hk * A.k.head_stride);
   const char* vb = A.v.data + eb * (seq_base(A.ks, A.v, pl.s, kr) + pl.hk * A.v.head_stride);
   const int64_t krow = eb * A.k.row_stride, vrow = eb * A.v.row_stride;
+  const int d_bytes = A.D * eb;
   const float* bias = BIAS ? A.bias + kr.row0 : nullptr;
   const int nb = (kr.len + kAttnBlockK - 1) / kAttnBlockK;
   const int per = (nb + A.splits - 1) / A.splits;
   const int b0 = pl.split * per;
-  int b1 = b0 + per < nb ? b0 + per : nb;
-  if (m0 >= mlen) b1 = b0;
+  const int b1 = m0 >= mlen ? b0 : (b0 + per < nb ? b0 + per : nb);
 
-  Stage<T, DP, kAttnBlockK> ks, vs;
-  float bs = 0.0f;
-  auto fetch = [&](int b) {
-    ks.load_rows(kb, krow, b * kAttnBlockK, kr.len, A.D * eb, bias);
-    vs.load_rows(vb, vrow, b * kAttnBlockK, kr.len, A.D * eb, bias);
-    if constexpr (BIAS) {
-      const int j = b * kAttnBlockK + (int)threadIdx.x;
-      if (threadIdx.x < kAttnBlockK) {
-        bs = j < kr.len ? bias[j] : -INFINITY;
-        bs = bs <= kBiasOut ? -INFINITY : bs;
-      }
-    }
-  };
-  if (b0 < b1) fetch(b0);
-  for (int b = b0; b < b1; ++b) {
-    __syncthreads();
-    ks.put(kl);
-    vs.put(vl);
-    if (BIAS && threadIdx.x < kAttnBlockK) bl[threadIdx.x] = bs;
-    __syncthreads();
-    if (b + 1 < b1) fetch(b + 1);
-
-    f32x16 st[KT];
+  Direct<T, DP, kAttnBlockK> kd, vd;
+  kd.init((uint32_t)krow, d_bytes);
+  vd.init((uint32_t)vrow, d_bytes);
+  auto scores = [&](const char* kl, f32x16* sn) __attribute__((always_inline)) {
 #pragma unroll
     for (int kt = 0; kt < KT; ++kt) {
-      st[kt] = zero16();
+      sn[kt] = zero16();
 #pragma unroll
       for (int kk = 0; kk < KD; ++kk)
-        st[kt] = Mat<T>::mma(L::row_frag(kl, kt * 32 + (lane & 31), kk, h), qf[kk], st[kt]);
+        sn[kt] = Mat<T>::mma(L::row_frag(kl, kt * 32 + (lane & 31), kk, h), qf[kk], sn[kt]);
     }
-    if constexpr (BIAS) {
-#pragma unroll
-      for (int kt = 0; kt < KT; ++kt)
-#pragma unroll
-        for (int r = 0; r < 16; ++r)
-          st[kt][r] = fmaf(st[kt][r], A.scale, bl[kt * 32 + 8 * (r >> 2) + 4 * h + (r & 3)]);
-    } else if ((b + 1) * kAttnBlockK > kr.len) {
-#pragma unroll
-      for (int kt = 0; kt < KT; ++kt)
-#pragma unroll
-        for (int r = 0; r < 16; ++r)
-          if (b * kAttnBlockK + kt * 32 + 8 * (r >> 2) + 4 * h + (r & 3) >= kr.len) st[kt][r] = -INFINITY;
-    }
-    float bm = -INFINITY;
-#pragma unroll
-    for (int kt = 0; kt < KT; ++kt)
-#pragma unroll
-      for (int r = 0; r < 16; ++r) bm = fmaxf(bm, st[kt][r]);
-    bm = other_half_max(bm);
-    if (__any((bm - mx) * c > kSlack)) {
-      const float nm = fmaxf(mx, bm);
-      const float f = mx == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f((mx - nm) * c);
-      mx = nm;
-      l *= f;
-#pragma unroll
-      for (int nd = 0; nd < ND; ++nd) o[nd] *= f;
-    }
+  };
+  // weights of the scores in st, their sums, and the product with V
+  auto values = [&](char* vl) __attribute__((always_inline)) {
     const float mu = mx == -INFINITY ? 0.0f : mx;
-    const float mc = mu * c;
+    const float mc = mu * unit;
 #pragma unroll
     for (int kt = 0; kt < KT; ++kt) {
       float p[16];
 #pragma unroll
       for (int r = 0; r < 16; ++r) {
-        p[r] = __builtin_amdgcn_exp2f(BIAS ? (st[kt][r] - mu) * c : fmaf(st[kt][r], c, -mc));
+        p[r] = __builtin_amdgcn_exp2f(BIAS ? st[kt][r] - mu : fmaf(st[kt][r], c, -mc));
         l += p[r];
       }
 #pragma unroll
@@ -372,6 +406,66 @@ __global__ __launch_bounds__(kTok, T == TDP_BF16 ? 2 : 1) void attn_forward_kern
         for (int nd = 0; nd < ND; ++nd)
           o[nd] = Mat<T>::mma(L::col_frag(vl, kt * 32 + 16 * s, nd * 32, lane), pf, o[nd]);
       }
+    }
+  };
+  // take block b's scores over: mask them, and move the maximum if they exceed it
+  auto take = [&](int b, f32x16* sn) __attribute__((always_inline)) {
+    if (BIAS || (b + 1) * kAttnBlockK > kr.len) {
+#pragma unroll
+      for (int kt = 0; kt < KT; ++kt)
+        mask_scores<BIAS>(sn[kt], bl[(b - b0) & 1] + kt * 32, c, b * kAttnBlockK + kt * 32, kr.len, h);
+    }
+    float bm = -INFINITY;
+#pragma unroll
+    for (int kt = 0; kt < KT; ++kt) {
+      st[kt] = sn[kt];
+#pragma unroll
+      for (int r = 0; r < 16; ++r) bm = fmaxf(bm, sn[kt][r]);
+    }
+    bm = other_half_max(bm);
+    if (__any((bm - mx) * unit > kSlack)) {
+      const float nm = fmaxf(mx, bm);
+      const float f = mx == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f((mx - nm) * unit);
+      mx = nm;
+      l *= f;
+#pragma unroll
+      for (int nd = 0; nd < ND; ++nd) o[nd] *= f;
+    }
+  };
+  // block b: its K in kc, the block before's V in vp; K of b + 1 goes to kn, V of b to vc
+  auto step = [&](int b, const char* kc, char* kn, char* vp, char* vc) __attribute__((always_inline)) {
+    if (b + 1 < b1) {
+      kd.load(kb, krow, d_bytes, (b + 1) * kAttnBlockK, kr.len, wave, kn);
+      if constexpr (BIAS) put_bias(bias, b + 1, kr.len, bl[(b + 1 - b0) & 1]);
+    }
+    vd.load(vb, vrow, d_bytes, b * kAttnBlockK, kr.len, wave, vc);
+    f32x16 sn[KT];
+    scores(kc, sn);
+    if (b > b0) values(vp);
+    take(b, sn);
+    wait_loads();
+    if constexpr (BIAS) {
+      vd.clear(bias, b, kr.len, vc);
+      if (b + 1 < b1) kd.clear(bias, b + 1, kr.len, kn);
+    }
+    __syncthreads();
+  };
+  if (b0 < b1) {
+    kd.load(kb, krow, d_bytes, b0 * kAttnBlockK, kr.len, wave, k0);
+    if constexpr (BIAS) put_bias(bias, b0, kr.len, bl[0]);
+    wait_loads();
+    if constexpr (BIAS) kd.clear(bias, b0, kr.len, k0);
+    __syncthreads();
+    int b = b0;
+    for (; b + 1 < b1; b += 2) {
+      step(b, k0, k1, v1, v0);
+      step(b + 1, k1, k0, v0, v1);
+    }
+    if (b < b1) {
+      step(b, k0, k1, v1, v0);
+      values(v0);
+    } else {
+      values(v1);
     }
   }
   l = other_half_sum(l);
@@ -383,16 +477,16 @@ __global__ __launch_bounds__(kTok, T == TDP_BF16 ? 2 : 1) void attn_forward_kern
     if (h == 0) *reinterpret_cast<f32x2*>(A.ws + n * DP + 2 * e) = f32x2{mx, l};
     return;
   }
-  const bool live = m < mlen;
+  const bool live = m < mlen && l != 0.0f;
   char* op = A.o.data + eb * (seq_base(A.qs, A.o, pl.s, qr) + row * A.o.row_stride + head * A.o.head_stride);
-  if (!live || l == 0.0f) {
+  if (!live) {
 #pragma unroll
     for (int nd = 0; nd < ND; ++nd) o[nd] = zero16();
   }
-  store_column<T, ND>(op, h, A.D, o, live && l != 0.0f ? 1.0f / l : 0.0f);
+  store_column<T, ND>(op, h, A.D, o, live ? 1.0f / l : 0.0f);
   if (A.lse && h == 0)
     A.lse[(int64_t)head * A.qs.total + qr.row0 + row] =
-        live && l != 0.0f ? mx * (BIAS ? 1.0f : A.scale) + logf(l) : -INFINITY;
+        live ? mx * (BIAS ? kLn2 : A.scale) + logf(l) : -INFINITY;
 }
 
 // Join the splits of one query entry per wave: weights 2^(c (m_i - max)).
@@ -463,17 +557,13 @@ __global__ __launch_bounds__(kTok) void attn_delta_kernel(const AttnArgs A, uint
   }
 }
 
-// A weight again from its score: exp(s - lse).  `nl` is -lse in the exponent's
-// unit (log2 without a bias, natural with one); -infinity for rows without keys.
+// A weight again from its score: exp(s - lse) in powers of two, nl = -lse log2(e),
+// -infinity for rows without keys.
 template <bool BIAS>
-__device__ inline float weight(float s, float scale, float c, float bias, float nl) {
-  if constexpr (BIAS) return __builtin_amdgcn_exp2f((fmaf(s, scale, bias) + nl) * kLog2e);
-  return __builtin_amdgcn_exp2f(fmaf(s, c, nl));
+__device__ inline float weight(float s, float c, float bias, float nl) {
+  return __builtin_amdgcn_exp2f(BIAS ? fmaf(s, c, bias) + nl : fmaf(s, c, nl));
 }
-template <bool BIAS>
-__device__ inline float neg_lse(float lse) {
-  return lse == -INFINITY ? -INFINITY : (BIAS ? -lse : -lse * kLog2e);
-}
+__device__ inline float neg_lse(float lse) { return lse == -INFINITY ? -INFINITY : -lse * kLog2e; }
 
 // dq: the forward's walk over the keys with a third product.
 template <int T, int DP, bool BIAS>
@@ -503,7 +593,7 @@ __global__ __launch_bounds__(kTok, T == TDP_BF16 && !(BIAS && DP == 128) ? 2 : 1
   load_frags<T, DP>(live ? A.dout.data + eb * (seq_base(A.qs, A.dout, pl.s, qr) + row * A.dout.row_stride +
                                                head * A.dout.head_stride) : nullptr, h, A.D, gf);
   const int64_t stat = (int64_t)head * A.qs.total + qr.row0 + row;
-  const float nl = live ? neg_lse<BIAS>(A.lse[stat]) : -INFINITY;
+  const float nl = live ? neg_lse(A.lse[stat]) : -INFINITY;
   const float delta = live ? A.delta[stat] : 0.0f;
   const float c = A.scale * kLog2e;
   f32x16 dq[ND];
@@ -518,14 +608,14 @@ __global__ __launch_bounds__(kTok, T == TDP_BF16 && !(BIAS && DP == 128) ? 2 : 1
 
   Stage<T, DP, kAttnBlockK> ks, vs;
   float bs = 0.0f;
-  auto fetch = [&](int b) {
+  auto fetch = [&](int b) __attribute__((always_inline)) {
     ks.load_rows(kb, krow, b * kAttnBlockK, kr.len, A.D * eb, bias);
     vs.load_rows(vb, vrow, b * kAttnBlockK, kr.len, A.D * eb, bias);
     if constexpr (BIAS) {
       const int j = b * kAttnBlockK + (int)threadIdx.x;
       if (threadIdx.x < kAttnBlockK) {
         bs = j < kr.len ? bias[j] : -INFINITY;
-        bs = bs <= kBiasOut ? -INFINITY : bs;
+        bs = bs <= kBiasOut ? -INFINITY : bs * kLog2e;
       }
     }
   };
@@ -550,7 +640,7 @@ __global__ __launch_bounds__(kTok, T == TDP_BF16 && !(BIAS && DP == 128) ? 2 : 1
       for (int r = 0; r < 16; ++r) {
         // keys past the end have zero rows in LDS: they add nothing to dq
         const float bi = BIAS ? bl[kt * 32 + 8 * (r >> 2) + 4 * h + (r & 3)] : 0.0f;
-        ds[r] = weight<BIAS>(st[r], A.scale, c, bi, nl) * (dp[r] - delta);
+        ds[r] = weight<BIAS>(st[r], c, bi, nl) * (dp[r] - delta);
       }
 #pragma unroll
       for (int s = 0; s < 2; ++s) {
@@ -596,7 +686,7 @@ __global__ __launch_bounds__(kTok, 1) void attn_dkv_kernel(const AttnArgs A) {
   bool live = j < kr.len;
   if constexpr (BIAS) {
     bi = live ? A.bias[kr.row0 + j] : -INFINITY;
-    bi = bi <= kBiasOut ? -INFINITY : bi;
+    bi = bi <= kBiasOut ? -INFINITY : bi * kLog2e;
     live = live && bi != -INFINITY;
   }
   Frag kf[KD], vf[KD];
@@ -614,7 +704,7 @@ __global__ __launch_bounds__(kTok, 1) void attn_dkv_kernel(const AttnArgs A) {
 
   Stage<T, DP, kBlockM> qs, gs;
   float nls = 0.0f, des = 0.0f;
-  auto fetch = [&](int m0) {
+  auto fetch = [&](int m0) __attribute__((always_inline)) {
     qs.load_entries(qb, eb * A.q.row_stride, eb * A.q.head_stride, A, m0, mlen, A.D * eb);
     gs.load_entries(gb, eb * A.dout.row_stride, eb * A.dout.head_stride, A, m0, mlen, A.D * eb);
     if (threadIdx.x < kBlockM) {
@@ -624,7 +714,7 @@ __global__ __launch_bounds__(kTok, 1) void attn_dkv_kernel(const AttnArgs A) {
       if (m < mlen) {
         const int row = (int)fastdiv((uint32_t)m, A.by_group);
         const int64_t stat = (hq0 + m - row * A.group) * A.qs.total + qr.row0 + row;
-        nls = neg_lse<BIAS>(A.lse[stat]);
+        nls = neg_lse(A.lse[stat]);
         des = A.delta[stat];
       }
     }
@@ -654,7 +744,7 @@ __global__ __launch_bounds__(kTok, 1) void attn_dkv_kernel(const AttnArgs A) {
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         const int r = 4 * r4 + e;
-        p[r] = weight<BIAS>(st[r], A.scale, c, bi, nl[e]);
+        p[r] = weight<BIAS>(st[r], c, bi, nl[e]);
         ds[r] = p[r] * (dp[r] - de[e]);
       }
     }
@@ -685,7 +775,7 @@ void launch_forward(const AttnArgs& A, hipStream_t st) {
   if (A.splits > 1) {
     const int64_t n = (int64_t)A.qs.S * A.k.heads * A.m_max;
     hipLaunchKernelGGL((attn_join_kernel<T, DP>), dim3((unsigned)((n + 3) / 4)), dim3(kTok), 0, st, A,
-                       BIAS ? kLog2e : A.scale * kLog2e, BIAS ? 1.0f : A.scale);
+                       BIAS ? 1.0f : A.scale * kLog2e, BIAS ? kLn2 : A.scale);
   }
 }
 
@@ -697,6 +787,14 @@ void launch_backward(AttnArgs A, uint32_t q_rows, uint32_t k_rows, hipStream_t s
   A.blocks = (k_rows + 127) / 128;
   A.tiles = A.blocks * (uint32_t)A.ks.S * (uint32_t)A.k.heads;
   hipLaunchKernelGGL((attn_dkv_kernel<T, DP, BIAS>), dim3(xcd_grid(A.tiles)), dim3(kTok), 0, st, A);
+}
+
+// The direct loads address a block of 64 rows with 32 bits.
+int check_row_strides(const char* fn, int32_t dtype, std::initializer_list<const tdp_heads*> ts) {
+  for (const tdp_heads* t : ts)
+    if (t->row_stride * dtype_bytes(dtype) > (1 << 25))
+      return fail(TDP_ESHAPE, "%s: a row stride of %lld elements exceeds 2^25 bytes", fn, (long long)t->row_stride);
+  return TDP_OK;
 }
 
 // Checks shared by both calls.
@@ -723,6 +821,8 @@ int begin(const char* fn, const tdp_seqs* q_seqs, const tdp_seqs* k_seqs, const 
                 fn, q->heads, k->heads, v->heads, out->heads);
   if ((reinterpret_cast<uintptr_t>(bias) | reinterpret_cast<uintptr_t>(lse)) & 3)
     return fail(TDP_EINVAL, "%s: key_bias and lse must be 4-byte aligned", fn);
+  st = check_row_strides(fn, dtype, {q, k, v});
+  if (st != TDP_OK) return st;
   A->bias = bias;
   A->lse = const_cast<float*>(lse);
   A->scale = scale;
