@@ -91,7 +91,7 @@ struct Tile {
   }
   // the chunk held by slot c of row r
   __device__ static inline int chunk_at(int r, int c) {
-    return c ^ (kChunks == 8 ? ((r >> 1) & 3) << 1 : (r & 7) << 1);
+    return c ^ (kChunks == 4 ? (r >> 2 & 1) << 1 : kChunks == 8 ? (r >> 1 & 3) << 1 : (r & 7) << 1);
   }
   // A[r][16 kk + 8h .. +7]
   __device__ static inline Frag row_frag(const char* lds, int r, int kk, int h) {
@@ -132,7 +132,7 @@ struct AttnArgs {
   HeadsDev q, k, v, o, dout, dq, dk, dv;
   const float* bias;
   float* lse;
-  float* delta;
+  f32x2* stats;  // backward, per query head and row: -lse log2(e) and delta
   float* ws;
   float scale;
   int32_t D, group, splits, m_max;  // m_max: query entries of the longest sequence
@@ -158,46 +158,6 @@ __device__ inline float other_half_sum(float x) {
   return __uint_as_float(r[0]) + __uint_as_float(r[1]);
 }
 
-// Rows [r0, r0 + ROWS) of a tensor through registers into LDS; rows at and past
-// `len`, and chunks past head_dim, are zero.
-template <int T, int DP, int ROWS>
-struct Stage {
-  typedef Tile<T, DP> L;
-  static constexpr int N = ROWS * L::kChunks / kTok;
-  u32x4 v[N];
-  // keys and values: base points at row 0 of the head
-  __device__ inline void load_rows(const char* base, int64_t row_bytes, int r0, int len, int d_bytes,
-                                   const float* bias) {
-#pragma unroll
-    for (int n = 0; n < N; ++n) {
-      const int i = threadIdx.x + n * kTok, r = r0 + i / L::kChunks, c = i % L::kChunks;
-      v[n] = u32x4{0, 0, 0, 0};
-      if (r < len && c * 16 < d_bytes && !(bias && bias[r] <= kBiasOut))
-        v[n] = *reinterpret_cast<const u32x4*>(base + r * row_bytes + c * 16);
-    }
-  }
-  // query entries m: row m / group, head m % group
-  __device__ inline void load_entries(const char* base, int64_t row_bytes, int64_t head_bytes, const AttnArgs& A,
-                                      int m0, int len, int d_bytes) {
-#pragma unroll
-    for (int n = 0; n < N; ++n) {
-      const int i = threadIdx.x + n * kTok, m = m0 + i / L::kChunks, c = i % L::kChunks;
-      v[n] = u32x4{0, 0, 0, 0};
-      if (m < len && c * 16 < d_bytes) {
-        const int row = (int)fastdiv((uint32_t)m, A.by_group);
-        v[n] = *reinterpret_cast<const u32x4*>(base + row * row_bytes + (m - row * A.group) * head_bytes + c * 16);
-      }
-    }
-  }
-  __device__ inline void put(char* lds) const {
-#pragma unroll
-    for (int n = 0; n < N; ++n) {
-      const int i = threadIdx.x + n * kTok;
-      *reinterpret_cast<u32x4*>(lds + L::at(i / L::kChunks, i % L::kChunks)) = v[n];
-    }
-  }
-};
-
 // Rows [r0, r0 + ROWS) of a head straight into a tile in LDS: a wave's 64 lanes
 // fill 64 neighbouring 16-byte slots, each lane fetching the chunk that the
 // swizzle puts there.  Rows at and past `len` and chunks past head_dim lie
@@ -205,7 +165,7 @@ struct Stage {
 template <int T, int DP, int ROWS>
 struct Direct {
   typedef Tile<T, DP> L;
-  static constexpr int N = ROWS * L::kChunks / kTok;
+  static constexpr int kSlots = ROWS * L::kChunks, N = (kSlots + kTok - 1) / kTok;
   uint32_t off[N];
   __device__ inline void init(uint32_t row_bytes, int d_bytes) {
 #pragma unroll
@@ -216,36 +176,57 @@ struct Direct {
   }
   __device__ inline void load(const char* head, int64_t row_bytes, int d_bytes, int r0, int len, int wave,
                               char* lds) const {
+#ifdef __HIP_DEVICE_COMPILE__  // the descriptor type exists on the device only
     const int left = len - r0 < ROWS ? len - r0 : ROWS;
     const uint32_t span = left > 0 ? (uint32_t)(left - 1) * (uint32_t)row_bytes + d_bytes : 0;
-#ifdef __HIP_DEVICE_COMPILE__  // the descriptor type exists on the device only
     const __amdgpu_buffer_rsrc_t rs = __builtin_amdgcn_make_buffer_rsrc(
         const_cast<char*>(head + r0 * row_bytes), 0, __builtin_amdgcn_readfirstlane(span), 0x00020000);
 #pragma unroll
     for (int n = 0; n < N; ++n)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (TDP_LDS void*)(lds + (n * kTok + wave * 64) * 16), 16, off[n], 0,
+      if (kSlots % kTok == 0 || n * kTok + wave * 64 < kSlots)
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (TDP_LDS void*)(lds + (n * kTok + wave * 64) * 16), 16, off[n], 0,
                                                0, 0);
 #endif
   }
-  // Clear what this lane has loaded of block b's keys that take no part: their
+  // Clear what this lane has loaded of a block's keys that take no part: their
   // rows may hold anything, and a weight of zero would not remove a NaN.
-  __device__ inline void clear(const float* bias, int b, int len, char* lds) const {
+  __device__ inline void clear(const float* bl, char* lds) const {
 #pragma unroll
     for (int n = 0; n < N; ++n) {
-      const int i = threadIdx.x + n * kTok, j = b * ROWS + i / L::kChunks;
-      if (j < len && bias[j] <= kBiasOut) *reinterpret_cast<u32x4*>(lds + i * 16) = u32x4{0, 0, 0, 0};
+      const int i = threadIdx.x + n * kTok;
+      if (i < kSlots && bl[i / L::kChunks] == -INFINITY) *reinterpret_cast<u32x4*>(lds + i * 16) = u32x4{0, 0, 0, 0};
     }
   }
 };
-// Block b's biases in powers of two, -infinity where a key takes no part or
-// lies past the end.
-__device__ inline void put_bias(const float* bias, int b, int len, float* bl) {
-  if (threadIdx.x < kAttnBlockK) {
-    const int j = b * kAttnBlockK + (int)threadIdx.x;
-    const float x = j < len ? bias[j] : -INFINITY;
-    bl[threadIdx.x] = x <= kBiasOut ? -INFINITY : x * kLog2e;
+// The biases of blocks of ROWS keys in powers of two, -infinity where a key takes
+// no part or lies past the end: four blocks in LDS, a fifth on its way in a
+// register, so that no step waits for the load that it issues.
+template <int ROWS>
+struct Biases {
+  const float* bias;
+  float* lds;
+  int len;
+  float next;
+  __device__ inline float get(int b) const {
+    const int j = b * ROWS + (int)threadIdx.x;
+    return threadIdx.x < ROWS && j < len ? bias[j] : -INFINITY;
   }
-}
+  __device__ inline void put(int b, float x) const {
+    if (threadIdx.x < ROWS) lds[(b & 3) * ROWS + threadIdx.x] = x <= kBiasOut ? -INFINITY : x * kLog2e;
+  }
+  __device__ inline const float* at(int b) const { return lds + (b & 3) * ROWS; }
+  // before the first block: it and the one after it
+  __device__ inline void start(int b) {
+    put(b, get(b));
+    put(b + 1, get(b + 1));
+    next = get(b + 2);
+  }
+  // in block b's step: what comes two blocks later is stored, three blocks later requested
+  __device__ inline void advance(int b) {
+    put(b + 2, next);
+    next = get(b + 3);
+  }
+};
 __device__ inline void wait_loads() { __builtin_amdgcn_s_waitcnt(0x0f70); }  // vmcnt(0)
 
 // The B operand of a product over head_dim, from global memory: element
@@ -341,7 +322,7 @@ __global__ __launch_bounds__(kTok, T == TDP_BF16 ? 2 : 1) void attn_forward_kern
   __shared__ __align__(16) char k1[kTile];
   __shared__ __align__(16) char v0[kTile];
   __shared__ __align__(16) char v1[kTile];
-  __shared__ __align__(16) float bl[2][BIAS ? kAttnBlockK : 4];
+  __shared__ __align__(16) float bl[BIAS ? 4 * kAttnBlockK : 4];
   const uint32_t item = xcd_item(A.tiles);
   if (item >= A.tiles) return;
   const Place pl = place(A, item);
@@ -369,7 +350,7 @@ __global__ __launch_bounds__(kTok, T == TDP_BF16 ? 2 : 1) void attn_forward_kern
   const char* vb = A.v.data + eb * (seq_base(A.ks, A.v, pl.s, kr) + pl.hk * A.v.head_stride);
   const int64_t krow = eb * A.k.row_stride, vrow = eb * A.v.row_stride;
   const int d_bytes = A.D * eb;
-  const float* bias = BIAS ? A.bias + kr.row0 : nullptr;
+  Biases<kAttnBlockK> biases = {BIAS ? A.bias + kr.row0 : nullptr, bl, kr.len, 0.0f};
   const int nb = (kr.len + kAttnBlockK - 1) / kAttnBlockK;
   const int per = (nb + A.splits - 1) / A.splits;
   const int b0 = pl.split * per;
@@ -413,7 +394,7 @@ __global__ __launch_bounds__(kTok, T == TDP_BF16 ? 2 : 1) void attn_forward_kern
     if (BIAS || (b + 1) * kAttnBlockK > kr.len) {
 #pragma unroll
       for (int kt = 0; kt < KT; ++kt)
-        mask_scores<BIAS>(sn[kt], bl[(b - b0) & 1] + kt * 32, c, b * kAttnBlockK + kt * 32, kr.len, h);
+        mask_scores<BIAS>(sn[kt], biases.at(b) + kt * 32, c, b * kAttnBlockK + kt * 32, kr.len, h);
     }
     float bm = -INFINITY;
 #pragma unroll
@@ -434,10 +415,8 @@ __global__ __launch_bounds__(kTok, T == TDP_BF16 ? 2 : 1) void attn_forward_kern
   };
   // block b: its K in kc, the block before's V in vp; K of b + 1 goes to kn, V of b to vc
   auto step = [&](int b, const char* kc, char* kn, char* vp, char* vc) __attribute__((always_inline)) {
-    if (b + 1 < b1) {
-      kd.load(kb, krow, d_bytes, (b + 1) * kAttnBlockK, kr.len, wave, kn);
-      if constexpr (BIAS) put_bias(bias, b + 1, kr.len, bl[(b + 1 - b0) & 1]);
-    }
+    if constexpr (BIAS) biases.advance(b);
+    if (b + 1 < b1) kd.load(kb, krow, d_bytes, (b + 1) * kAttnBlockK, kr.len, wave, kn);
     vd.load(vb, vrow, d_bytes, b * kAttnBlockK, kr.len, wave, vc);
     f32x16 sn[KT];
     scores(kc, sn);
@@ -445,17 +424,20 @@ __global__ __launch_bounds__(kTok, T == TDP_BF16 ? 2 : 1) void attn_forward_kern
     take(b, sn);
     wait_loads();
     if constexpr (BIAS) {
-      vd.clear(bias, b, kr.len, vc);
-      if (b + 1 < b1) kd.clear(bias, b + 1, kr.len, kn);
+      vd.clear(biases.at(b), vc);
+      if (b + 1 < b1) kd.clear(biases.at(b + 1), kn);
     }
     __syncthreads();
   };
   if (b0 < b1) {
     kd.load(kb, krow, d_bytes, b0 * kAttnBlockK, kr.len, wave, k0);
-    if constexpr (BIAS) put_bias(bias, b0, kr.len, bl[0]);
+    if constexpr (BIAS) biases.start(b0);
     wait_loads();
-    if constexpr (BIAS) kd.clear(bias, b0, kr.len, k0);
     __syncthreads();
+    if constexpr (BIAS) {
+      kd.clear(biases.at(b0), k0);
+      __syncthreads();
+    }
     int b = b0;
     for (; b + 1 < b1; b += 2) {
       step(b, k0, k1, v1, v0);
@@ -489,39 +471,53 @@ __global__ __launch_bounds__(kTok, T == TDP_BF16 ? 2 : 1) void attn_forward_kern
         live ? mx * (BIAS ? kLn2 : A.scale) + logf(l) : -INFINITY;
 }
 
-// Join the splits of one query entry per wave: weights 2^(c (m_i - max)).
+// Join the splits of one query entry per workgroup: weights 2^(c (m_i - max)).
+// The waves take the splits in turn, two to four of them in flight each.
 template <int T, int DP>
 __global__ __launch_bounds__(kTok) void attn_join_kernel(const AttnArgs A, float c, float unit) {
+  constexpr int E = DP < 64 ? 1 : DP / 64;
+  __shared__ float part[4][E * 64];
+  __shared__ f32x2 ml[kAttnMaxSplits];
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
-  const int64_t g = (int64_t)blockIdx.x * 4 + wave;  // ((s, hk), m)
+  const int64_t g = blockIdx.x;  // ((s, hk), m)
   const int64_t n1 = (int64_t)A.qs.S * A.k.heads * A.m_max;
-  if (g >= n1) return;
   const int64_t sh = g / A.m_max;
   const int m = (int)(g - sh * A.m_max), s = (int)(sh / A.k.heads), hk = (int)(sh - (int64_t)s * A.k.heads);
   const SeqRows qr = seq_rows(A.qs, s);
   if (m >= qr.cap * A.group) return;
-  const f32x2* ml = reinterpret_cast<const f32x2*>(A.ws + n1 * A.splits * DP);
-  float mx = -INFINITY;
-  for (int i = 0; i < A.splits; ++i) mx = fmaxf(mx, ml[i * n1 + g].x);
-  float l = 0.0f, x[DP / 64];
+  if ((int)threadIdx.x < A.splits)
+    ml[threadIdx.x] = reinterpret_cast<const f32x2*>(A.ws + n1 * A.splits * DP)[threadIdx.x * n1 + g];
+  __syncthreads();
+  float mx = -INFINITY, l = 0.0f;
+  for (int i = 0; i < A.splits; ++i) mx = fmaxf(mx, ml[i].x);
+  float x[E];
 #pragma unroll
-  for (int e = 0; e < DP / 64; ++e) x[e] = 0.0f;
-  for (int i = 0; i < A.splits; ++i) {
-    const f32x2 v = ml[i * n1 + g];
-    if (v.y == 0.0f) continue;  // no key in this part
-    const float f = v.x == mx ? 1.0f : __builtin_amdgcn_exp2f((v.x - mx) * c);
-    l = fmaf(v.y, f, l);
+  for (int e = 0; e < E; ++e) x[e] = 0.0f;
+#pragma unroll 4
+  for (int i = wave; i < A.splits; i += 4) {
+    // a part without a key holds zeros and -infinity; without any maximum all
+    // weights are one (scores that are not numbers come through)
+    const float f = mx == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f((ml[i].x - mx) * c);
 #pragma unroll
-    for (int e = 0; e < DP / 64; ++e) x[e] = fmaf(A.ws[(i * n1 + g) * DP + e * 64 + lane], f, x[e]);
+    for (int e = 0; e < E; ++e) {
+      const int d = e * 64 + lane;
+      if (d < DP) x[e] = fmaf(A.ws[(i * n1 + g) * DP + d], f, x[e]);
+    }
   }
+  for (int i = 0; i < A.splits; ++i)
+    l = fmaf(ml[i].y, mx == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f((ml[i].x - mx) * c), l);
+#pragma unroll
+  for (int e = 0; e < E; ++e) part[wave][e * 64 + lane] = x[e];
+  __syncthreads();
+  if (wave) return;
   const int row = (int)fastdiv((uint32_t)m, A.by_group), head = hk * A.group + (m - row * A.group);
   const bool live = row < qr.len && l != 0.0f;
   char* op = A.o.data + Mat<T>::kBytes * (seq_base(A.qs, A.o, s, qr) + row * A.o.row_stride + head * A.o.head_stride);
 #pragma unroll
-  for (int e = 0; e < DP / 64; ++e) {
+  for (int e = 0; e < E; ++e) {
     const int d = e * 64 + lane;
     if (d >= A.D) continue;
-    const float y = live ? x[e] / l : 0.0f;
+    const float y = live ? ((part[0][d] + part[1][d]) + (part[2][d] + part[3][d])) / l : 0.0f;
     if constexpr (T == TDP_BF16)
       reinterpret_cast<__bf16*>(op)[d] = (__bf16)y;
     else
@@ -529,32 +525,6 @@ __global__ __launch_bounds__(kTok) void attn_join_kernel(const AttnArgs A, float
   }
   if (A.lse && lane == 0)
     A.lse[(int64_t)head * A.qs.total + qr.row0 + row] = live ? mx * unit + logf(l) : -INFINITY;
-}
-
-// delta = dout . out per query head and row: 16 lanes per head, a wave per row.
-template <int T>
-__global__ __launch_bounds__(kTok) void attn_delta_kernel(const AttnArgs A, uint32_t blocks) {
-  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
-  const int s = blockIdx.x / blocks;
-  const int i = (blockIdx.x - s * blocks) * 4 + wave;
-  const SeqRows qr = seq_rows(A.qs, s);
-  if (i >= qr.len) return;
-  const int chunk = lane & 15;
-  const int64_t gb = seq_base(A.qs, A.dout, s, qr) + i * A.dout.row_stride + chunk * 8;
-  const int64_t ob = seq_base(A.qs, A.o, s, qr) + i * A.o.row_stride + chunk * 8;
-  for (int hd = lane >> 4; hd < A.q.heads; hd += 4) {
-    float v = 0.0f;
-    if (chunk * 8 < A.D) {
-      float a[8], b[8];
-      load8<T>(A.dout.data, gb + hd * A.dout.head_stride, a);
-      load8<T>(A.o.data, ob + hd * A.o.head_stride, b);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) v = fmaf(a[e], b[e], v);
-    }
-#pragma unroll
-    for (int x = 1; x < 16; x <<= 1) v += __shfl_xor(v, x);
-    if (chunk == 0) A.delta[(int64_t)hd * A.qs.total + qr.row0 + i] = v;
-  }
 }
 
 // A weight again from its score: exp(s - lse) in powers of two, nl = -lse log2(e),
@@ -565,15 +535,24 @@ __device__ inline float weight(float s, float c, float bias, float nl) {
 }
 __device__ inline float neg_lse(float lse) { return lse == -INFINITY ? -INFINITY : -lse * kLog2e; }
 
-// dq: the forward's walk over the keys with a third product.
+// dq: the forward's walk over the keys with a third product.  128 query entries
+// per workgroup, 32 per wave; blocks of 32 keys pass through three LDS buffers:
+// one being loaded, one whose scores are multiplied, and the one before it,
+// whose weights become ds and meet K again.  delta = dout . out is made here, by
+// the lanes that hold dout, and left with lse for the dk and dv kernel.
+constexpr int kDqKeys = 32;
 template <int T, int DP, bool BIAS>
-__global__ __launch_bounds__(kTok, T == TDP_BF16 && !(BIAS && DP == 128) ? 2 : 1) void attn_dq_kernel(const AttnArgs A) {
+__global__ __launch_bounds__(kTok, T == TDP_BF16 ? 2 : 1) void attn_dq_kernel(const AttnArgs A) {
   typedef Tile<T, DP> L;
   typedef typename Mat<T>::Frag Frag;
-  constexpr int KD = DP / 16, ND = DP / 32, KT = kAttnBlockK / 32;
-  __shared__ __align__(16) char kl[kAttnBlockK * L::kRow];
-  __shared__ __align__(16) char vl[kAttnBlockK * L::kRow];
-  __shared__ __align__(16) float bl[BIAS ? kAttnBlockK : 4];
+  constexpr int KD = DP / 16, ND = DP / 32, kTile = kDqKeys * L::kRow;
+  __shared__ __align__(16) char k0[kTile];
+  __shared__ __align__(16) char k1[kTile];
+  __shared__ __align__(16) char k2[kTile];
+  __shared__ __align__(16) char v0[kTile];
+  __shared__ __align__(16) char v1[kTile];
+  __shared__ __align__(16) char v2[kTile];
+  __shared__ __align__(16) float bl[BIAS ? 4 * kDqKeys : 4];
   const uint32_t item = xcd_item(A.tiles);
   if (item >= A.tiles) return;
   const Place pl = place(A, item);
@@ -581,74 +560,110 @@ __global__ __launch_bounds__(kTok, T == TDP_BF16 && !(BIAS && DP == 128) ? 2 : 1
   const int M = qr.cap * A.group, mlen = qr.len * A.group;
   const int m0 = pl.blk * kAttnBlockQ;
   if (m0 >= M) return;
-  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, h = lane >> 5;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, h = lane >> 5;
   const int m = m0 + wave * 32 + (lane & 31);
   const bool live = m < mlen;
   const int row = (int)fastdiv((uint32_t)m, A.by_group), head = pl.hk * A.group + (m - row * A.group);
   constexpr int eb = Mat<T>::kBytes;
 
+  auto at = [&](const HeadsDev& t) __attribute__((always_inline)) {
+    return live ? t.data + eb * (seq_base(A.qs, t, pl.s, qr) + row * t.row_stride + head * t.head_stride) : nullptr;
+  };
   Frag qf[KD], gf[KD];
-  load_frags<T, DP>(live ? A.q.data + eb * (seq_base(A.qs, A.q, pl.s, qr) + row * A.q.row_stride +
-                                            head * A.q.head_stride) : nullptr, h, A.D, qf);
-  load_frags<T, DP>(live ? A.dout.data + eb * (seq_base(A.qs, A.dout, pl.s, qr) + row * A.dout.row_stride +
-                                               head * A.dout.head_stride) : nullptr, h, A.D, gf);
+  float delta = 0.0f;
+  {
+    Frag of[KD];
+    load_frags<T, DP>(at(A.dout), h, A.D, gf);
+    load_frags<T, DP>(at(A.o), h, A.D, of);
+#pragma unroll
+    for (int kk = 0; kk < KD; ++kk)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) delta = fmaf((float)gf[kk][e], (float)of[kk][e], delta);
+    delta = other_half_sum(delta);
+  }
+  load_frags<T, DP>(at(A.q), h, A.D, qf);
   const int64_t stat = (int64_t)head * A.qs.total + qr.row0 + row;
   const float nl = live ? neg_lse(A.lse[stat]) : -INFINITY;
-  const float delta = live ? A.delta[stat] : 0.0f;
+  if (live && h == 0) A.stats[stat] = f32x2{nl, delta};
   const float c = A.scale * kLog2e;
-  f32x16 dq[ND];
+  f32x16 dq[ND], st = zero16(), dp = zero16();
 #pragma unroll
   for (int nd = 0; nd < ND; ++nd) dq[nd] = zero16();
 
   const char* kb = A.k.data + eb * (seq_base(A.ks, A.k, pl.s, kr) + pl.hk * A.k.head_stride);
   const char* vb = A.v.data + eb * (seq_base(A.ks, A.v, pl.s, kr) + pl.hk * A.v.head_stride);
   const int64_t krow = eb * A.k.row_stride, vrow = eb * A.v.row_stride;
-  const float* bias = BIAS ? A.bias + kr.row0 : nullptr;
-  const int nb = m0 >= mlen ? 0 : (kr.len + kAttnBlockK - 1) / kAttnBlockK;
+  const int d_bytes = A.D * eb;
+  Biases<kDqKeys> biases = {BIAS ? A.bias + kr.row0 : nullptr, bl, kr.len, 0.0f};
+  const int nb = m0 >= mlen ? 0 : (kr.len + kDqKeys - 1) / kDqKeys;
 
-  Stage<T, DP, kAttnBlockK> ks, vs;
-  float bs = 0.0f;
-  auto fetch = [&](int b) __attribute__((always_inline)) {
-    ks.load_rows(kb, krow, b * kAttnBlockK, kr.len, A.D * eb, bias);
-    vs.load_rows(vb, vrow, b * kAttnBlockK, kr.len, A.D * eb, bias);
-    if constexpr (BIAS) {
-      const int j = b * kAttnBlockK + (int)threadIdx.x;
-      if (threadIdx.x < kAttnBlockK) {
-        bs = j < kr.len ? bias[j] : -INFINITY;
-        bs = bs <= kBiasOut ? -INFINITY : bs * kLog2e;
-      }
+  Direct<T, DP, kDqKeys> kd, vd;
+  kd.init((uint32_t)krow, d_bytes);
+  vd.init((uint32_t)vrow, d_bytes);
+  auto load = [&](int b, char* kn, char* vn) __attribute__((always_inline)) {
+    kd.load(kb, krow, d_bytes, b * kDqKeys, kr.len, wave, kn);
+    vd.load(vb, vrow, d_bytes, b * kDqKeys, kr.len, wave, vn);
+  };
+  // the block whose scores are in st and dp: ds, and its product with K
+  auto values = [&](int b, char* kl) __attribute__((always_inline)) {
+    float ds[16];
+#pragma unroll
+    for (int r = 0; r < 16; ++r)
+      ds[r] = weight<BIAS>(st[r], c, BIAS ? biases.at(b)[8 * (r >> 2) + 4 * h + (r & 3)] : 0.0f, nl) * (dp[r] - delta);
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+      const Frag f = Mat<T>::pack(ds + 8 * s);
+#pragma unroll
+      for (int nd = 0; nd < ND; ++nd) dq[nd] = Mat<T>::mma(L::col_frag(kl, 16 * s, nd * 32, lane), f, dq[nd]);
     }
   };
-  if (nb) fetch(0);
-  for (int b = 0; b < nb; ++b) {
+  auto step = [&](int b, const char* kc, char* kp, char* kn, const char* vc, char* vn) __attribute__((always_inline)) {
+    if constexpr (BIAS) biases.advance(b);
+    if (b + 1 < nb) load(b + 1, kn, vn);
+    f32x16 sn = zero16(), dn = zero16();
+#pragma unroll
+    for (int kk = 0; kk < KD; ++kk) {
+      sn = Mat<T>::mma(L::row_frag(kc, lane & 31, kk, h), qf[kk], sn);
+      dn = Mat<T>::mma(L::row_frag(vc, lane & 31, kk, h), gf[kk], dn);
+    }
+    if (b > 0) values(b - 1, kp);
+    st = sn;
+    dp = dn;
+    if (!BIAS && (b + 1) * kDqKeys > kr.len) mask_scores<false>(st, nullptr, c, b * kDqKeys, kr.len, h);
+    wait_loads();
+    if constexpr (BIAS) {
+      if (b + 1 < nb) {
+        kd.clear(biases.at(b + 1), kn);
+        vd.clear(biases.at(b + 1), vn);
+      }
+    }
     __syncthreads();
-    ks.put(kl);
-    vs.put(vl);
-    if (BIAS && threadIdx.x < kAttnBlockK) bl[threadIdx.x] = bs;
+  };
+  if (nb) {
+    load(0, k0, v0);
+    if constexpr (BIAS) biases.start(0);
+    wait_loads();
     __syncthreads();
-    if (b + 1 < nb) fetch(b + 1);
-#pragma unroll
-    for (int kt = 0; kt < KT; ++kt) {
-      f32x16 st = zero16(), dp = zero16();
-#pragma unroll
-      for (int kk = 0; kk < KD; ++kk) {
-        st = Mat<T>::mma(L::row_frag(kl, kt * 32 + (lane & 31), kk, h), qf[kk], st);
-        dp = Mat<T>::mma(L::row_frag(vl, kt * 32 + (lane & 31), kk, h), gf[kk], dp);
-      }
-      float ds[16];
-#pragma unroll
-      for (int r = 0; r < 16; ++r) {
-        // keys past the end have zero rows in LDS: they add nothing to dq
-        const float bi = BIAS ? bl[kt * 32 + 8 * (r >> 2) + 4 * h + (r & 3)] : 0.0f;
-        ds[r] = weight<BIAS>(st[r], c, bi, nl) * (dp[r] - delta);
-      }
-#pragma unroll
-      for (int s = 0; s < 2; ++s) {
-        const Frag f = Mat<T>::pack(ds + 8 * s);
-#pragma unroll
-        for (int nd = 0; nd < ND; ++nd)
-          dq[nd] = Mat<T>::mma(L::col_frag(kl, kt * 32 + 16 * s, nd * 32, lane), f, dq[nd]);
-      }
+    if constexpr (BIAS) {
+      kd.clear(biases.at(0), k0);
+      vd.clear(biases.at(0), v0);
+      __syncthreads();
+    }
+    int b = 0;
+    for (; b + 2 < nb; b += 3) {
+      step(b, k0, k2, k1, v0, v1);
+      step(b + 1, k1, k0, k2, v1, v2);
+      step(b + 2, k2, k1, k0, v2, v0);
+    }
+    if (b + 1 < nb) {
+      step(b, k0, k2, k1, v0, v1);
+      step(b + 1, k1, k0, k2, v1, v2);
+      values(b + 1, k1);
+    } else if (b < nb) {
+      step(b, k0, k2, k1, v0, v1);
+      values(b, k0);
+    } else {
+      values(b - 1, k2);
     }
   }
   if (m >= M) return;
@@ -660,26 +675,44 @@ __global__ __launch_bounds__(kTok, T == TDP_BF16 && !(BIAS && DP == 128) ? 2 : 1
   store_column<T, ND>(op, h, A.D, dq, A.scale);
 }
 
+// The (-lse log2(e), delta) pairs of up to 32 rows into LDS, by the first wave.
+__device__ inline void load_stats(const f32x2* from, int left, int wave, int lane, float* lds) {
+#ifdef __HIP_DEVICE_COMPILE__
+  if (wave) return;
+  const uint32_t span = left < 32 ? left * 8 : 256;
+  const __amdgpu_buffer_rsrc_t rs = __builtin_amdgcn_make_buffer_rsrc(
+      const_cast<f32x2*>(from), 0, __builtin_amdgcn_readfirstlane(span), 0x00020000);
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (TDP_LDS void*)lds, 4, lane * 4, 0, 0, 0);
+#endif
+}
+
 // dk and dv: 128 keys of one key head per workgroup, 32 per wave, their K and V
-// in registers; blocks of 32 query entries (all heads of the group) pass
-// through LDS with their dout, lse and delta.
-constexpr int kBlockM = 32;
+// in registers.  Blocks of 32 rows of Q and dout, one query head of the group
+// after another, pass through three LDS buffers as the keys do in dq, with
+// their lse and delta.  Where few key blocks meet many rows, the blocks are
+// split over workgroups, whose sums are joined by attn_sum_kernel.
+constexpr int kDkvRows = 32;
 template <int T, int DP, bool BIAS>
-__global__ __launch_bounds__(kTok, 1) void attn_dkv_kernel(const AttnArgs A) {
+__global__ __launch_bounds__(kTok, T == TDP_BF16 && DP <= 64 ? 2 : 1) void attn_dkv_kernel(const AttnArgs A) {
   typedef Tile<T, DP> L;
   typedef typename Mat<T>::Frag Frag;
-  constexpr int KD = DP / 16, ND = DP / 32;
-  __shared__ __align__(16) char ql[kBlockM * L::kRow];
-  __shared__ __align__(16) char gl[kBlockM * L::kRow];
-  __shared__ __align__(16) float nll[kBlockM], del[kBlockM];
+  constexpr int KD = DP / 16, ND = DP / 32, kTile = kDkvRows * L::kRow;
+  __shared__ __align__(16) char q0[kTile];
+  __shared__ __align__(16) char q1[kTile];
+  __shared__ __align__(16) char q2[kTile];
+  __shared__ __align__(16) char g0[kTile];
+  __shared__ __align__(16) char g1[kTile];
+  __shared__ __align__(16) char g2[kTile];
+  __shared__ __align__(16) float s0[2 * kDkvRows];
+  __shared__ __align__(16) float s1[2 * kDkvRows];
+  __shared__ __align__(16) float s2[2 * kDkvRows];
   const uint32_t item = xcd_item(A.tiles);
   if (item >= A.tiles) return;
   const Place pl = place(A, item);
   const SeqRows qr = seq_rows(A.qs, pl.s), kr = seq_rows(A.ks, pl.s);
-  const int j0 = pl.blk * 128;
+  const int j0 = pl.blk * kAttnBlockQ;
   if (j0 >= kr.cap) return;
-  const int mlen = j0 < kr.len ? qr.len * A.group : 0;
-  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, h = lane >> 5;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, h = lane >> 5;
   const int j = j0 + wave * 32 + (lane & 31);
   constexpr int eb = Mat<T>::kBytes;
   float bi = 0.0f;
@@ -694,60 +727,52 @@ __global__ __launch_bounds__(kTok, 1) void attn_dkv_kernel(const AttnArgs A) {
                                             pl.hk * A.k.head_stride) : nullptr, h, A.D, kf);
   load_frags<T, DP>(live ? A.v.data + eb * (seq_base(A.ks, A.v, pl.s, kr) + j * A.v.row_stride +
                                             pl.hk * A.v.head_stride) : nullptr, h, A.D, vf);
-  f32x16 dk[ND], dv[ND];
+  f32x16 dk[ND], dv[ND], st = zero16(), dp = zero16();
 #pragma unroll
   for (int nd = 0; nd < ND; ++nd) dk[nd] = dv[nd] = zero16();
   const float c = A.scale * kLog2e;
-  const int64_t hq0 = (int64_t)pl.hk * A.group;
-  const char* qb = A.q.data + eb * (seq_base(A.qs, A.q, pl.s, qr) + hq0 * A.q.head_stride);
-  const char* gb = A.dout.data + eb * (seq_base(A.qs, A.dout, pl.s, qr) + hq0 * A.dout.head_stride);
+  const int d_bytes = A.D * eb;
+  const int64_t qrow = eb * A.q.row_stride, grow = eb * A.dout.row_stride;
 
-  Stage<T, DP, kBlockM> qs, gs;
-  float nls = 0.0f, des = 0.0f;
-  auto fetch = [&](int m0) __attribute__((always_inline)) {
-    qs.load_entries(qb, eb * A.q.row_stride, eb * A.q.head_stride, A, m0, mlen, A.D * eb);
-    gs.load_entries(gb, eb * A.dout.row_stride, eb * A.dout.head_stride, A, m0, mlen, A.D * eb);
-    if (threadIdx.x < kBlockM) {
-      const int m = m0 + (int)threadIdx.x;
-      nls = -INFINITY;
-      des = 0.0f;
-      if (m < mlen) {
-        const int row = (int)fastdiv((uint32_t)m, A.by_group);
-        const int64_t stat = (hq0 + m - row * A.group) * A.qs.total + qr.row0 + row;
-        nls = neg_lse(A.lse[stat]);
-        des = A.delta[stat];
-      }
+  // blocks of all heads of the group in a row: block b is rows
+  // (b mod per_head) * 32 of head b / per_head
+  const int per_head = (qr.len + kDkvRows - 1) / kDkvRows;
+  const int all = j0 < kr.len ? per_head * A.group : 0;
+  const int per = (all + A.splits - 1) / A.splits;
+  const int b0 = pl.split * per, b1 = b0 + per < all ? b0 + per : all;
+
+  Direct<T, DP, kDkvRows> qd, gd;
+  qd.init((uint32_t)qrow, d_bytes);
+  gd.init((uint32_t)grow, d_bytes);
+  int gh = 0, gr = 0;  // head and row of the next block to load
+  int left = 0, left_next = 0;  // rows of the block multiplied last, of the one after it
+  auto load = [&](char* qn, char* gn, float* sn) __attribute__((always_inline)) {
+    const int64_t head = (int64_t)pl.hk * A.group + gh;
+    qd.load(A.q.data + eb * (seq_base(A.qs, A.q, pl.s, qr) + head * A.q.head_stride), qrow, d_bytes, gr, qr.len, wave,
+            qn);
+    gd.load(A.dout.data + eb * (seq_base(A.qs, A.dout, pl.s, qr) + head * A.dout.head_stride), grow, d_bytes, gr,
+            qr.len, wave, gn);
+    load_stats(A.stats + head * A.qs.total + qr.row0 + gr, qr.len - gr, wave, lane, sn);
+    gr += kDkvRows;
+    if (gr >= qr.len) {
+      gr = 0;
+      ++gh;
     }
   };
-  if (mlen) fetch(0);
-  for (int m0 = 0; m0 < mlen; m0 += kBlockM) {
-    __syncthreads();
-    qs.put(ql);
-    gs.put(gl);
-    if (threadIdx.x < kBlockM) {
-      nll[threadIdx.x] = nls;
-      del[threadIdx.x] = des;
-    }
-    __syncthreads();
-    if (m0 + kBlockM < mlen) fetch(m0 + kBlockM);
-    f32x16 st = zero16(), dp = zero16();
-#pragma unroll
-    for (int kk = 0; kk < KD; ++kk) {
-      st = Mat<T>::mma(L::row_frag(ql, lane & 31, kk, h), kf[kk], st);
-      dp = Mat<T>::mma(L::row_frag(gl, lane & 31, kk, h), vf[kk], dp);
-    }
+  auto values = [&](char* ql, char* gl, const float* sl, int rows) __attribute__((always_inline)) {
     float p[16], ds[16];
 #pragma unroll
-    for (int r4 = 0; r4 < 4; ++r4) {
-      const f32x4 nl = *reinterpret_cast<const f32x4*>(nll + 8 * r4 + 4 * h);
-      const f32x4 de = *reinterpret_cast<const f32x4*>(del + 8 * r4 + 4 * h);
+    for (int r4 = 0; r4 < 4; ++r4)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int r = 4 * r4 + e;
-        p[r] = weight<BIAS>(st[r], c, bi, nl[e]);
-        ds[r] = p[r] * (dp[r] - de[e]);
+      for (int e = 0; e < 4; e += 2) {
+        const int r = 4 * r4 + e, i = 8 * r4 + 4 * h + e;
+        const f32x4 x = *reinterpret_cast<const f32x4*>(sl + 2 * i);
+        // rows past the end have zeros for Q and dout
+        p[r] = weight<BIAS>(st[r], c, bi, i < rows ? x[0] : -INFINITY);
+        p[r + 1] = weight<BIAS>(st[r + 1], c, bi, i + 1 < rows ? x[2] : -INFINITY);
+        ds[r] = p[r] * (dp[r] - x[1]);
+        ds[r + 1] = p[r + 1] * (dp[r + 1] - x[3]);
       }
-    }
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
       const Frag pf = Mat<T>::pack(p + 8 * s), df = Mat<T>::pack(ds + 8 * s);
@@ -757,11 +782,62 @@ __global__ __launch_bounds__(kTok, 1) void attn_dkv_kernel(const AttnArgs A) {
         dk[nd] = Mat<T>::mma(L::col_frag(ql, 16 * s, nd * 32, lane), df, dk[nd]);
       }
     }
+  };
+  auto step = [&](int b, const char* qc, const char* gc, char* qp, char* gp, const float* sp, char* qn, char* gn,
+                  float* sn) __attribute__((always_inline)) {
+    const int rows = left_next;
+    if (b + 1 < b1) {
+      left_next = qr.len - gr;
+      load(qn, gn, sn);
+    }
+    f32x16 sc = zero16(), dc = zero16();
+#pragma unroll
+    for (int kk = 0; kk < KD; ++kk) {
+      sc = Mat<T>::mma(L::row_frag(qc, lane & 31, kk, h), kf[kk], sc);
+      dc = Mat<T>::mma(L::row_frag(gc, lane & 31, kk, h), vf[kk], dc);
+    }
+    if (b > b0) values(qp, gp, sp, left);
+    st = sc;
+    dp = dc;
+    left = rows;
+    wait_loads();
+    __syncthreads();
+  };
+  if (b0 < b1) {
+    gh = b0 / per_head;
+    gr = (b0 - gh * per_head) * kDkvRows;
+    left_next = qr.len - gr;
+    load(q0, g0, s0);
+    wait_loads();
+    __syncthreads();
+    int b = b0;
+    for (; b + 2 < b1; b += 3) {
+      step(b, q0, g0, q2, g2, s2, q1, g1, s1);
+      step(b + 1, q1, g1, q0, g0, s0, q2, g2, s2);
+      step(b + 2, q2, g2, q1, g1, s1, q0, g0, s0);
+    }
+    if (b + 1 < b1) {
+      step(b, q0, g0, q2, g2, s2, q1, g1, s1);
+      step(b + 1, q1, g1, q0, g0, s0, q2, g2, s2);
+      values(q1, g1, s1, left);
+    } else if (b < b1) {
+      step(b, q0, g0, q2, g2, s2, q1, g1, s1);
+      values(q0, g0, s0, left);
+    } else {
+      values(q2, g2, s2, left);
+    }
   }
   if (j >= kr.cap) return;
   if (!live) {
 #pragma unroll
     for (int nd = 0; nd < ND; ++nd) dk[nd] = dv[nd] = zero16();
+  }
+  if (A.splits > 1) {
+    const int64_t e = (((int64_t)pl.split * A.ks.S + pl.s) * A.k.heads + pl.hk) * A.ks.max_rows + j;
+    const int64_t n = (int64_t)A.splits * A.ks.S * A.k.heads * A.ks.max_rows;
+    store_column<TDP_F32, ND>(reinterpret_cast<char*>(A.ws + e * DP), h, DP, dk, A.scale);
+    store_column<TDP_F32, ND>(reinterpret_cast<char*>(A.ws + (n + e) * DP), h, DP, dv, 1.0f);
+    return;
   }
   store_column<T, ND>(A.dk.data + eb * (seq_base(A.ks, A.dk, pl.s, kr) + j * A.dk.row_stride +
                                         pl.hk * A.dk.head_stride), h, A.D, dk, A.scale);
@@ -769,24 +845,51 @@ __global__ __launch_bounds__(kTok, 1) void attn_dkv_kernel(const AttnArgs A) {
                                         pl.hk * A.dv.head_stride), h, A.D, dv, 1.0f);
 }
 
-template <int T, int DP, bool BIAS>
-void launch_forward(const AttnArgs& A, hipStream_t st) {
-  hipLaunchKernelGGL((attn_forward_kernel<T, DP, BIAS>), dim3(xcd_grid(A.tiles)), dim3(kTok), 0, st, A);
-  if (A.splits > 1) {
-    const int64_t n = (int64_t)A.qs.S * A.k.heads * A.m_max;
-    hipLaunchKernelGGL((attn_join_kernel<T, DP>), dim3((unsigned)((n + 3) / 4)), dim3(kTok), 0, st, A,
-                       BIAS ? 1.0f : A.scale * kLog2e, BIAS ? kLn2 : A.scale);
+// Sum the parts of dk and dv in order: a thread per eight elements of a key.
+template <int T, int DP>
+__global__ __launch_bounds__(kTok) void attn_sum_kernel(const AttnArgs A) {
+  constexpr int kPer = DP / 8;
+  const int64_t n1 = (int64_t)A.ks.S * A.k.heads * A.ks.max_rows;
+  const int64_t t = (int64_t)blockIdx.x * kTok + threadIdx.x;
+  const int64_t which = t / (n1 * kPer);  // dk, then dv
+  if (which > 1) return;
+  const int64_t e = t / kPer - which * n1;
+  const int d = (int)(t % kPer) * 8;
+  const int64_t sh = e / A.ks.max_rows;
+  const int j = (int)(e - sh * A.ks.max_rows), s = (int)(sh / A.k.heads), hk = (int)(sh - (int64_t)s * A.k.heads);
+  const SeqRows kr = seq_rows(A.ks, s);
+  if (j >= kr.cap || d >= A.D) return;
+  float x[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+#pragma unroll 4
+  for (int i = 0; i < A.splits; ++i) {
+    float y[8];
+    load8<TDP_F32>(reinterpret_cast<const char*>(A.ws), ((which * A.splits + i) * n1 + e) * DP + d, y);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) x[k] += y[k];
   }
+  const HeadsDev& out = which ? A.dv : A.dk;
+  store8<T>(out.data, seq_base(A.ks, out, s, kr) + j * out.row_stride + hk * out.head_stride + d, x);
 }
 
 template <int T, int DP, bool BIAS>
-void launch_backward(AttnArgs A, uint32_t q_rows, uint32_t k_rows, hipStream_t st) {
-  const uint32_t db = (q_rows + 3) / 4;
-  hipLaunchKernelGGL((attn_delta_kernel<T>), dim3(A.qs.S * db), dim3(kTok), 0, st, A, db);
+void launch_forward(const AttnArgs& A, hipStream_t st) {
+  hipLaunchKernelGGL((attn_forward_kernel<T, DP, BIAS>), dim3(xcd_grid(A.tiles)), dim3(kTok), 0, st, A);
+  if (A.splits > 1)
+    hipLaunchKernelGGL((attn_join_kernel<T, DP>), dim3((unsigned)(A.qs.S * A.k.heads * A.m_max)), dim3(kTok), 0, st, A,
+                       BIAS ? 1.0f : A.scale * kLog2e, BIAS ? kLn2 : A.scale);
+}
+
+template <int T, int DP, bool BIAS>
+void launch_backward(AttnArgs A, int splits, hipStream_t st) {
   hipLaunchKernelGGL((attn_dq_kernel<T, DP, BIAS>), dim3(xcd_grid(A.tiles)), dim3(kTok), 0, st, A);
-  A.blocks = (k_rows + 127) / 128;
-  A.tiles = A.blocks * (uint32_t)A.ks.S * (uint32_t)A.k.heads;
+  A.blocks = (uint32_t)((A.ks.max_rows + kAttnBlockQ - 1) / kAttnBlockQ);
+  A.splits = splits;
+  A.tiles = A.blocks * (uint32_t)A.ks.S * (uint32_t)A.k.heads * splits;
   hipLaunchKernelGGL((attn_dkv_kernel<T, DP, BIAS>), dim3(xcd_grid(A.tiles)), dim3(kTok), 0, st, A);
+  if (splits > 1) {
+    const int64_t n = (int64_t)A.ks.S * A.k.heads * A.ks.max_rows * 2 * (DP / 8);
+    hipLaunchKernelGGL((attn_sum_kernel<T, DP>), dim3((unsigned)((n + kTok - 1) / kTok)), dim3(kTok), 0, st, A);
+  }
 }
 
 // The direct loads address a block of 64 rows with 32 bits.
@@ -848,25 +951,24 @@ int check_items(const char* fn, int64_t workgroups) {
 
 using namespace tdp;
 
-#define TDP_ATTN_DISPATCH(call)                                     \
-  do {                                                              \
-    if (dtype == TDP_BF16) {                                        \
-      if (head_dim <= 64) {                                         \
-        if (key_bias) call(TDP_BF16, 64, true);                     \
-        else call(TDP_BF16, 64, false);                             \
-      } else {                                                      \
-        if (key_bias) call(TDP_BF16, 128, true);                    \
-        else call(TDP_BF16, 128, false);                            \
-      }                                                             \
-    } else {                                                        \
-      if (head_dim <= 64) {                                         \
-        if (key_bias) call(TDP_F32, 64, true);                      \
-        else call(TDP_F32, 64, false);                              \
-      } else {                                                      \
-        if (key_bias) call(TDP_F32, 128, true);                     \
-        else call(TDP_F32, 128, false);                             \
-      }                                                             \
-    }                                                               \
+#define TDP_ATTN_DIMS(call, T)                    \
+  do {                                            \
+    const int dp = attention_padded_dim(head_dim); \
+    if (dp == 32) {                               \
+      if (key_bias) call(T, 32, true);            \
+      else call(T, 32, false);                    \
+    } else if (dp == 64) {                        \
+      if (key_bias) call(T, 64, true);            \
+      else call(T, 64, false);                    \
+    } else {                                      \
+      if (key_bias) call(T, 128, true);           \
+      else call(T, 128, false);                   \
+    }                                             \
+  } while (0)
+#define TDP_ATTN_DISPATCH(call)                    \
+  do {                                             \
+    if (dtype == TDP_BF16) TDP_ATTN_DIMS(call, TDP_BF16); \
+    else TDP_ATTN_DIMS(call, TDP_F32);             \
   } while (0)
 
 extern "C" {
@@ -883,7 +985,7 @@ int tdp_attention(const tdp_seqs* q_seqs, const tdp_seqs* k_seqs, const tdp_head
     return fail(TDP_EINVAL, "%s: workspace must be a 16-byte aligned device pointer (tdp_attention_workspace)", fn);
   A.ws = static_cast<float*>(workspace);
   const int64_t tiles = (int64_t)A.blocks * q_seqs->num_seqs * k->heads * A.splits;
-  const int64_t join = A.splits > 1 ? ((int64_t)q_seqs->num_seqs * k->heads * A.m_max + 3) / 4 : 0;
+  const int64_t join = A.splits > 1 ? (int64_t)q_seqs->num_seqs * k->heads * A.m_max : 0;
   st = check_items(fn, tiles > join ? tiles : join);
   if (st != TDP_OK) return st;
   A.tiles = (uint32_t)tiles;
@@ -913,15 +1015,19 @@ int tdp_attention_backward(const tdp_seqs* q_seqs, const tdp_seqs* k_seqs, const
   if (!lse) return fail(TDP_EINVAL, "%s: null lse", fn);
   if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 15))
     return fail(TDP_EINVAL, "%s: workspace must be a 16-byte aligned device pointer", fn);
-  A.delta = static_cast<float*>(workspace);
-  const int64_t sh = (int64_t)q_seqs->num_seqs * k->heads;
-  const int64_t qt = A.blocks * sh, kt = ((int64_t)k_seqs->max_rows + 127) / 128 * sh;
-  const int64_t db = seq_blocks(*q_seqs, 4);
-  st = check_items(fn, qt > kt ? (qt > db ? qt : db) : (kt > db ? kt : db));
+  st = check_row_strides(fn, dtype, {dout});
+  if (st != TDP_OK) return st;
+  A.stats = static_cast<f32x2*>(workspace);
+  A.ws = reinterpret_cast<float*>(static_cast<char*>(workspace) + stats_bytes(*q_seqs, q->heads));
+  const int splits = dkv_splits(*q_seqs, *k_seqs, q->heads, k->heads);
+  const int64_t qt = A.blocks * ((int64_t)q_seqs->num_seqs * k->heads);
+  const int64_t kt = dkv_blocks(*k_seqs, k->heads) * splits;
+  const int64_t sum = splits > 1 ? ((int64_t)k_seqs->num_seqs * k->heads * k_seqs->max_rows * 32 + kTok - 1) / kTok : 0;
+  st = check_items(fn, qt > kt ? (qt > sum ? qt : sum) : (kt > sum ? kt : sum));
   if (st != TDP_OK) return st;
   A.tiles = (uint32_t)qt;
   hipStream_t hs = reinterpret_cast<hipStream_t>(stream);
-#define CALL(T, DP, B) launch_backward<T, DP, B>(A, (uint32_t)q_seqs->max_rows, (uint32_t)k_seqs->max_rows, hs)
+#define CALL(T, DP, B) launch_backward<T, DP, B>(A, splits, hs)
   TDP_ATTN_DISPATCH(CALL);
 #undef CALL
   const hipError_t e = hipGetLastError();

@@ -87,7 +87,7 @@ inline int attention_splits(const tdp_seqs& q, const tdp_seqs& k, int32_t q_head
   if (n > kAttnMaxSplits) n = kAttnMaxSplits;
   return n < 2 ? 1 : (int)n;
 }
-inline int attention_padded_dim(int32_t head_dim) { return head_dim <= 64 ? 64 : 128; }
+inline int attention_padded_dim(int32_t head_dim) { return head_dim <= 32 ? 32 : head_dim <= 64 ? 64 : 128; }
 // Per split, sequence, key head and query entry: the unscaled sum (padded
 // head_dim floats), then the maximum and the sum of weights (2 floats).
 inline int64_t attention_workspace(const tdp_seqs& q, const tdp_seqs& k, int32_t q_heads, int32_t k_heads,
@@ -95,6 +95,33 @@ inline int64_t attention_workspace(const tdp_seqs& q, const tdp_seqs& k, int32_t
   const int n = attention_splits(q, k, q_heads, k_heads);
   if (n == 1) return 0;
   return align256((int64_t)n * q.num_seqs * q_heads * q.max_rows * (attention_padded_dim(head_dim) + 2) * 4);
+}
+
+// Row splits of the dk and dv kernel, for the same reason: parts of at least
+// kDkvSplitRows query rows, until about kAttnSplitBlocks workgroups run.
+constexpr int kDkvSplitRows = 512;
+inline int64_t dkv_blocks(const tdp_seqs& k, int32_t k_heads) {
+  return (int64_t)k.num_seqs * k_heads * ((k.max_rows + kAttnBlockQ - 1) / kAttnBlockQ);
+}
+inline int dkv_splits(const tdp_seqs& q, const tdp_seqs& k, int32_t q_heads, int32_t k_heads) {
+  const int64_t blocks = dkv_blocks(k, k_heads);
+  if (blocks * 2 > kAttnSplitBlocks) return 1;
+  int64_t n = kAttnSplitBlocks / blocks;
+  const int64_t by_rows = (int64_t)q.max_rows * (q_heads / k_heads) / kDkvSplitRows;
+  if (n > by_rows) n = by_rows;
+  if (n > kAttnMaxSplits) n = kAttnMaxSplits;
+  return n < 2 ? 1 : (int)n;
+}
+// The backward's workspace: lse and delta, two floats per (query head, row), then per
+// split, sequence, key head and key padded rows of dk, and the same of dv.
+inline int64_t stats_bytes(const tdp_seqs& q, int32_t q_heads) {
+  return align256((int64_t)q_heads * q.total_rows * 8);
+}
+inline int64_t backward_workspace(const tdp_seqs& q, const tdp_seqs& k, int32_t q_heads, int32_t k_heads,
+                                  int32_t head_dim) {
+  const int n = dkv_splits(q, k, q_heads, k_heads);
+  const int64_t parts = n == 1 ? 0 : (int64_t)n * k.num_seqs * k_heads * k.max_rows * attention_padded_dim(head_dim) * 8;
+  return stats_bytes(q, q_heads) + align256(parts);
 }
 
 }  // namespace tdp

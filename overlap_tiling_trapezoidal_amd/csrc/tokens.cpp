@@ -146,8 +146,7 @@ int64_t tdp_attention_backward_workspace(const tdp_seqs* q_seqs, const tdp_seqs*
       check_seqs("tdp_attention_backward_workspace", "k_seqs", k_seqs, nullptr) != TDP_OK || q_heads < 1 ||
       k_heads < 1 || q_heads % k_heads != 0 || head_dim < 8)
     return 0;
-  // delta, one float per (query head, row)
-  return align256((int64_t)q_heads * q_seqs->total_rows * 4);
+  return backward_workspace(*q_seqs, *k_seqs, q_heads, k_heads, head_dim);
 }
 
 }  // extern "C"
