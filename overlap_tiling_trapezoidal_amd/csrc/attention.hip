@@ -162,11 +162,14 @@ __device__ inline float other_half_sum(float x) {
 // fill 64 neighbouring 16-byte slots, each lane fetching the chunk that the
 // swizzle puts there.  Rows at and past `len` and chunks past head_dim lie
 // outside the buffer descriptor's range, which makes them zero.
-template <int T, int DP, int ROWS>
+// With EXACT a row past the end is zero whatever the strides; without, rows of
+// stride 0 repeat the last one there, which the scores' mask takes out.
+template <int T, int DP, int ROWS, bool EXACT = false>
 struct Direct {
   typedef Tile<T, DP> L;
   static constexpr int kSlots = ROWS * L::kChunks, N = (kSlots + kTok - 1) / kTok;
   uint32_t off[N];
+  __device__ static inline int row_of(int n) { return threadIdx.x / L::kChunks + n * (kTok / L::kChunks); }
   __device__ inline void init(uint32_t row_bytes, int d_bytes) {
 #pragma unroll
     for (int n = 0; n < N; ++n) {
@@ -184,8 +187,8 @@ struct Direct {
 #pragma unroll
     for (int n = 0; n < N; ++n)
       if (kSlots % kTok == 0 || n * kTok + wave * 64 < kSlots)
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (TDP_LDS void*)(lds + (n * kTok + wave * 64) * 16), 16, off[n], 0,
-                                               0, 0);
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (TDP_LDS void*)(lds + (n * kTok + wave * 64) * 16), 16,
+                                                 EXACT && row_of(n) >= left ? 0xfffffff0u : off[n], 0, 0, 0);
 #endif
   }
   // Clear what this lane has loaded of a block's keys that take no part: their
@@ -675,23 +678,28 @@ __global__ __launch_bounds__(kTok, T == TDP_BF16 ? 2 : 1) void attn_dq_kernel(co
   store_column<T, ND>(op, h, A.D, dq, A.scale);
 }
 
-// The (-lse log2(e), delta) pairs of up to 32 rows into LDS, by the first wave.
+// The (-lse log2(e), delta) pairs of up to 64 rows into LDS, by the first wave.
 __device__ inline void load_stats(const f32x2* from, int left, int wave, int lane, float* lds) {
 #ifdef __HIP_DEVICE_COMPILE__
   if (wave) return;
-  const uint32_t span = left < 32 ? left * 8 : 256;
+  const uint32_t span = left < 64 ? left * 8 : 512;
   const __amdgpu_buffer_rsrc_t rs = __builtin_amdgcn_make_buffer_rsrc(
       const_cast<f32x2*>(from), 0, __builtin_amdgcn_readfirstlane(span), 0x00020000);
   __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (TDP_LDS void*)lds, 4, lane * 4, 0, 0, 0);
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (TDP_LDS void*)(lds + 64), 4, 256 + lane * 4, 0, 0, 0);
 #endif
 }
 
 // dk and dv: 128 keys of one key head per workgroup, 32 per wave, their K and V
-// in registers.  Blocks of 32 rows of Q and dout, one query head of the group
-// after another, pass through three LDS buffers as the keys do in dq, with
-// their lse and delta.  Where few key blocks meet many rows, the blocks are
-// split over workgroups, whose sums are joined by attn_sum_kernel.
-constexpr int kDkvRows = 32;
+// in registers.  Blocks of 64 rows of Q and dout, one query head of the group
+// after another, pass through three LDS buffers with their lse and delta, one
+// being loaded.  They are taken by halves: while one half's scores are
+// multiplied, the half before it becomes weights and meets dout and Q again.
+// fp32 tiles, twice the size under matrix instructions of a sixteenth the rate,
+// take two buffers and one half after the other.  Where few key blocks meet many
+// rows, the blocks are split over workgroups, whose sums are joined by
+// attn_sum_kernel.
+constexpr int kDkvRows = 64;
 template <int T, int DP, bool BIAS>
 __global__ __launch_bounds__(kTok, T == TDP_BF16 && DP <= 64 ? 2 : 1) void attn_dkv_kernel(const AttnArgs A) {
   typedef Tile<T, DP> L;
@@ -699,10 +707,11 @@ __global__ __launch_bounds__(kTok, T == TDP_BF16 && DP <= 64 ? 2 : 1) void attn_
   constexpr int KD = DP / 16, ND = DP / 32, kTile = kDkvRows * L::kRow;
   __shared__ __align__(16) char q0[kTile];
   __shared__ __align__(16) char q1[kTile];
-  __shared__ __align__(16) char q2[kTile];
   __shared__ __align__(16) char g0[kTile];
   __shared__ __align__(16) char g1[kTile];
-  __shared__ __align__(16) char g2[kTile];
+  constexpr bool kAhead = T == TDP_BF16;
+  __shared__ __align__(16) char q2[kAhead ? kTile : 16];
+  __shared__ __align__(16) char g2[kAhead ? kTile : 16];
   __shared__ __align__(16) float s0[2 * kDkvRows];
   __shared__ __align__(16) float s1[2 * kDkvRows];
   __shared__ __align__(16) float s2[2 * kDkvRows];
@@ -727,7 +736,7 @@ __global__ __launch_bounds__(kTok, T == TDP_BF16 && DP <= 64 ? 2 : 1) void attn_
                                             pl.hk * A.k.head_stride) : nullptr, h, A.D, kf);
   load_frags<T, DP>(live ? A.v.data + eb * (seq_base(A.ks, A.v, pl.s, kr) + j * A.v.row_stride +
                                             pl.hk * A.v.head_stride) : nullptr, h, A.D, vf);
-  f32x16 dk[ND], dv[ND], st = zero16(), dp = zero16();
+  f32x16 dk[ND], dv[ND], sa, da, sb, db;  // scores and dout . v of first and second halves
 #pragma unroll
   for (int nd = 0; nd < ND; ++nd) dk[nd] = dv[nd] = zero16();
   const float c = A.scale * kLog2e;
@@ -735,96 +744,177 @@ __global__ __launch_bounds__(kTok, T == TDP_BF16 && DP <= 64 ? 2 : 1) void attn_
   const int64_t qrow = eb * A.q.row_stride, grow = eb * A.dout.row_stride;
 
   // blocks of all heads of the group in a row: block b is rows
-  // (b mod per_head) * 32 of head b / per_head
+  // (b mod per_head) * 64 of head b / per_head
   const int per_head = (qr.len + kDkvRows - 1) / kDkvRows;
   const int all = j0 < kr.len ? per_head * A.group : 0;
   const int per = (all + A.splits - 1) / A.splits;
   const int b0 = pl.split * per, b1 = b0 + per < all ? b0 + per : all;
 
-  Direct<T, DP, kDkvRows> qd, gd;
+  Direct<T, DP, kDkvRows, true> qd, gd;
   qd.init((uint32_t)qrow, d_bytes);
   gd.init((uint32_t)grow, d_bytes);
-  int gh = 0, gr = 0;  // head and row of the next block to load
-  int left = 0, left_next = 0;  // rows of the block multiplied last, of the one after it
+  const char* qhead = A.q.data + eb * seq_base(A.qs, A.q, pl.s, qr);
+  const char* ghead = A.dout.data + eb * seq_base(A.qs, A.dout, pl.s, qr);
+  const f32x2* shead = A.stats + qr.row0;
+  int gr = 0;  // row of the next block to load
+  // the buffers' rows from the block's first to the end of its head
+  int left = 0, left_next = 0;
+  auto seek = [&](int head, int row) __attribute__((always_inline)) {
+    qhead += eb * head * A.q.head_stride;
+    ghead += eb * head * A.dout.head_stride;
+    shead += head * A.qs.total;
+    gr = row;
+  };
   auto load = [&](char* qn, char* gn, float* sn) __attribute__((always_inline)) {
-    const int64_t head = (int64_t)pl.hk * A.group + gh;
-    qd.load(A.q.data + eb * (seq_base(A.qs, A.q, pl.s, qr) + head * A.q.head_stride), qrow, d_bytes, gr, qr.len, wave,
-            qn);
-    gd.load(A.dout.data + eb * (seq_base(A.qs, A.dout, pl.s, qr) + head * A.dout.head_stride), grow, d_bytes, gr,
-            qr.len, wave, gn);
-    load_stats(A.stats + head * A.qs.total + qr.row0 + gr, qr.len - gr, wave, lane, sn);
+    left_next = qr.len - gr;
+    qd.load(qhead, qrow, d_bytes, gr, qr.len, wave, qn);
+    gd.load(ghead, grow, d_bytes, gr, qr.len, wave, gn);
+    load_stats(shead + gr, left_next, wave, lane, sn);
     gr += kDkvRows;
-    if (gr >= qr.len) {
-      gr = 0;
-      ++gh;
-    }
+    if (gr >= qr.len) seek(1, 0);
   };
-  auto values = [&](char* ql, char* gl, const float* sl, int rows) __attribute__((always_inline)) {
-    float p[16], ds[16];
-#pragma unroll
-    for (int r4 = 0; r4 < 4; ++r4)
-#pragma unroll
-      for (int e = 0; e < 4; e += 2) {
-        const int r = 4 * r4 + e, i = 8 * r4 + 4 * h + e;
-        const f32x4 x = *reinterpret_cast<const f32x4*>(sl + 2 * i);
-        // rows past the end have zeros for Q and dout
-        p[r] = weight<BIAS>(st[r], c, bi, i < rows ? x[0] : -INFINITY);
-        p[r + 1] = weight<BIAS>(st[r + 1], c, bi, i + 1 < rows ? x[2] : -INFINITY);
-        ds[r] = p[r] * (dp[r] - x[1]);
-        ds[r + 1] = p[r + 1] * (dp[r + 1] - x[3]);
-      }
-#pragma unroll
-    for (int s = 0; s < 2; ++s) {
-      const Frag pf = Mat<T>::pack(p + 8 * s), df = Mat<T>::pack(ds + 8 * s);
-#pragma unroll
-      for (int nd = 0; nd < ND; ++nd) {
-        dv[nd] = Mat<T>::mma(L::col_frag(gl, 16 * s, nd * 32, lane), pf, dv[nd]);
-        dk[nd] = Mat<T>::mma(L::col_frag(ql, 16 * s, nd * 32, lane), df, dk[nd]);
-      }
-    }
-  };
-  auto step = [&](int b, const char* qc, const char* gc, char* qp, char* gp, const float* sp, char* qn, char* gn,
-                  float* sn) __attribute__((always_inline)) {
-    const int rows = left_next;
-    if (b + 1 < b1) {
-      left_next = qr.len - gr;
-      load(qn, gn, sn);
-    }
-    f32x16 sc = zero16(), dc = zero16();
+  // What a half needs from LDS is read ahead of its products, behind barriers
+  // for the compiler's scheduler: left to itself it reads each operand right
+  // before its product, which with one wave per SIMD exposes every read
+  // (4 x 2240 rows, 16 heads of 128: 582 us without, 469 with).
+  auto scores = [&](char* ql, char* gl, int r0, f32x16& st, f32x16& dp) __attribute__((always_inline)) {
+    st = dp = zero16();
+    Frag a[KD], b[KD];
 #pragma unroll
     for (int kk = 0; kk < KD; ++kk) {
-      sc = Mat<T>::mma(L::row_frag(qc, lane & 31, kk, h), kf[kk], sc);
-      dc = Mat<T>::mma(L::row_frag(gc, lane & 31, kk, h), vf[kk], dc);
+      a[kk] = L::row_frag(ql, r0 + (lane & 31), kk, h);
+      b[kk] = L::row_frag(gl, r0 + (lane & 31), kk, h);
     }
-    if (b > b0) values(qp, gp, sp, left);
-    st = sc;
-    dp = dc;
+    if (kAhead) __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int kk = 0; kk < KD; ++kk) {
+      st = Mat<T>::mma(a[kk], kf[kk], st);
+      dp = Mat<T>::mma(b[kk], vf[kk], dp);
+    }
+  };
+  auto statistics = [&](const float* sl, int r0, f32x4* x) __attribute__((always_inline)) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      x[i] = *reinterpret_cast<const f32x4*>(sl + 2 * (r0 + 8 * (i >> 1) + 4 * h + 2 * (i & 1)));
+  };
+  auto values = [&](char* ql, char* gl, const f32x4* x, int r0, int rows, const f32x16& st,
+                    const f32x16& dp) __attribute__((always_inline)) {
+    float p[16], ds[16];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int r = 2 * i, row = r0 + 8 * (i >> 1) + 4 * h + 2 * (i & 1);
+      float n0 = x[i][0], n1 = x[i][2];
+      if constexpr (BIAS) {
+        // rows past the end have zeros for Q, dout and their statistics, which
+        // a weight of one leaves at zero, but not one that a bias makes infinite
+        n0 = row < rows ? n0 : -INFINITY;
+        n1 = row + 1 < rows ? n1 : -INFINITY;
+      }
+      p[r] = weight<BIAS>(st[r], c, bi, n0);
+      p[r + 1] = weight<BIAS>(st[r + 1], c, bi, n1);
+      ds[r] = p[r] * (dp[r] - x[i][1]);
+      ds[r + 1] = p[r + 1] * (dp[r + 1] - x[i][3]);
+    }
+    const Frag pf[2] = {Mat<T>::pack(p), Mat<T>::pack(p + 8)}, df[2] = {Mat<T>::pack(ds), Mat<T>::pack(ds + 8)};
+    if constexpr (kAhead && DP == 128) {
+      Frag tv[ND], tk[ND];
+#pragma unroll
+      for (int nd = 0; nd < ND; ++nd) {
+        tv[nd] = L::col_frag(gl, r0, nd * 32, lane);
+        tk[nd] = L::col_frag(ql, r0, nd * 32, lane);
+      }
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int nd = 0; nd < ND; ++nd) {
+        dv[nd] = Mat<T>::mma(tv[nd], pf[0], dv[nd]);
+        tv[nd] = L::col_frag(gl, r0 + 16, nd * 32, lane);
+        dk[nd] = Mat<T>::mma(tk[nd], df[0], dk[nd]);
+        tk[nd] = L::col_frag(ql, r0 + 16, nd * 32, lane);
+      }
+#pragma unroll
+      for (int nd = 0; nd < ND; ++nd) {
+        dv[nd] = Mat<T>::mma(tv[nd], pf[1], dv[nd]);
+        dk[nd] = Mat<T>::mma(tk[nd], df[1], dk[nd]);
+      }
+    } else {
+#pragma unroll
+      for (int s = 0; s < 2; ++s)
+#pragma unroll
+        for (int nd = 0; nd < ND; ++nd) {
+          dv[nd] = Mat<T>::mma(L::col_frag(gl, r0 + 16 * s, nd * 32, lane), pf[s], dv[nd]);
+          dk[nd] = Mat<T>::mma(L::col_frag(ql, r0 + 16 * s, nd * 32, lane), df[s], dk[nd]);
+        }
+    }
+  };
+  auto step = [&](int b, char* qc, char* gc, float* sc, char* qp, char* gp, float* sp, char* qn, char* gn,
+                  float* sn) __attribute__((always_inline)) {
+    const int rows = left_next;
+    if (b + 1 < b1) load(qn, gn, sn);
+    f32x4 x[8];
+    statistics(sp, 32, x);
+    scores(qc, gc, 0, sa, da);
+    values(qp, gp, x, 32, left, sb, db);
+    statistics(sc, 0, x);
+    scores(qc, gc, 32, sb, db);
+    values(qc, gc, x, 0, rows, sa, da);
     left = rows;
     wait_loads();
     __syncthreads();
   };
+  auto step_in_order = [&](int b, char* qc, char* gc, float* sc, char* qn, char* gn,
+                           float* sn) __attribute__((always_inline)) {
+    const int rows = left_next;
+    if (b + 1 < b1) load(qn, gn, sn);
+    for (int r0 = 0; r0 < kDkvRows; r0 += 32) {
+      f32x4 x[8];
+      statistics(sc, r0, x);
+      scores(qc, gc, r0, sa, da);
+      values(qc, gc, x, r0, rows, sa, da);
+    }
+    wait_loads();
+    __syncthreads();
+  };
   if (b0 < b1) {
-    gh = b0 / per_head;
-    gr = (b0 - gh * per_head) * kDkvRows;
-    left_next = qr.len - gr;
+    const int head0 = b0 / per_head;
+    seek(pl.hk * A.group + head0, (b0 - head0 * per_head) * kDkvRows);
     load(q0, g0, s0);
     wait_loads();
     __syncthreads();
-    int b = b0;
-    for (; b + 2 < b1; b += 3) {
-      step(b, q0, g0, q2, g2, s2, q1, g1, s1);
-      step(b + 1, q1, g1, q0, g0, s0, q2, g2, s2);
-      step(b + 2, q2, g2, q1, g1, s1, q0, g0, s0);
-    }
-    if (b + 1 < b1) {
-      step(b, q0, g0, q2, g2, s2, q1, g1, s1);
-      step(b + 1, q1, g1, q0, g0, s0, q2, g2, s2);
-      values(q1, g1, s1, left);
-    } else if (b < b1) {
-      step(b, q0, g0, q2, g2, s2, q1, g1, s1);
-      values(q0, g0, s0, left);
+    if constexpr (!kAhead) {
+      int b = b0;
+      for (; b + 1 < b1; b += 2) {
+        step_in_order(b, q0, g0, s0, q1, g1, s1);
+        step_in_order(b + 1, q1, g1, s1, q0, g0, s0);
+      }
+      if (b < b1) step_in_order(b, q0, g0, s0, q1, g1, s1);
     } else {
-      values(q2, g2, s2, left);
+      left = left_next;
+      if (b0 + 1 < b1) load(q1, g1, s1);
+      f32x4 x[8];
+      statistics(s0, 0, x);
+      scores(q0, g0, 0, sa, da);
+      scores(q0, g0, 32, sb, db);
+      values(q0, g0, x, 0, left, sa, da);
+      wait_loads();
+      __syncthreads();
+      int b = b0 + 1;
+      for (; b + 2 < b1; b += 3) {
+        step(b, q1, g1, s1, q0, g0, s0, q2, g2, s2);
+        step(b + 1, q2, g2, s2, q1, g1, s1, q0, g0, s0);
+        step(b + 2, q0, g0, s0, q2, g2, s2, q1, g1, s1);
+      }
+      if (b < b1) step(b, q1, g1, s1, q0, g0, s0, q2, g2, s2);
+      if (b + 1 < b1) step(b + 1, q2, g2, s2, q1, g1, s1, q0, g0, s0);
+      if (b1 == b) {
+        statistics(s0, 32, x);
+        values(q0, g0, x, 32, left, sb, db);
+      } else if (b1 == b + 1) {
+        statistics(s1, 32, x);
+        values(q1, g1, x, 32, left, sb, db);
+      } else {
+        statistics(s2, 32, x);
+        values(q2, g2, x, 32, left, sb, db);
+      }
     }
   }
   if (j >= kr.cap) return;
