@@ -809,11 +809,9 @@ class Sequences:
             s.seq_len = _ptr(seq_len, "seq_len", torch.int32, (num_seqs + len_group - 1) // len_group, dev)
             dev = seq_len.device
         self.c, self.device = s, dev
+        self.num_seqs, self.max_rows, self.total_rows = num_seqs, max_rows, total_rows
         self._keep = (row_range, seq_len)
-
-    num_seqs = property(lambda self: self.c.num_seqs)
-    max_rows = property(lambda self: self.c.max_rows)
-    total_rows = property(lambda self: self.c.total_rows)
+        self._layouts = {}
 
 
 def tdp_plan_sequences(plan: Plan) -> list[tuple[int, int]]:
@@ -891,50 +889,58 @@ def _dtype_code(t, name):
     raise ValueError(f"{name} must be torch.float32 or torch.bfloat16, got {t.dtype}")
 
 
-def _heads(t, name, seqs: Sequences, head_dim, like, written=False):
-    """tdp_heads of a (total_rows, heads, head_dim) tensor, or of a
-    (num_seqs, max_rows, heads, head_dim) one for uniform sequences."""
-    if t is None:
-        raise ValueError(f"{name} is required")
-    if not t.is_cuda or t.device != like.device:
-        raise ValueError(f"{name} must be on {like.device if like.is_cuda else 'a GPU'}, got {t.device}")
-    if seqs.device is not None and seqs.device != t.device:
-        raise ValueError(f"{name} is on {t.device}, its sequences on {seqs.device}")
-    if t.dtype != like.dtype:
-        raise ValueError(f"{name} must be {like.dtype}, got {t.dtype}")
-    h = tdp_heads()
-    if t.dim() == 4 and not seqs.c.row_range:
-        if t.shape[0] != seqs.num_seqs or t.shape[1] != seqs.max_rows:
-            raise ValueError(f"{name} is {tuple(t.shape)}, needs ({seqs.num_seqs}, {seqs.max_rows}, heads, {head_dim})")
-        h.seq_stride, h.row_stride, h.head_stride = t.stride()[:3]
-    elif t.dim() == 3:
-        if t.shape[0] != seqs.total_rows:
-            raise ValueError(f"{name} holds {t.shape[0]} rows, needs {seqs.total_rows}")
-        h.row_stride, h.head_stride = t.stride()[:2]
-        h.seq_stride = seqs.max_rows * h.row_stride
+def _layout(t, name, seqs: Sequences, head_dim, written):
+    """(seq, row, head strides, heads) of a (total_rows, heads, head_dim) tensor, or of a
+    (num_seqs, max_rows, heads, head_dim) one for uniform sequences, after checking it."""
+    shape, stride = t.shape, t.stride()
+    if len(shape) == 4 and not seqs.c.row_range:
+        if shape[0] != seqs.num_seqs or shape[1] != seqs.max_rows:
+            raise ValueError(f"{name} is {tuple(shape)}, needs ({seqs.num_seqs}, {seqs.max_rows}, heads, {head_dim})")
+        seq_stride, row_stride, head_stride = stride[:3]
+    elif len(shape) == 3:
+        if shape[0] != seqs.total_rows:
+            raise ValueError(f"{name} holds {shape[0]} rows, needs {seqs.total_rows}")
+        row_stride, head_stride = stride[:2]
+        seq_stride = seqs.max_rows * row_stride
     else:
         raise ValueError(f"{name} must be (rows, heads, head_dim), or (sequences, rows, heads, head_dim) without row "
-                         f"ranges; got {tuple(t.shape)}")
-    if t.shape[-1] != head_dim or (head_dim > 1 and t.stride(-1) != 1):
-        raise ValueError(f"{name} needs {head_dim} contiguous elements per head, got {tuple(t.shape)} with strides "
-                         f"{t.stride()}")
+                         f"ranges; got {tuple(shape)}")
+    if shape[-1] != head_dim or stride[-1] != 1:
+        raise ValueError(f"{name} needs {head_dim} contiguous elements per head, got {tuple(shape)} with strides "
+                         f"{stride}")
     if written:   # every element its own place
-        dims = sorted((st, n) for st, n in zip(t.stride(), t.shape) if n > 1)
         reach = 1
-        for st, n in dims:
+        for st, n in sorted((st, n) for st, n in zip(stride, shape) if n > 1):
             if st < reach:
-                raise ValueError(f"{name} is written and must not overlap itself (strides {t.stride()})")
+                raise ValueError(f"{name} is written and must not overlap itself (strides {stride})")
             reach = st * (n - 1) + reach
     # a dimension of one element is never stepped over: torch may report any stride for it
-    sizes = t.shape[:-1] if t.dim() == 4 else (1,) + tuple(t.shape[:-1])
-    if sizes[-1] == 1:
-        h.head_stride = 0
-    if sizes[-2] == 1:
-        h.row_stride = 0
-    if t.dim() == 4 and sizes[0] == 1 or seqs.num_seqs == 1:
-        h.seq_stride = 0
-    h.data, h.heads = t.data_ptr(), t.shape[-2]
-    return h
+    heads, rows = shape[-2], shape[-3]
+    if len(shape) == 4 and shape[0] == 1 or seqs.num_seqs == 1:
+        seq_stride = 0
+    return seq_stride, row_stride if rows > 1 else 0, head_stride if heads > 1 else 0, heads
+
+
+def _heads(t, name, seqs: Sequences, head_dim, like, written=False):
+    """tdp_heads of a tensor after checking it against ``like``'s device and dtype."""
+    if t is None:
+        raise ValueError(f"{name} is required")
+    if t is not like:
+        if t.device != like.device:
+            raise ValueError(f"{name} must be on {like.device}, got {t.device}")
+        if t.dtype != like.dtype:
+            raise ValueError(f"{name} must be {like.dtype}, got {t.dtype}")
+    elif not t.is_cuda:
+        raise ValueError(f"{name} must be on a GPU, got {t.device}")
+    if seqs.device is not None and seqs.device != t.device:
+        raise ValueError(f"{name} is on {t.device}, its sequences on {seqs.device}")
+    key = (t.shape, t.stride(), head_dim, written)
+    lay = seqs._layouts.get(key)   # layouts of these sequences checked before, whatever tensor had them
+    if lay is None:
+        lay = _layout(t, name, seqs, head_dim, written)
+        if len(seqs._layouts) < 64:
+            seqs._layouts[key] = lay
+    return tdp_heads(t.data_ptr(), *lay)
 
 
 def _vec(t, name, dtype, numel, device):
