@@ -539,11 +539,12 @@ __device__ inline float weight(float s, float c, float bias, float nl) {
 __device__ inline float neg_lse(float lse) { return lse == -INFINITY ? -INFINITY : -lse * kLog2e; }
 
 // dq: the forward's walk over the keys with a third product.  128 query entries
-// per workgroup, 32 per wave; blocks of 32 keys pass through three LDS buffers:
-// one being loaded, one whose scores are multiplied, and the one before it,
-// whose weights become ds and meet K again.  delta = dout . out is made here, by
-// the lanes that hold dout, and left with lse for the dk and dv kernel.
-constexpr int kDqKeys = 32;
+// per workgroup, 32 per wave; blocks of 64 keys pass through two LDS buffers,
+// 32 keys at a time.  The operands of the score products are read ahead of them
+// (a barrier for the scheduler, as in attn_dkv_kernel); two workgroups share a
+// CU and fill each other's waits.  delta = dout . out is made here, by the lanes
+// that hold dout, and left with lse for the dk and dv kernel.
+constexpr int kDqKeys = 64;
 template <int T, int DP, bool BIAS>
 __global__ __launch_bounds__(kTok, T == TDP_BF16 ? 2 : 1) void attn_dq_kernel(const AttnArgs A) {
   typedef Tile<T, DP> L;
@@ -551,10 +552,8 @@ __global__ __launch_bounds__(kTok, T == TDP_BF16 ? 2 : 1) void attn_dq_kernel(co
   constexpr int KD = DP / 16, ND = DP / 32, kTile = kDqKeys * L::kRow;
   __shared__ __align__(16) char k0[kTile];
   __shared__ __align__(16) char k1[kTile];
-  __shared__ __align__(16) char k2[kTile];
   __shared__ __align__(16) char v0[kTile];
   __shared__ __align__(16) char v1[kTile];
-  __shared__ __align__(16) char v2[kTile];
   __shared__ __align__(16) float bl[BIAS ? 4 * kDqKeys : 4];
   const uint32_t item = xcd_item(A.tiles);
   if (item >= A.tiles) return;
@@ -589,7 +588,7 @@ __global__ __launch_bounds__(kTok, T == TDP_BF16 ? 2 : 1) void attn_dq_kernel(co
   const float nl = live ? neg_lse(A.lse[stat]) : -INFINITY;
   if (live && h == 0) A.stats[stat] = f32x2{nl, delta};
   const float c = A.scale * kLog2e;
-  f32x16 dq[ND], st = zero16(), dp = zero16();
+  f32x16 dq[ND];
 #pragma unroll
   for (int nd = 0; nd < ND; ++nd) dq[nd] = zero16();
 
@@ -607,32 +606,40 @@ __global__ __launch_bounds__(kTok, T == TDP_BF16 ? 2 : 1) void attn_dq_kernel(co
     kd.load(kb, krow, d_bytes, b * kDqKeys, kr.len, wave, kn);
     vd.load(vb, vrow, d_bytes, b * kDqKeys, kr.len, wave, vn);
   };
-  // the block whose scores are in st and dp: ds, and its product with K
-  auto values = [&](int b, char* kl) __attribute__((always_inline)) {
+  // 32 keys from key k0 of the block in kl and vl
+  auto part = [&](int b, int r0, char* kl, char* vl) __attribute__((always_inline)) {
+    f32x16 st = zero16(), dp = zero16();
+    Frag ka[KD], va[KD];
+#pragma unroll
+    for (int kk = 0; kk < KD; ++kk) ka[kk] = L::row_frag(kl, r0 + (lane & 31), kk, h);
+#pragma unroll
+    for (int kk = 0; kk < KD; ++kk) va[kk] = L::row_frag(vl, r0 + (lane & 31), kk, h);
+    if (T == TDP_BF16) __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int kk = 0; kk < KD; ++kk) st = Mat<T>::mma(ka[kk], qf[kk], st);
+#pragma unroll
+    for (int kk = 0; kk < KD; ++kk) dp = Mat<T>::mma(va[kk], gf[kk], dp);
+    if (!BIAS && b * kDqKeys + r0 + 32 > kr.len) mask_scores<false>(st, nullptr, c, b * kDqKeys + r0, kr.len, h);
     float ds[16];
 #pragma unroll
     for (int r = 0; r < 16; ++r)
-      ds[r] = weight<BIAS>(st[r], c, BIAS ? biases.at(b)[8 * (r >> 2) + 4 * h + (r & 3)] : 0.0f, nl) * (dp[r] - delta);
+      ds[r] = weight<BIAS>(st[r], c, BIAS ? biases.at(b)[r0 + 8 * (r >> 2) + 4 * h + (r & 3)] : 0.0f, nl) *
+              (dp[r] - delta);
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
       const Frag f = Mat<T>::pack(ds + 8 * s);
+      Frag tk[ND];
 #pragma unroll
-      for (int nd = 0; nd < ND; ++nd) dq[nd] = Mat<T>::mma(L::col_frag(kl, 16 * s, nd * 32, lane), f, dq[nd]);
+      for (int nd = 0; nd < ND; ++nd) tk[nd] = L::col_frag(kl, r0 + 16 * s, nd * 32, lane);
+#pragma unroll
+      for (int nd = 0; nd < ND; ++nd) dq[nd] = Mat<T>::mma(tk[nd], f, dq[nd]);
     }
   };
-  auto step = [&](int b, const char* kc, char* kp, char* kn, const char* vc, char* vn) __attribute__((always_inline)) {
+  auto step = [&](int b, char* kc, char* vc, char* kn, char* vn) __attribute__((always_inline)) {
     if constexpr (BIAS) biases.advance(b);
     if (b + 1 < nb) load(b + 1, kn, vn);
-    f32x16 sn = zero16(), dn = zero16();
 #pragma unroll
-    for (int kk = 0; kk < KD; ++kk) {
-      sn = Mat<T>::mma(L::row_frag(kc, lane & 31, kk, h), qf[kk], sn);
-      dn = Mat<T>::mma(L::row_frag(vc, lane & 31, kk, h), gf[kk], dn);
-    }
-    if (b > 0) values(b - 1, kp);
-    st = sn;
-    dp = dn;
-    if (!BIAS && (b + 1) * kDqKeys > kr.len) mask_scores<false>(st, nullptr, c, b * kDqKeys, kr.len, h);
+    for (int r0 = 0; r0 < kDqKeys; r0 += 32) part(b, r0, kc, vc);
     wait_loads();
     if constexpr (BIAS) {
       if (b + 1 < nb) {
@@ -653,21 +660,11 @@ __global__ __launch_bounds__(kTok, T == TDP_BF16 ? 2 : 1) void attn_dq_kernel(co
       __syncthreads();
     }
     int b = 0;
-    for (; b + 2 < nb; b += 3) {
-      step(b, k0, k2, k1, v0, v1);
-      step(b + 1, k1, k0, k2, v1, v2);
-      step(b + 2, k2, k1, k0, v2, v0);
+    for (; b + 1 < nb; b += 2) {
+      step(b, k0, v0, k1, v1);
+      step(b + 1, k1, v1, k0, v0);
     }
-    if (b + 1 < nb) {
-      step(b, k0, k2, k1, v0, v1);
-      step(b + 1, k1, k0, k2, v1, v2);
-      values(b + 1, k1);
-    } else if (b < nb) {
-      step(b, k0, k2, k1, v0, v1);
-      values(b, k0);
-    } else {
-      values(b - 1, k2);
-    }
+    if (b < nb) step(b, k0, v0, k1, v1);
   }
   if (m >= M) return;
   char* op = A.dq.data + eb * (seq_base(A.qs, A.dq, pl.s, qr) + row * A.dq.row_stride + head * A.dq.head_stride);
@@ -709,7 +706,7 @@ __global__ __launch_bounds__(kTok, T == TDP_BF16 && DP <= 64 ? 2 : 1) void attn_
   __shared__ __align__(16) char q1[kTile];
   __shared__ __align__(16) char g0[kTile];
   __shared__ __align__(16) char g1[kTile];
-  constexpr bool kAhead = T == TDP_BF16;
+  constexpr bool kAhead = T == TDP_BF16 && DP == 128;
   __shared__ __align__(16) char q2[kAhead ? kTile : 16];
   __shared__ __align__(16) char g2[kAhead ? kTile : 16];
   __shared__ __align__(16) float s0[2 * kDkvRows];
@@ -785,7 +782,7 @@ __global__ __launch_bounds__(kTok, T == TDP_BF16 && DP <= 64 ? 2 : 1) void attn_
       a[kk] = L::row_frag(ql, r0 + (lane & 31), kk, h);
       b[kk] = L::row_frag(gl, r0 + (lane & 31), kk, h);
     }
-    if (kAhead) __builtin_amdgcn_sched_barrier(0);
+    if (T == TDP_BF16) __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
     for (int kk = 0; kk < KD; ++kk) {
       st = Mat<T>::mma(a[kk], kf[kk], st);
@@ -816,7 +813,7 @@ __global__ __launch_bounds__(kTok, T == TDP_BF16 && DP <= 64 ? 2 : 1) void attn_
       ds[r + 1] = p[r + 1] * (dp[r + 1] - x[i][3]);
     }
     const Frag pf[2] = {Mat<T>::pack(p), Mat<T>::pack(p + 8)}, df[2] = {Mat<T>::pack(ds), Mat<T>::pack(ds + 8)};
-    if constexpr (kAhead && DP == 128) {
+    if constexpr (kAhead) {
       Frag tv[ND], tk[ND];
 #pragma unroll
       for (int nd = 0; nd < ND; ++nd) {
@@ -865,6 +862,7 @@ __global__ __launch_bounds__(kTok, T == TDP_BF16 && DP <= 64 ? 2 : 1) void attn_
                            float* sn) __attribute__((always_inline)) {
     const int rows = left_next;
     if (b + 1 < b1) load(qn, gn, sn);
+#pragma unroll
     for (int r0 = 0; r0 < kDkvRows; r0 += 32) {
       f32x4 x[8];
       statistics(sc, r0, x);
