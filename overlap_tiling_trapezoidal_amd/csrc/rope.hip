@@ -175,15 +175,15 @@ template <int T, bool HALVES>
 struct LaneAngles {
   static constexpr int N = HALVES ? 8 : 4;
   float c[N], s[N];
-  __device__ inline void read(int D, int chunk, bool on, const Angles* a) {
+  __device__ inline void read(int D, int chunk, bool on, const float* ac, const float* as) {
     const int d0 = on ? lane_dim<T>(D, chunk, 0) : 0, d1 = on ? lane_dim<T>(D, chunk, 4) : 0;
     float cc[8], ss[8];
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      cc[e] = a->c[d0 + e];
-      cc[4 + e] = a->c[d1 + e];
-      ss[e] = a->s[d0 + e];
-      ss[4 + e] = a->s[d1 + e];
+      cc[e] = ac[d0 + e];
+      cc[4 + e] = ac[d1 + e];
+      ss[e] = as[d0 + e];
+      ss[4 + e] = as[d1 + e];
     }
 #pragma unroll
     for (int e = 0; e < N; ++e) {
@@ -258,6 +258,7 @@ struct RopeArgs {
   float eps, dir;          // dir -1: inverse rotation
   uint32_t blocks;         // row blocks per sequence
   uint32_t per_wg;         // forward: row blocks per workgroup
+  int32_t rows;            // forward: rows a wave takes side by side
   uint32_t q_wgs;          // backward: workgroups on queries, the others take keys
 };
 
@@ -369,7 +370,7 @@ __global__ __launch_bounds__(kTok, U == 2 ? 4 : 3) void rope_kernel(const RopeAr
     turns.fill(iv, A.rope.point == TDP_POINT_MIDDLE, A.dir, &ang[wave]);
     wave_lds_fence();
     LaneAngles<T, HALVES> la;
-    la.read(A.rope.D, chunk, on, &ang[wave]);
+    la.read(A.rope.D, chunk, on, ang[wave].c, ang[wave].s);
     for (int b = 0; b < nq + nk; ++b) {
       const bool k = b >= nq;
       const int heads = k ? ik.heads : iq.heads;
@@ -405,6 +406,85 @@ __global__ __launch_bounds__(kTok, U == 2 ? 4 : 3) void rope_kernel(const RopeAr
 #pragma unroll
       for (int u = 0; u < U; ++u)
         if (on && hb + u * kPer + grp < heads) Raw<T>::store(p + u * step, half, x[u]);
+    }
+  }
+}
+
+// The same for few heads: a row of fewer heads than the wave's lanes hold leaves
+// most lanes idle, so the wave takes P rows of a sequence side by side, one pass
+// for queries and one for keys (hslots heads per row, P * hslots = 64 / G).
+template <int T, int G, bool HALVES, bool NORM>
+__global__ __launch_bounds__(kTok, 4) void rope_few_kernel(const RopeArgs A) {
+  constexpr int kPer = 64 / G, kDims = kPer * 8 * G, N = kDims / 2 / 64;  // dims and pairs of P rows at most
+  __shared__ float angc[kWaves][kDims], angs[kWaves][kDims];
+  __shared__ float exch[HALVES ? kWaves : 1][HALVES ? 512 : 1];
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+  const int chunk = lane % G, grp = lane / G, D = A.rope.D, half = D * 2;
+  const int P = A.rows, hslots = kPer / P, sub = grp / hslots, head = grp - sub * hslots;
+  const uint32_t nblk = A.blocks * (uint32_t)A.seqs.S;
+  const uint32_t b0 = blockIdx.x * A.per_wg, b1 = b0 + A.per_wg < nblk ? b0 + A.per_wg : nblk;
+  const bool on = chunk * 8 < D;
+  const Lanes<T, G> in[2] = {Lanes<T, G>(A.in[0], chunk, head), Lanes<T, G>(A.in[1], chunk, head)};
+  const Lanes<T, G> out[2] = {Lanes<T, G>(A.out[0], chunk, head), Lanes<T, G>(A.out[1], chunk, head)};
+  const Partners<T, HALVES> pt(A.rope, chunk, lane - chunk);
+  const float inv_d = 1.0f / (float)D;
+  // this lane's pairs: slot lane + 64 n is pair p of row r
+  const int pairs = D / 2;
+  for (uint32_t blk = b0; blk < b1; ++blk) {
+    RowAt at;
+    at.s = blk / A.blocks;
+    at.i = (int)(blk - at.s * A.blocks) * kWaves * P + wave * P;
+    at.sr = seq_rows(A.seqs, at.s);
+    if (!at.owned()) continue;
+    const bool owned = at.i + sub < at.sr.cap, live = at.i + sub < at.sr.len;
+    Raw<T> raw[2];
+#pragma unroll
+    for (int t = 0; t < 2; ++t)
+      raw[t].load(in[t].at(A.seqs, at, 0) + sub * in[t].row_step, half, on && live && head < in[t].heads);
+    wave_lds_fence();
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+      const int slot = lane + 64 * n, r = slot / pairs, q = slot - r * pairs;
+      if (r >= P) break;
+      int d0 = 2 * q, d1 = d0 + 1;
+      float c = 1.0f, si = 0.0f;
+      if (q < A.rope.pairs) {
+        const int ax = pair_axis(A.rope, q);
+        if (HALVES) {
+          d0 = q + (ax == 0 ? 0 : A.rope.pair_end[ax - 1]);
+          d1 = d0 + A.rope.half[ax];
+        }
+        if (at.i + r < at.sr.len) {
+          const f32x2 iv = (reinterpret_cast<const f32x2*>(A.pos) + 3 * at.sr.row0 + at.i + r)[(int64_t)ax * at.sr.span];
+          turn(iv.x, iv.y, A.rope.point == TDP_POINT_MIDDLE, A.rope.hi[q], A.rope.lo[q], &c, &si);
+          si *= A.dir;
+        }
+      }
+      angc[wave][r * D + d0] = angc[wave][r * D + d1] = c;
+      angs[wave][r * D + d0] = -si;
+      angs[wave][r * D + d1] = si;
+    }
+    wave_lds_fence();
+    LaneAngles<T, HALVES> la;
+    la.read(D, chunk, on, angc[wave] + sub * D, angs[wave] + sub * D);
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+      if (t && A.in[1].heads == 0) break;
+      float x[1][8];
+      raw[t].unpack(x[0]);
+      if constexpr (NORM) {
+        float ss = 0.0f;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) ss = fmaf(x[0][e], x[0][e], ss);
+        const float r = __builtin_amdgcn_rsqf(fmaf(group_sum<G>(ss), inv_d, A.eps));
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          x[0][e] *= r * (A.w[t] && on ? A.w[t][lane_dim<T>(D, chunk, e)] : 1.0f);
+      }
+      rotate<T, HALVES, 1>(pt, la, exch[HALVES ? wave : 0], lane, 1, x);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) x[0][e] = live ? x[0][e] : 0.0f;
+      if (on && owned && head < out[t].heads) Raw<T>::store(out[t].at(A.seqs, at, 0) + sub * out[t].row_step, half, x[0]);
     }
   }
 }
@@ -477,7 +557,7 @@ __global__ __launch_bounds__(kTok, 3) void norm_backward_kernel(const RopeArgs A
     turns.fill(iv, A.rope.point == TDP_POINT_MIDDLE, -1.0f, &ang[wave]);
     wave_lds_fence();
     LaneAngles<T, HALVES> la;
-    la.read(A.rope.D, chunk, on, &ang[wave]);
+    la.read(A.rope.D, chunk, on, ang[wave].c, ang[wave].s);
     for (int b = 0; b < nb; ++b) {
       const int hb = b * kPer * U;
       const int n = (in.heads - hb + kPer - 1) / kPer;
@@ -556,7 +636,9 @@ __global__ __launch_bounds__(kTok) void norm_weights_kernel(const float* parts, 
 // 182 us for 0.8 GB against 208, registers and exchange buffers being smaller.
 template <int T, int G, bool NORM, bool HALVES>
 void launch_forward(const RopeArgs& a, uint32_t grid, hipStream_t st) {
-  if (a.in[0].heads >= 4 * (64 / G))
+  if (a.rows > 1)
+    hipLaunchKernelGGL((rope_few_kernel<T, G, HALVES, NORM>), dim3(grid), dim3(kTok), 0, st, a);
+  else if (a.in[0].heads >= 4 * (64 / G))
     hipLaunchKernelGGL((rope_kernel<T, G, HALVES, NORM, 4>), dim3(grid), dim3(kTok), 0, st, a);
   else
     hipLaunchKernelGGL((rope_kernel<T, G, HALVES, NORM, 2>), dim3(grid), dim3(kTok), 0, st, a);
@@ -612,13 +694,19 @@ int begin(const char* fn, const tdp_rope* rope, const tdp_seqs* seqs, const floa
   return TDP_OK;
 }
 
-// Row blocks per workgroup of a forward launch: rows of fewer than 4 passes of
-// 64 lanes are taken 32 passes at a time, so that the wave's setup is shared,
-// as long as 4096 workgroups (16 per CU) remain.
+// Rows side by side, and row blocks per workgroup of a forward launch: rows of
+// fewer than 4 passes of 64 lanes are taken 32 passes at a time, so that the
+// wave's setup is shared, as long as 4096 workgroups (16 per CU) remain.
 uint32_t forward_grid(const tdp_seqs& s, RopeArgs* a) {
-  const int64_t nblk = seq_blocks(s, kWaves);
-  const int64_t lanes = (int64_t)(a->in[0].heads + a->in[1].heads) * ((a->rope.D + 7) / 8);
-  int64_t per = lanes < 4 * 64 ? 32 * 64 / lanes : 1;
+  int lanes = 1;  // of a head
+  while (lanes * 8 < a->rope.D) lanes *= 2;
+  int slots = 1;  // heads of a row
+  while (slots < a->in[0].heads || slots < a->in[1].heads) slots *= 2;
+  a->rows = slots * lanes * 2 <= 64 ? 64 / (slots * lanes) : 1;
+  a->blocks = (uint32_t)((s.max_rows + kWaves * a->rows - 1) / (kWaves * a->rows));
+  const int64_t nblk = (int64_t)a->blocks * s.num_seqs;
+  const int64_t work = (int64_t)(a->in[0].heads + a->in[1].heads) * ((a->rope.D + 7) / 8) * a->rows;
+  int64_t per = work < 4 * 64 ? 32 * 64 / work : 1;
   if (per > nblk / 4096) per = nblk / 4096;
   a->per_wg = (uint32_t)(per < 1 ? 1 : per);
   return (uint32_t)((nblk + a->per_wg - 1) / a->per_wg);
