@@ -79,8 +79,14 @@ struct Mat<TDP_F32> {
 };
 
 // A tile of rows in LDS: DP elements per row in 16-byte chunks, chunk c of row
-// r at c ^ swizzle(r), so that neither 16-byte reads of one column chunk over
-// eight rows nor the transposing reads of four rows meet in a bank.
+// r at c ^ swizzle(r).  LDS has 64 banks: one pass serves 32 lanes of a
+// transposing read (four rows at an aligned group of four chunks) or 16 lanes of
+// a 16-byte read (16 rows at the same chunk).  The swizzle's upper bits differ
+// between four neighbouring rows, so the first meet no bank twice; it repeats
+// after eight rows, so the second take two passes.  A swizzle over 16 rows
+// removes that too (no conflict counted), but then rows r and r + 8 need an
+// address each, whose registers spill: dq took 432 us instead of 283 on
+// 4 x 2240 rows, 16 heads of 128.
 template <int T, int DP>
 struct Tile {
   typedef typename Mat<T>::Frag Frag;
@@ -91,7 +97,9 @@ struct Tile {
   }
   // the chunk held by slot c of row r
   __device__ static inline int chunk_at(int r, int c) {
-    return c ^ (kChunks == 4 ? (r >> 2 & 1) << 1 : kChunks == 8 ? (r >> 1 & 3) << 1 : (r & 7) << 1);
+    if (kChunks == 4) return c ^ (r >> 2 & 1);
+    if (kChunks == 8) return c ^ ((r >> 1 & 1) << 2 | (r >> 2 & 1));
+    return c ^ ((r & 3) << 2 | (r >> 2 & 1));
   }
   // A[r][16 kk + 8h .. +7]
   __device__ static inline Frag row_frag(const char* lds, int r, int kk, int h) {
@@ -316,7 +324,7 @@ __device__ inline void mask_scores(f32x16& st, const float* bl, float c, int j0,
 // of block b - 1 run, so that matrix and vector instructions of one wave have
 // each other to overlap with; two workgroups share a CU.
 template <int T, int DP, bool BIAS>
-__global__ __launch_bounds__(kTok, T == TDP_BF16 ? 2 : 1) void attn_forward_kernel(const AttnArgs A) {
+__global__ __launch_bounds__(kTok, T != TDP_BF16 ? 1 : DP == 64 ? 3 : 2) void attn_forward_kernel(const AttnArgs A) {
   typedef Tile<T, DP> L;
   typedef typename Mat<T>::Frag Frag;
   constexpr int KD = DP / 16, ND = DP / 32, KT = kAttnBlockK / 32, kTile = kAttnBlockK * L::kRow;
