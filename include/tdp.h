@@ -20,8 +20,10 @@
  * rank plan runs one rank's round-robin share instead and writes that
  * rank's full-size partial sum, the input of the all_reduce.
  * Around it: plan-quality figures (decoded area, seams, round-robin
- * imbalance), a streaming blend that takes one tile at a time, and the blend
- * of decoded pixel tiles for a tiled VAE decode.
+ * imbalance), a streaming blend that takes one tile at a time, the blend
+ * of decoded pixel tiles for a tiled VAE decode, and what a denoiser's
+ * attention computes on a plan's slots (three-axis rotation, per-head norms,
+ * attention, and their gradients).
  *
  * Conventions
  *   - Every function returns TDP_OK (0) or a negative status; the message of
@@ -660,7 +662,8 @@ int tdp_qk_norm_rope_backward(const tdp_rope* rope, const tdp_seqs* seqs, const 
  * Scores, softmax and sums are fp32; for TDP_BF16 the softmax's weights are
  * rounded to bf16 for the product with v, as its matrix instructions take
  * them.  out overlaps no input.  head_dim is a multiple of 8, at most
- * TDP_MAX_ATTENTION_DIM; scale is finite and > 0.  workspace as above, of
+ * TDP_MAX_ATTENTION_DIM; scale is finite and > 0; rows of q, k, v (and dout) lie
+ * at most 2^25 bytes apart (TDP_ESHAPE).  workspace as above, of
  * tdp_attention_workspace bytes (0: NULL allowed): where few query rows meet
  * long keys, the keys are split over workgroups and joined from there. */
 int64_t tdp_attention_workspace(const tdp_seqs* q_seqs, const tdp_seqs* k_seqs, int32_t q_heads, int32_t k_heads,

@@ -322,7 +322,11 @@ __device__ inline void mask_scores(f32x16& st, const float* bl, float c, int j0,
 // V blocks of 64 keys come through two LDS buffers each, loaded one step ahead.
 // A step multiplies block b's scores while the softmax and the product with V
 // of block b - 1 run, so that matrix and vector instructions of one wave have
-// each other to overlap with; two workgroups share a CU.
+// each other to overlap with; two workgroups share a CU (three at head_dim 64).
+// On 4 x 15456 rows, 12 heads of 128: 5.11 ms, 1.15 PFLOP/s, 0.89 of a large
+// library product's rate; the matrix pipes are busy 68% of the time, at a clock
+// that the card lowers to about 1.7 GHz under this load.  Twice the query entries
+// per wave need all 512 registers and spill: 13.0 ms.
 template <int T, int DP, bool BIAS>
 __global__ __launch_bounds__(kTok, T != TDP_BF16 ? 1 : DP == 64 ? 3 : 2) void attn_forward_kernel(const AttnArgs A) {
   typedef Tile<T, DP> L;
@@ -551,10 +555,15 @@ __device__ inline float neg_lse(float lse) { return lse == -INFINITY ? -INFINITY
 // 32 keys at a time.  The operands of the score products are read ahead of them
 // (a barrier for the scheduler, as in attn_dkv_kernel); two workgroups share a
 // CU and fill each other's waits.  delta = dout . out is made here, by the lanes
-// that hold dout, and left with lse for the dk and dv kernel.
+// that hold dout, and left with lse for the dk and dv kernel.  On 4 x 2240 rows,
+// 16 heads of 128: 283 us, 0.87 PFLOP/s of its three products (324 us when it ran
+// its third product one block behind the scores, as the forward does).
+// The form with a bias takes one workgroup per CU at head_dim 128, where it would
+// spill in the loop (8 x 480 rows on 343 keys, 9 heads of 96: 74 us a backward
+// against 90).
 constexpr int kDqKeys = 64;
 template <int T, int DP, bool BIAS>
-__global__ __launch_bounds__(kTok, T == TDP_BF16 ? 2 : 1) void attn_dq_kernel(const AttnArgs A) {
+__global__ __launch_bounds__(kTok, T == TDP_BF16 && !(BIAS && DP == 128) ? 2 : 1) void attn_dq_kernel(const AttnArgs A) {
   typedef Tile<T, DP> L;
   typedef typename Mat<T>::Frag Frag;
   constexpr int KD = DP / 16, ND = DP / 32, kTile = kDqKeys * L::kRow;
@@ -703,7 +712,9 @@ __device__ inline void load_stats(const f32x2* from, int left, int wave, int lan
 // fp32 tiles, twice the size under matrix instructions of a sixteenth the rate,
 // take two buffers and one half after the other.  Where few key blocks meet many
 // rows, the blocks are split over workgroups, whose sums are joined by
-// attn_sum_kernel.
+// attn_sum_kernel.  On 4 x 2240 rows, 16 heads of 128: 445 us, 0.74 PFLOP/s of its
+// four products; K, V and the sums fill the registers, so one wave per SIMD has
+// nothing but its own instructions to cover its waits.
 constexpr int kDkvRows = 64;
 template <int T, int DP, bool BIAS>
 __global__ __launch_bounds__(kTok, T == TDP_BF16 && DP <= 64 ? 2 : 1) void attn_dkv_kernel(const AttnArgs A) {

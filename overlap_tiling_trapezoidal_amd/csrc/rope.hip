@@ -696,7 +696,9 @@ int begin(const char* fn, const tdp_rope* rope, const tdp_seqs* seqs, const floa
 
 // Rows side by side, and row blocks per workgroup of a forward launch: rows of
 // fewer than 4 passes of 64 lanes are taken 32 passes at a time, so that the
-// wave's setup is shared, as long as 4096 workgroups (16 per CU) remain.
+// wave's setup is shared, as long as 4096 workgroups (16 per CU) remain (8 and 4
+// fp32 heads of 64: 180 us for 0.8 GB against 251 with 4 passes); longer rows are
+// taken one by one (16 bf16 heads of 128: 318 us for 2.0 GB against 354 with 16).
 uint32_t forward_grid(const tdp_seqs& s, RopeArgs* a) {
   int lanes = 1;  // of a head
   while (lanes * 8 < a->rope.D) lanes *= 2;

@@ -48,7 +48,9 @@ inline int64_t seq_blocks(const tdp_seqs& s, int rows) {
 
 // Partial sums of the norm weights' gradients: one row of head_dim floats per
 // workgroup of the backward launch.  A workgroup takes queries or keys; they
-// share at most kNormParts workgroups in proportion to their heads.
+// share at most kNormParts workgroups in proportion to their heads (three per
+// CU, what its registers allow at once: 187 us on 35 840 rows of 16 + 16 heads of
+// 128 against 195 with 2048).
 constexpr int kNormParts = 768;
 constexpr int kNormRowsPerWg = 4;  // one row per wave
 struct NormParts {
@@ -70,7 +72,8 @@ constexpr int kAttnBlockK = 64;   // keys per step
 
 // Key splits of the forward: few query blocks would leave most of the 256
 // CUs idle while each walks all keys, so the keys are cut into parts of at
-// least kAttnSplitKeys until about kAttnSplitBlocks workgroups run.
+// least kAttnSplitKeys until about kAttnSplitBlocks workgroups run (one query row
+// of 2 x 32 heads on 24 576 keys of 8 heads of 128: 44 us against 448 unsplit).
 constexpr int kAttnSplitBlocks = 512;
 constexpr int kAttnSplitKeys = 256;
 constexpr int kAttnMaxSplits = 64;
@@ -98,7 +101,8 @@ inline int64_t attention_workspace(const tdp_seqs& q, const tdp_seqs& k, int32_t
 }
 
 // Row splits of the dk and dv kernel, for the same reason: parts of at least
-// kDkvSplitRows query rows, until about kAttnSplitBlocks workgroups run.
+// kDkvSplitRows query rows, until about kAttnSplitBlocks workgroups run (backward
+// of 4 x 8960 rows, 16 heads on 4 of 64, a 77-token prompt: 148 us against 804).
 constexpr int kDkvSplitRows = 512;
 inline int64_t dkv_blocks(const tdp_seqs& k, int32_t k_heads) {
   return (int64_t)k.num_seqs * k_heads * ((k.max_rows + kAttnBlockQ - 1) / kAttnBlockQ);

@@ -177,6 +177,9 @@ def test_attention_refusals(backward):
         assert attn_call(backward, scale=scale) == tdp.TDP_EINVAL
     for dim in (0, 4, 36, 136):
         assert attn_call(backward, dim=dim) == tdp.TDP_ESHAPE
+    for name in ("q", "k", "v") + (("do",) if backward else ()):
+        assert attn_call(backward, **{name: heads(row_stride=1 << 25)}) == tdp.TDP_ESHAPE   # 2^26 bytes of bf16
+        assert "row stride" in tdp.tdp_last_error()
     assert attn_call(backward, dtype=5) == tdp.TDP_EINVAL
     assert attn_call(backward, bias=P + 2) == tdp.TDP_EINVAL
     assert attn_call(backward, lse=P + 1) == tdp.TDP_EINVAL
