@@ -709,8 +709,10 @@ __device__ inline void load_stats(const f32x2* from, int left, int wave, int lan
 // after another, pass through three LDS buffers with their lse and delta, one
 // being loaded.  They are taken by halves: while one half's scores are
 // multiplied, the half before it becomes weights and meets dout and Q again.
-// fp32 tiles, twice the size under matrix instructions of a sixteenth the rate,
-// take two buffers and one half after the other.  Where few key blocks meet many
+// That is the bf16 form at head_dim 128, where only one wave fits a SIMD; smaller
+// heads, of which two do (2256 us either way on the conditioned slots), and fp32
+// tiles, twice the size under matrix instructions of a sixteenth the rate, take
+// two buffers and one half after the other.  Where few key blocks meet many
 // rows, the blocks are split over workgroups, whose sums are joined by
 // attn_sum_kernel.  On 4 x 2240 rows, 16 heads of 128: 445 us, 0.74 PFLOP/s of its
 // four products; K, V and the sums fill the registers, so one wave per SIMD has
