@@ -584,7 +584,9 @@ __global__ __launch_bounds__(kTok, 3) void norm_backward_kernel(const RopeArgs A
           ss = fmaf(x[u][e], x[u][e], ss);
           gx = fmaf(g[u][e] * w[e], x[u][e], gx);
         }
-        const float r = __builtin_amdgcn_rsqf(fmaf(group_sum<G>(ss), inv_d, A.eps));
+        // lanes without a head hold zeros, whose r is infinite when eps is 0: they stay out of dw
+        const bool has = hb + u * kPer + grp < in.heads;
+        const float r = has ? __builtin_amdgcn_rsqf(fmaf(group_sum<G>(ss), inv_d, A.eps)) : 0.0f;
         const float m = group_sum<G>(gx) * inv_d * r * r;
         float y[8];
 #pragma unroll
@@ -592,7 +594,7 @@ __global__ __launch_bounds__(kTok, 3) void norm_backward_kernel(const RopeArgs A
           dw[e] = fmaf(g[u][e], x[u][e] * r, dw[e]);
           y[e] = r * fmaf(g[u][e], w[e], -x[u][e] * m);
         }
-        if (on && hb + u * kPer + grp < in.heads) Raw<T>::store(op + u * kPer * out.head_step, half, y);
+        if (on && has) Raw<T>::store(op + u * kPer * out.head_step, half, y);
       }
     }
   }
