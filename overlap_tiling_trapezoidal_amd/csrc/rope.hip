@@ -45,8 +45,8 @@ __device__ inline void turn(float a, float b, bool middle, float hi, float lo, f
 
 __device__ inline int pair_axis(const RopeDev& r, int p) { return (p >= r.pair_end[0]) + (p >= r.pair_end[1]); }
 
-// One wave's row of angles, per dim: the factor of the dim itself and of its
-// partner, y[d] = x[d] c[d] + x[partner] s[d] (s carries the pair's sign).
+// One wave's row of angles, per dim that turns: the factor of the dim itself and
+// of its partner, y[d] = x[d] c[d] + x[partner] s[d] (s carries the pair's sign).
 struct Angles {
   float c[TDP_MAX_ROPE_DIM], s[TDP_MAX_ROPE_DIM];
 };
@@ -79,13 +79,6 @@ struct LaneTurns {
         d0[n] = p + (axis[n] == 0 ? 0 : r.pair_end[axis[n] - 1]);
         d1[n] = d0[n] + r.half[axis[n]];
       }
-    }
-  }
-  // the dims that do not turn follow the pairs; once per wave
-  __device__ inline void clear(int D, int lane, Angles* a) const {
-    for (int d = lane; d < D; d += 64) {
-      a->c[d] = 1.0f;
-      a->s[d] = 0.0f;
     }
   }
   __device__ inline void load(const float* pos, const SeqRows& sr, int i, f32x2* iv) const {
@@ -149,11 +142,22 @@ struct Raw {
 };
 
 // Where the partners of a lane's dims pass through a wave's exchange buffer
-// (half-split pairs; the other pairs lie in one lane).
-template <int T, bool HALVES>
+// (half-split pairs; the other pairs lie in one lane), and with PART, for heads of
+// which only the first dims turn, how many turn from the lane's first dim on and
+// from its fifth.  Dims that do not turn are kept by selection: factors of 1 and 0
+// would make a NaN of an infinity, their own or a neighbour's.  Heads that turn
+// whole have kernels of their own, without the selection: as one kernel, a branch
+// or masks cost up to 6 or 30 % there (norm gradients of 8 + 4 fp32 heads of 64,
+// conditioned: 519 us, with them 548 or 672).
+template <int T, bool HALVES, bool PART>
 struct Partners {
+  int left[2];
   int src[HALVES ? 8 : 1];
+  // an even count turns, so a dim and the next turn or pass together
+  __device__ inline bool turns(int e) const { return !PART || (e & 2) < left[e >> 2]; }
   __device__ inline Partners(const RopeDev& r, int chunk, int group_lane0) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) left[i] = 2 * r.pairs - lane_dim<T>(r.D, chunk, 4 * i);
     if constexpr (HALVES) {
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
@@ -196,9 +200,9 @@ struct LaneAngles {
 // Turn the first n of U vectors.  Half-split partners sit in other lanes: they
 // pass through LDS, element e of lane l at e * 64 + l, so writes and reads touch
 // consecutive banks; all vectors are written before the first is read.
-template <int T, bool HALVES, int U>
-__device__ inline void rotate(const Partners<T, HALVES>& pt, const LaneAngles<T, HALVES>& la, float* ex, int lane, int n,
-                              float (*x)[8]) {
+template <int T, bool HALVES, bool PART, int U>
+__device__ inline void rotate(const Partners<T, HALVES, PART>& pt, const LaneAngles<T, HALVES>& la, float* ex, int lane,
+                              int n, float (*x)[8]) {
   if constexpr (!HALVES) {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
@@ -206,8 +210,8 @@ __device__ inline void rotate(const Partners<T, HALVES>& pt, const LaneAngles<T,
 #pragma unroll
       for (int e = 0; e < 8; e += 2) {
         const float a = x[u][e], b = x[u][e + 1];
-        x[u][e] = fmaf(a, la.c[e / 2], -b * la.s[e / 2]);
-        x[u][e + 1] = fmaf(b, la.c[e / 2], a * la.s[e / 2]);
+        x[u][e] = pt.turns(e) ? fmaf(a, la.c[e / 2], -b * la.s[e / 2]) : a;
+        x[u][e + 1] = pt.turns(e) ? fmaf(b, la.c[e / 2], a * la.s[e / 2]) : b;
       }
     }
   } else {
@@ -223,7 +227,8 @@ __device__ inline void rotate(const Partners<T, HALVES>& pt, const LaneAngles<T,
     for (int u = 0; u < U; ++u) {
       if (u >= n) break;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) x[u][e] = fmaf(x[u][e], la.c[e], ex[u * 512 + pt.src[e]] * la.s[e]);
+      for (int e = 0; e < 8; ++e)
+        x[u][e] = pt.turns(e) ? fmaf(x[u][e], la.c[e], ex[u * 512 + pt.src[e]] * la.s[e]) : x[u][e];
     }
   }
 }
@@ -309,7 +314,7 @@ struct Lanes {
   }
 };
 
-template <int T, int G, bool HALVES, bool NORM, int U>
+template <int T, int G, bool HALVES, bool PART, bool NORM, int U>
 __global__ __launch_bounds__(kTok, U == 2 ? 4 : 3) void rope_kernel(const RopeArgs A) {
   constexpr int kPer = 64 / G;
   __shared__ Angles ang[kWaves];
@@ -322,8 +327,7 @@ __global__ __launch_bounds__(kTok, U == 2 ? 4 : 3) void rope_kernel(const RopeAr
   const Lanes<T, G> iq(A.in[0], chunk, grp), ik(A.in[1], chunk, grp), oq(A.out[0], chunk, grp), ok(A.out[1], chunk, grp);
   const int nq = (iq.heads + kPer * U - 1) / (kPer * U), nk = (ik.heads + kPer * U - 1) / (kPer * U);
   const LaneTurns<HALVES, G> turns(A.rope, lane);
-  const Partners<T, HALVES> pt(A.rope, chunk, lane - chunk);
-  turns.clear(A.rope.D, lane, &ang[wave]);
+  const Partners<T, HALVES, PART> pt(A.rope, chunk, lane - chunk);
   const float inv_d = 1.0f / (float)A.rope.D;
   float wq[8], wk[8];
   if constexpr (NORM) {
@@ -400,7 +404,7 @@ __global__ __launch_bounds__(kTok, U == 2 ? 4 : 3) void rope_kernel(const RopeAr
           for (int e = 0; e < 8; ++e) x[u][e] *= r * w[e];
         }
       }
-      rotate<T, HALVES, U>(pt, la, exch[HALVES ? wave : 0], lane, n, x);
+      rotate<T, HALVES, PART, U>(pt, la, exch[HALVES ? wave : 0], lane, n, x);
       char* p = k ? ok.at(A.seqs, at, hb) : oq.at(A.seqs, at, hb);
       const int64_t step = (k ? ok.head_step : oq.head_step) * kPer;
 #pragma unroll
@@ -413,7 +417,7 @@ __global__ __launch_bounds__(kTok, U == 2 ? 4 : 3) void rope_kernel(const RopeAr
 // The same for few heads: a row of fewer heads than the wave's lanes hold leaves
 // most lanes idle, so the wave takes P rows of a sequence side by side, one pass
 // for queries and one for keys (hslots heads per row, P * hslots = 64 / G).
-template <int T, int G, bool HALVES, bool NORM>
+template <int T, int G, bool HALVES, bool PART, bool NORM>
 __global__ __launch_bounds__(kTok, 4) void rope_few_kernel(const RopeArgs A) {
   constexpr int kPer = 64 / G, kDims = kPer * 8 * G, N = kDims / 2 / 64;  // dims and pairs of P rows at most
   __shared__ float angc[kWaves][kDims], angs[kWaves][kDims];
@@ -426,7 +430,7 @@ __global__ __launch_bounds__(kTok, 4) void rope_few_kernel(const RopeArgs A) {
   const bool on = chunk * 8 < D;
   const Lanes<T, G> in[2] = {Lanes<T, G>(A.in[0], chunk, head), Lanes<T, G>(A.in[1], chunk, head)};
   const Lanes<T, G> out[2] = {Lanes<T, G>(A.out[0], chunk, head), Lanes<T, G>(A.out[1], chunk, head)};
-  const Partners<T, HALVES> pt(A.rope, chunk, lane - chunk);
+  const Partners<T, HALVES, PART> pt(A.rope, chunk, lane - chunk);
   const float inv_d = 1.0f / (float)D;
   // this lane's pairs: slot lane + 64 n is pair p of row r
   const int pairs = D / 2;
@@ -446,19 +450,18 @@ __global__ __launch_bounds__(kTok, 4) void rope_few_kernel(const RopeArgs A) {
     for (int n = 0; n < N; ++n) {
       const int slot = lane + 64 * n, r = slot / pairs, q = slot - r * pairs;
       if (r >= P) break;
+      if (PART && q >= A.rope.pairs) continue;
+      const int ax = pair_axis(A.rope, q);
       int d0 = 2 * q, d1 = d0 + 1;
+      if (HALVES) {
+        d0 = q + (ax == 0 ? 0 : A.rope.pair_end[ax - 1]);
+        d1 = d0 + A.rope.half[ax];
+      }
       float c = 1.0f, si = 0.0f;
-      if (q < A.rope.pairs) {
-        const int ax = pair_axis(A.rope, q);
-        if (HALVES) {
-          d0 = q + (ax == 0 ? 0 : A.rope.pair_end[ax - 1]);
-          d1 = d0 + A.rope.half[ax];
-        }
-        if (at.i + r < at.sr.len) {
-          const f32x2 iv = (reinterpret_cast<const f32x2*>(A.pos) + 3 * at.sr.row0 + at.i + r)[(int64_t)ax * at.sr.span];
-          turn(iv.x, iv.y, A.rope.point == TDP_POINT_MIDDLE, A.rope.hi[q], A.rope.lo[q], &c, &si);
-          si *= A.dir;
-        }
+      if (at.i + r < at.sr.len) {
+        const f32x2 iv = (reinterpret_cast<const f32x2*>(A.pos) + 3 * at.sr.row0 + at.i + r)[(int64_t)ax * at.sr.span];
+        turn(iv.x, iv.y, A.rope.point == TDP_POINT_MIDDLE, A.rope.hi[q], A.rope.lo[q], &c, &si);
+        si *= A.dir;
       }
       angc[wave][r * D + d0] = angc[wave][r * D + d1] = c;
       angs[wave][r * D + d0] = -si;
@@ -481,7 +484,7 @@ __global__ __launch_bounds__(kTok, 4) void rope_few_kernel(const RopeArgs A) {
         for (int e = 0; e < 8; ++e)
           x[0][e] *= r * (A.w[t] && on ? A.w[t][lane_dim<T>(D, chunk, e)] : 1.0f);
       }
-      rotate<T, HALVES, 1>(pt, la, exch[HALVES ? wave : 0], lane, 1, x);
+      rotate<T, HALVES, PART, 1>(pt, la, exch[HALVES ? wave : 0], lane, 1, x);
 #pragma unroll
       for (int e = 0; e < 8; ++e) x[0][e] = live ? x[0][e] : 0.0f;
       if (on && owned && head < out[t].heads) Raw<T>::store(out[t].at(A.seqs, at, 0) + sub * out[t].row_step, half, x[0]);
@@ -493,7 +496,7 @@ __global__ __launch_bounds__(kTok, 4) void rope_few_kernel(const RopeArgs A) {
 // the weight's gradient over its rows, in a fixed order.  A workgroup takes
 // queries or keys (the first q_wgs take queries), which keeps one tensor's sums
 // and weights in registers.
-template <int T, int G, bool HALVES>
+template <int T, int G, bool HALVES, bool PART>
 __global__ __launch_bounds__(kTok, 3) void norm_backward_kernel(const RopeArgs A) {
   constexpr int kPer = 64 / G, U = 2;
   __shared__ Angles ang[kWaves];
@@ -511,8 +514,7 @@ __global__ __launch_bounds__(kTok, 3) void norm_backward_kernel(const RopeArgs A
   const uint32_t b0 = (uint32_t)((uint64_t)nblk * wg / wgs), b1 = (uint32_t)((uint64_t)nblk * (wg + 1) / wgs);
   const int nb = (in.heads + kPer * U - 1) / (kPer * U);
   const LaneTurns<HALVES, G> turns(A.rope, lane);
-  const Partners<T, HALVES> pt(A.rope, chunk, lane - chunk);
-  turns.clear(A.rope.D, lane, &ang[wave]);
+  const Partners<T, HALVES, PART> pt(A.rope, chunk, lane - chunk);
   const float inv_d = 1.0f / (float)A.rope.D;
   float w[8], dw[8];
 #pragma unroll
@@ -573,7 +575,7 @@ __global__ __launch_bounds__(kTok, 3) void norm_backward_kernel(const RopeArgs A
         nx.next(A.seqs, A.blocks, wave);
         begin_row();
       }
-      rotate<T, HALVES, U>(pt, la, exch[HALVES ? wave : 0], lane, n, g);
+      rotate<T, HALVES, PART, U>(pt, la, exch[HALVES ? wave : 0], lane, n, g);
       char* op = out.at(A.seqs, at, hb);
 #pragma unroll
       for (int u = 0; u < U; ++u) {
@@ -636,37 +638,35 @@ __global__ __launch_bounds__(kTok) void norm_weights_kernel(const float* parts, 
 // they would not: on 16 bf16 heads of 128 dims (4 passes) four took 329 us for
 // 2.0 GB against 354, on 8 and 4 fp32 heads of 64 dims (one pass each) two took
 // 182 us for 0.8 GB against 208, registers and exchange buffers being smaller.
-template <int T, int G, bool NORM, bool HALVES>
+template <int T, int G, bool NORM, bool HALVES, bool PART>
 void launch_forward(const RopeArgs& a, uint32_t grid, hipStream_t st) {
   if (a.rows > 1)
-    hipLaunchKernelGGL((rope_few_kernel<T, G, HALVES, NORM>), dim3(grid), dim3(kTok), 0, st, a);
+    hipLaunchKernelGGL((rope_few_kernel<T, G, HALVES, PART, NORM>), dim3(grid), dim3(kTok), 0, st, a);
   else if (a.in[0].heads >= 4 * (64 / G))
-    hipLaunchKernelGGL((rope_kernel<T, G, HALVES, NORM, 4>), dim3(grid), dim3(kTok), 0, st, a);
+    hipLaunchKernelGGL((rope_kernel<T, G, HALVES, PART, NORM, 4>), dim3(grid), dim3(kTok), 0, st, a);
   else
-    hipLaunchKernelGGL((rope_kernel<T, G, HALVES, NORM, 2>), dim3(grid), dim3(kTok), 0, st, a);
+    hipLaunchKernelGGL((rope_kernel<T, G, HALVES, PART, NORM, 2>), dim3(grid), dim3(kTok), 0, st, a);
 }
-template <int T, int G, bool NORM>
-void launch_forward(const RopeArgs& a, uint32_t grid, hipStream_t st) {
-  if (a.rope.pairing == TDP_PAIR_HALVES)
-    launch_forward<T, G, NORM, true>(a, grid, st);
-  else
-    launch_forward<T, G, NORM, false>(a, grid, st);
-}
-template <int T, int G>
+template <int T, int G, bool HALVES, bool PART>
 void launch_backward(const RopeArgs& a, uint32_t grid, hipStream_t st) {
-  if (a.rope.pairing == TDP_PAIR_HALVES)
-    hipLaunchKernelGGL((norm_backward_kernel<T, G, true>), dim3(grid), dim3(kTok), 0, st, a);
-  else
-    hipLaunchKernelGGL((norm_backward_kernel<T, G, false>), dim3(grid), dim3(kTok), 0, st, a);
+  hipLaunchKernelGGL((norm_backward_kernel<T, G, HALVES, PART>), dim3(grid), dim3(kTok), 0, st, a);
 }
 
 enum class Mode { kRope, kNorm, kBackward };
 
+template <int T, int G, bool HALVES, bool PART>
+void launch_mode(Mode m, const RopeArgs& a, uint32_t grid, hipStream_t st) {
+  if (m == Mode::kRope) launch_forward<T, G, false, HALVES, PART>(a, grid, st);
+  if (m == Mode::kNorm) launch_forward<T, G, true, HALVES, PART>(a, grid, st);
+  if (m == Mode::kBackward) launch_backward<T, G, HALVES, PART>(a, grid, st);
+}
 template <int T, int G>
 void launch_mode(Mode m, const RopeArgs& a, uint32_t grid, hipStream_t st) {
-  if (m == Mode::kRope) launch_forward<T, G, false>(a, grid, st);
-  if (m == Mode::kNorm) launch_forward<T, G, true>(a, grid, st);
-  if (m == Mode::kBackward) launch_backward<T, G>(a, grid, st);
+  const bool halves = a.rope.pairing == TDP_PAIR_HALVES, part = 2 * a.rope.pairs < a.rope.D;
+  if (halves && part) launch_mode<T, G, true, true>(m, a, grid, st);
+  else if (halves) launch_mode<T, G, true, false>(m, a, grid, st);
+  else if (part) launch_mode<T, G, false, true>(m, a, grid, st);
+  else launch_mode<T, G, false, false>(m, a, grid, st);
 }
 template <int T>
 void launch_group(Mode m, const RopeArgs& a, uint32_t grid, hipStream_t st) {

@@ -1,4 +1,7 @@
-"""Values at the edge of the token operators' formulas: a norm without eps."""
+"""Values at the edge of the token operators' formulas: a norm without eps,
+values that are not finite in dims that do not turn."""
+import math
+
 import pytest
 import torch
 
@@ -8,7 +11,7 @@ import token_reference as R
 from harness import note
 
 pytestmark = pytest.mark.gpu
-DT, NAN = G.DT, float("nan")
+DT, NAN, INF = G.DT, float("nan"), math.inf
 
 
 @pytest.mark.parametrize("dtype", list(DT))
@@ -38,3 +41,87 @@ def test_norm_without_eps(D, hq, hk, pairing, dtype, cuda):
             G.check("dx", dx[a:a + n], v, b)
             want_dw, bound_dw = want_dw + w1, bound_dw + b1
         G.check("dw", dw, want_dw, bound_dw)
+
+
+def same(a, b):
+    """Equal values, signs of zeros among them, or both not a number."""
+    a, b = a.detach().float().cpu(), b.detach().float().cpu()
+    return bool(((a.view(torch.int32) == b.view(torch.int32)) | (a.isnan() & b.isnan())).all())
+
+
+# head_dim, rot dims, heads, rows: the general form (two and four passes) and the one for few heads
+PASS = [(64, (24, 0, 16), 12, 7), (128, (40, 20, 20), 16, 5), (32, (12, 0, 0), 2, 19), (256, (64, 64, 64), 1, 6),
+        (40, (2, 2, 2), 1, 30), (64, (0, 0, 0), 3, 9)]
+
+
+def partial(D, rot_dims, heads, n, pairing, dtype, cuda, seed):
+    case = (D, rot_dims, heads, heads, (n,), (n,), False, pairing, "middle", "rows", 100.0)
+    gen, seqs, rows, rope, pos, planes, rot = G.rope_setup(case, dtype, cuda, seed)
+    return gen, seqs, rope, pos, planes[0], rot
+
+
+@pytest.mark.parametrize("dtype", list(DT))
+@pytest.mark.parametrize("pairing", ["interleaved", "halves"])
+@pytest.mark.parametrize("case", PASS, ids=[f"d{c[0]}-h{c[2]}" for c in PASS])
+def test_dims_that_do_not_turn_pass_unchanged(case, pairing, dtype, cuda):
+    """Infinities, NaN and zeros of either sign beyond the turned dims come out as they are and touch nothing else."""
+    (D, rot_dims, heads, n), dt = case, DT[dtype]
+    gen, seqs, rope, pos, planes, rot = partial(*case, pairing, dtype, cuda, 41)
+    first = sum(rot_dims)
+    x = torch.randn(n, heads, D, generator=gen).to(dt)
+    x[0, :, first] = INF
+    x[1, :, first + 1] = -INF
+    x[2, :, D - 1] = NAN
+    x[3, :, first:] = -0.0
+    x[4, 0, first::2] = torch.finfo(dt).max
+    xd = x.to(cuda)
+    for inverse in (False, True):
+        y = torch.full_like(xd, 7.0)
+        note(f"partial rotation {case} {pairing} {dtype}")
+        tdp.tdp_rope_apply(rope, seqs, pos, xd, y, inverse=inverse)
+        torch.cuda.synchronize()
+        assert same(y[..., first:], x[..., first:])
+        if first:
+            want, mag = R.turn(x.double(), planes, *rot, inverse=inverse)
+            bound = 12 * R.U32 * mag + R.half_step(dt) * want.abs()
+            G.check("turned", y[..., :first], want[..., :first], bound[..., :first])
+
+
+@pytest.mark.parametrize("dtype", list(DT))
+@pytest.mark.parametrize("pairing", ["interleaved", "halves"])
+@pytest.mark.parametrize("case", PASS, ids=[f"d{c[0]}-h{c[2]}" for c in PASS])
+def test_norm_keeps_values_that_do_not_turn_apart(case, pairing, dtype, cuda):
+    """An infinite weight in a dim that does not turn reaches that dim of the output alone; an output gradient that is
+    not finite there reaches that dim of the weight's gradient alone (and, through the mean, its own head's dx)."""
+    (D, rot_dims, heads, n), dt = case, DT[dtype]
+    gen, seqs, rope, pos, planes, rot = partial(*case, pairing, dtype, cuda, 42)
+    d = sum(rot_dims) + 2
+    others = [i for i in range(D) if i != d]
+    x, g = (torch.randn(n, heads, D, generator=gen).to(dt) for _ in range(2))
+    w = 1 + 0.3 * torch.randn(D, generator=gen)
+    xd, w_inf = x.to(cuda), w.clone()
+    w_inf[d] = INF
+    y, y2 = torch.full_like(xd, 7.0), torch.full_like(xd, 7.0)
+    note(f"norm with an infinite weight {case} {pairing} {dtype}")
+    tdp.tdp_qk_norm_rope(rope, seqs, pos, xd, xd, w_inf.to(cuda), w_inf.to(cuda), y, y2, eps=1e-5)
+    torch.cuda.synchronize()
+    want, bound = R.norm_rope(x, w, planes, rot, 1e-5, dt)
+    for t in (y, y2):
+        G.check("others", t[..., others], want[..., others], bound[..., others])
+        assert same(t[..., d], torch.where(x[..., d].float() > 0, INF, -INF))
+    bad = g.clone()
+    bad[n // 2, 0, d] = NAN
+    dx, dx2 = torch.full_like(xd, 7.0), torch.full_like(xd, 7.0)
+    dw, dw2 = torch.full((2, D), 7.0, device=cuda)
+    ws = tdp.allocate_qk_norm_rope_workspace(rope, seqs, heads, heads, cuda)
+    note(f"norm gradients with a NaN {case} {pairing} {dtype}")
+    tdp.tdp_qk_norm_rope_backward(rope, seqs, pos, xd, xd, w.to(cuda), w.to(cuda), bad.to(cuda), bad.to(cuda), dx, dx2,
+                                  dw, dw2, ws, eps=1e-5)
+    torch.cuda.synchronize()
+    want, bound, want_dw, bound_dw = R.norm_rope_backward(x, w, g, planes, rot, 1e-5, dt)
+    keep = torch.ones(n, heads, dtype=torch.bool)
+    keep[n // 2, 0] = False
+    for t, tw in ((dx, dw), (dx2, dw2)):
+        G.check("dx", t.cpu()[keep], want[keep], bound[keep])
+        G.check("dw", tw[others], want_dw[others], bound_dw[others])
+        assert math.isnan(tw[d].item())
