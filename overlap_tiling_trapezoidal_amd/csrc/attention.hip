@@ -359,6 +359,15 @@ __global__ __launch_bounds__(kTok, T != TDP_BF16 ? 1 : DP == 64 ? 3 : 2) void at
 #pragma unroll
   for (int nd = 0; nd < ND; ++nd) o[nd] = zero16();
   float mx = -INFINITY, l = 0.0f;  // mx in the scores' unit
+  // Without a bias a weight's exponent is s c - mc in one fma.  The rounding of
+  // mc = mx c scales all weights of a row alike, which is harmless until it passes
+  // fp32's range (scores past 10^9 would give infinite weights, or none at all);
+  // such rows' scores are lowered by mx first, and mc is 0.  fp32 tensors, whose
+  // matrix instructions leave time for it, always take (s - mx) c (the branch
+  // costs them 3 % at head_dim 64, this 1).
+  constexpr bool kFused = !BIAS && T == TDP_BF16;
+  float mc = 0.0f;
+  bool far = false;  // a row of the wave needs that
   const float c = A.scale * kLog2e, unit = BIAS ? 1.0f : c;
 
   const char* kb = A.k.data + eb * (seq_base(A.ks, A.k, pl.s, kr) + pl.hk * A.k.head_stride);
@@ -386,13 +395,12 @@ __global__ __launch_bounds__(kTok, T != TDP_BF16 ? 1 : DP == 64 ? 3 : 2) void at
   // weights of the scores in st, their sums, and the product with V
   auto values = [&](char* vl) __attribute__((always_inline)) {
     const float mu = mx == -INFINITY ? 0.0f : mx;
-    const float mc = mu * unit;
 #pragma unroll
     for (int kt = 0; kt < KT; ++kt) {
       float p[16];
 #pragma unroll
       for (int r = 0; r < 16; ++r) {
-        p[r] = __builtin_amdgcn_exp2f(BIAS ? st[kt][r] - mu : fmaf(st[kt][r], c, -mc));
+        p[r] = __builtin_amdgcn_exp2f(BIAS ? st[kt][r] - mu : kFused ? fmaf(st[kt][r], c, -mc) : (st[kt][r] - mu) * c);
         l += p[r];
       }
 #pragma unroll
@@ -426,6 +434,15 @@ __global__ __launch_bounds__(kTok, T != TDP_BF16 ? 1 : DP == 64 ? 3 : 2) void at
       l *= f;
 #pragma unroll
       for (int nd = 0; nd < ND; ++nd) o[nd] *= f;
+      if constexpr (kFused) {
+        mc = mx == -INFINITY ? 0.0f : mx * c;
+        far = __any(fabsf(mc) > 0x1p24f);
+        if (far) mc = 0.0f;
+      }
+    }
+    if (kFused && far) {
+#pragma unroll
+      for (int kt = 0; kt < KT; ++kt) st[kt] -= mx == -INFINITY ? 0.0f : mx;
     }
   };
   // block b: its K in kc, the block before's V in vp; K of b + 1 goes to kn, V of b to vc

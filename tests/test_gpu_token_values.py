@@ -1,5 +1,5 @@
 """Values at the edge of the token operators' formulas: a norm without eps,
-values that are not finite in dims that do not turn."""
+values that are not finite in dims that do not turn, scores of 1e9 and more."""
 import math
 
 import pytest
@@ -125,3 +125,31 @@ def test_norm_keeps_values_that_do_not_turn_apart(case, pairing, dtype, cuda):
         G.check("dx", t.cpu()[keep], want[keep], bound[keep])
         G.check("dw", tw[others], want_dw[others], bound_dw[others])
         assert math.isnan(tw[d].item())
+
+
+@pytest.mark.parametrize("dtype", list(DT))
+@pytest.mark.parametrize("D", [32, 64, 128])
+@pytest.mark.parametrize("rows,keys", [(200, 130), (3, 1200)], ids=["whole", "keys-split"])
+@pytest.mark.parametrize("spread", [3e4, 3e5, 1e7])
+def test_attention_of_huge_scores(spread, rows, keys, D, dtype, cuda):
+    """Scores of 1e9 to 1e15: every row whose largest score leads by more than the fp32 errors of two dot products and
+    what makes the other weights vanish gives that key's value, exactly, and its score as lse."""
+    dt, scale = DT[dtype], D ** -0.5
+    gen = torch.Generator().manual_seed(52)
+    q, k, v = (torch.randn(n, 1, D, generator=gen) for n in (rows, keys, keys))
+    q, k, v = ((t * s).to(dt) for t, s in ((q, spread), (k, spread), (v, 1.0)))
+    qs, ks = tdp.Sequences(1, rows), tdp.Sequences(1, keys)
+    out, lse = torch.empty(rows, 1, D, dtype=dt, device=cuda), torch.empty(1, rows, device=cuda)
+    note(f"huge scores {spread} {rows} {D} {dtype}")
+    tdp.tdp_attention(qs, ks, q.to(cuda), k.to(cuda), v.to(cuda), out, lse,
+                      workspace=tdp.allocate_attention_workspace(qs, ks, 1, 1, D, cuda))
+    torch.cuda.synchronize()
+    s = scale * q[:, 0].double() @ k[:, 0].double().T
+    err = (D + 4) * R.U32 * scale * (q[:, 0].double().abs() @ k[:, 0].double().abs().T).max(1).values
+    two = s.topk(2, 1)
+    lead = two.values[:, 0] - two.values[:, 1] > 2 * err + 120   # exp(-120) vanishes in fp32
+    assert lead.sum() > rows // 2 and s.max() > 1e9
+    assert torch.isfinite(out).all() and torch.isfinite(lse).all()
+    assert torch.equal(out[:, 0].cpu()[lead], v[two.indices[:, 0], 0][lead])
+    top = two.values[:, 0]
+    assert ((lse[0].double().cpu() - top).abs() <= err + 4 * R.U32 * top.abs())[lead].all()
