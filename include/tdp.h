@@ -677,7 +677,10 @@ int tdp_attention(const tdp_seqs* q_seqs, const tdp_seqs* k_seqs, const tdp_head
  *   ds = p * (dout_i . v_j - delta_i),  dq = scale * sum_j ds k_j,
  *   dk = scale * sum_i ds q_i,  dv = sum_i p dout_i,
  * dk and dv summed over the query heads that share a key head.  out and lse
- * come from tdp_attention on the same arguments.  No atomics: results repeat
+ * come from tdp_attention on the same arguments.  A row's weights are as good
+ * as its lse: off by about |lse| 2^-22, so a row all of whose scores lie beyond
+ * 10^6 (every key with a bias of -10^9, say, instead of one that takes the key
+ * out) learns only coarsely; its gradients stay finite.  No atomics: results repeat
  * bit for bit.  key_bias takes no gradient.  workspace as above, of
  * tdp_attention_backward_workspace bytes. */
 int64_t tdp_attention_backward_workspace(const tdp_seqs* q_seqs, const tdp_seqs* k_seqs, int32_t q_heads,

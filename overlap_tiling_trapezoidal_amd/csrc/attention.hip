@@ -560,12 +560,25 @@ __global__ __launch_bounds__(kTok) void attn_join_kernel(const AttnArgs A, float
 }
 
 // A weight again from its score: exp(s - lse) in powers of two, nl = -lse log2(e),
-// -infinity for rows without keys.
+// -infinity for rows without keys.  No weight exceeds one, but lse and its change
+// of unit are rounded by up to 2^-22 of it altogether, so past |lse| = 10^8 the
+// exponent can be too high by tens or hundreds: infinite weights, gradients that
+// are not numbers.  With a bias, which takes scores there more easily, the exponent
+// is cut at 0 (one instruction per score, 1 to 2 % of the gradients' time: 6144
+// tokens, 16 heads of 128, a 512-token prompt 242 -> 246 us; the minimum keeps a
+// NaN, unlike fminf).  Without, the cut would cost 1 % at head_dim
+// 128 and 5 % at 64; instead nl is lowered by twice its error beyond 2^24, once
+// per row, which keeps every weight below 2^4.
 template <bool BIAS>
 __device__ inline float weight(float s, float c, float bias, float nl) {
-  return __builtin_amdgcn_exp2f(BIAS ? fmaf(s, c, bias) + nl : fmaf(s, c, nl));
+  return __builtin_amdgcn_exp2f(BIAS ? __builtin_elementwise_minimum(fmaf(s, c, bias) + nl, 0.0f) : fmaf(s, c, nl));
 }
-__device__ inline float neg_lse(float lse) { return lse == -INFINITY ? -INFINITY : -lse * kLog2e; }
+template <bool BIAS>
+__device__ inline float neg_lse(float lse) {
+  if (lse == -INFINITY) return -INFINITY;
+  const float nl = -lse * kLog2e, past = fabsf(nl) - 0x1p24f;
+  return !BIAS && past > 0.0f ? fmaf(past, -0x1p-21f, nl) : nl;
+}
 
 // dq: the forward's walk over the keys with a third product.  128 query entries
 // per workgroup, 32 per wave; blocks of 64 keys pass through two LDS buffers,
@@ -619,7 +632,7 @@ __global__ __launch_bounds__(kTok, T == TDP_BF16 && !(BIAS && DP == 128) ? 2 : 1
   }
   load_frags<T, DP>(at(A.q), h, A.D, qf);
   const int64_t stat = (int64_t)head * A.qs.total + qr.row0 + row;
-  const float nl = live ? neg_lse(A.lse[stat]) : -INFINITY;
+  const float nl = live ? neg_lse<BIAS>(A.lse[stat]) : -INFINITY;
   if (live && h == 0) A.stats[stat] = f32x2{nl, delta};
   const float c = A.scale * kLog2e;
   f32x16 dq[ND];

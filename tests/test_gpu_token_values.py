@@ -1,5 +1,6 @@
 """Values at the edge of the token operators' formulas: a norm without eps,
-values that are not finite in dims that do not turn, scores of 1e9 and more."""
+values that are not finite in dims that do not turn, scores of 1e9 and more
+and the gradients' weights computed again from their lse."""
 import math
 
 import pytest
@@ -153,3 +154,60 @@ def test_attention_of_huge_scores(spread, rows, keys, D, dtype, cuda):
     assert torch.equal(out[:, 0].cpu()[lead], v[two.indices[:, 0], 0][lead])
     top = two.values[:, 0]
     assert ((lse[0].double().cpu() - top).abs() <= err + 4 * R.U32 * top.abs())[lead].all()
+
+
+def bounded_gradients(cuda, dt, D, spread, bias, scale, most, seed):
+    """Attention of 200 rows over 130 keys and its gradients.  Whatever weight in [0, most] a key is given,
+    |dv_j| <= most sum_i |do_i|, |dp - delta| <= D max|do| (max|v| + max|o|) =: z, |dq_i| <= most scale n z max|k| and
+    |dk_j| <= most scale m z max|q|; each may be off by roundings of 2^-7 altogether."""
+    m, n = 200, 130
+    gen = torch.Generator().manual_seed(seed)
+    qs, ks = tdp.Sequences(1, m), tdp.Sequences(1, n)
+    q, g = (torch.randn(m, 1, D, generator=gen) for _ in range(2))
+    k, v = (torch.randn(n, 1, D, generator=gen) for _ in range(2))
+    q, k, v, g = ((t * s).to(dt).to(cuda) for t, s in ((q, spread), (k, spread), (v, 1.0), (g, 1.0)))
+    bd = None if bias is None else torch.full((n,), bias, device=cuda)
+    out, lse = torch.empty_like(q), torch.empty(1, m, device=cuda)
+    dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
+    note(f"bounded gradients {spread} {bias} {D} {dt}")
+    tdp.tdp_attention(qs, ks, q, k, v, out, lse, key_bias=bd, scale=scale)
+    tdp.tdp_attention_backward(qs, ks, q, k, v, out, lse, g, dq, dk, dv,
+                               tdp.allocate_attention_backward_workspace(qs, ks, 1, 1, D, cuda), key_bias=bd,
+                               scale=scale)
+    torch.cuda.synchronize()
+    top = lambda t: t.detach().double().abs().max().item()  # noqa: E731
+    z = most * D * top(g) * (top(v) + top(out))
+    for name, t, limit in (("out", out, top(v)), ("dv", dv, most * g.double().abs().sum(0).max().item()),
+                           ("dq", dq, scale * n * z * top(k)), ("dk", dk, scale * m * z * top(q))):
+        assert torch.isfinite(t).all(), f"{name} is not finite"
+        assert top(t) <= (1 + 2.0 ** -7) * limit, f"{name}: {top(t)} above {limit}"
+    return q, k, v, g, lse, dq
+
+
+@pytest.mark.parametrize("dtype", list(DT))
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("bias", [-1.2e9, -2.5e9, 1.7e9])
+def test_gradients_with_huge_biases(bias, D, dtype, cuda):
+    """Every key's bias huge: fp32 scores keep next to nothing of q . k, lse is rounded by tens, and a weight computed
+    again from it must not pass one."""
+    bounded_gradients(cuda, DT[dtype], D, 1.0, bias, 40.0, 1.0, 51)
+
+
+@pytest.mark.parametrize("dtype", list(DT))
+@pytest.mark.parametrize("D", [32, 64, 128])
+@pytest.mark.parametrize("spread", [3e4, 3e5])
+def test_gradients_of_huge_scores(spread, D, dtype, cuda):
+    """Scores of 1e9 to 1e12 without a bias: no weight above 2^4.  Rows with a clear leader hold its value as their
+    output, so dp - delta there is two fp32 dot products of the same numbers, and dq no more than that makes it."""
+    scale = D ** -0.5
+    q, k, v, g, lse, dq = (t[:, 0].double().cpu() for t in
+                           bounded_gradients(cuda, DT[dtype], D, spread, None, scale, 16.0, 52))
+    s = scale * q @ k.T
+    err = (D + 4) * R.U32 * scale * (q.abs() @ k.abs().T).max(1).values
+    two = s.topk(2, 1)
+    first = two.indices[:, 0]
+    lead = two.values[:, 0] - two.values[:, 1] > 2 * err + 2.0 ** -20 * two.values[:, 0].abs() + 120
+    assert lead.sum() > 100 and s.max() > 1e9
+    same_dots = 2 * (D + 4) * R.U32 * (g.abs() * v[first].abs()).sum(1, keepdim=True)
+    limit = 16 * scale * same_dots * k[first].abs() * (1 + 2.0 ** -6)
+    assert (dq.abs() <= limit)[lead].all()
