@@ -34,17 +34,22 @@ class TileAttention:
         side = head_dim // 3 // 2 * 2
         self.rope = tdp.tdp_rope_create(tdp.make_rope_config(
             head_dim, (head_dim - 2 * side, side, side), scale=(1 / 8, 1 / 32, 1 / 32)))
-        # a slot's unused rows are not written by the extract
-        used = torch.zeros(self.seqs.total_rows, dtype=torch.bool, device=dev)
-        counts = bufs["tile_count"].repeat_interleave(plan.cfg.batch).tolist()
-        for (a, _), n in zip(tdp.tdp_plan_sequences(plan), counts):
-            used[a:a + n] = True
-        self.used = used[:, None]
+        # every row's slot and place in its sequence
+        self.tile_count = bufs["tile_count"]
+        self.slot = torch.zeros(self.seqs.total_rows, dtype=torch.int64, device=dev)
+        self.place = torch.full((self.seqs.total_rows,), self.seqs.max_rows, dtype=torch.int32, device=dev)
+        for s, (a, b) in enumerate(tdp.tdp_plan_sequences(plan)):
+            self.slot[a:b] = s // plan.cfg.batch
+            self.place[a:b] = torch.arange(b - a, dtype=torch.int32, device=dev)
+
+    def used(self):
+        """The rows that the last extract wrote, (rows, 1): a slot's others may hold anything."""
+        return (self.place < self.tile_count[self.slot])[:, None]
 
     def forward(self, tile_lat, tile_pos):
         rows = self.seqs.total_rows
         hq, hk, D = self.heads, self.kv_heads, self.dim
-        x = torch.where(self.used, tile_lat.view(rows, self.channels), 0)
+        x = torch.where(self.used(), tile_lat.view(rows, self.channels), 0)
         qkv = (x @ self.w_qkv.T).view(rows, hq + 2 * hk, D)
         q, k, v = qkv[:, :hq], qkv[:, hq:hq + hk], qkv[:, hq + hk:]
         qn, kn = torch.empty_like(q, memory_format=torch.contiguous_format), torch.empty(
@@ -62,7 +67,7 @@ class TileAttention:
         x, q, k, v, qn, kn, out, lse, tile_pos = saved
         rows = self.seqs.total_rows
         hq, hk, D = self.heads, self.kv_heads, self.dim
-        dy = torch.where(self.used, dy, 0)
+        dy = torch.where(self.used(), dy, 0)
         d_w_out = dy.T @ out.view(rows, hq * D)
         dout = (dy @ self.w_out).view(rows, hq, D)
         dqkv = torch.empty(rows, hq + 2 * hk, D, dtype=dy.dtype, device=dy.device)
