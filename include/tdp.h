@@ -590,9 +590,10 @@ int tdp_plan_sequences(const tdp_plan* plan, int64_t* row_range);
  * section (TDP_PAIR_INTERLEAVED) or (i, i + rot_dim / 2) (TDP_PAIR_HALVES):
  *   y0 = x0 cos(a) - x1 sin(a),  y1 = x0 sin(a) + x1 cos(a),  a = f * p
  * with p the middle of the token's [start, end) interval (TDP_POINT_MIDDLE)
- * or its start (TDP_POINT_START).  Angles are reduced as two-float turns, so
- * positions far from the origin lose nothing against 64 bits that an fp32
- * result could hold. */
+ * or its start (TDP_POINT_START).  All heads of a row turn by the same angles.
+ * Angles are reduced as two-float turns: up to 2^23 turns they are within about
+ * 2^-24 of a turn of the 64-bit angle, however far the position is; beyond, the
+ * error grows with the angle (2^-47 of it). */
 #define TDP_PAIR_INTERLEAVED 0
 #define TDP_PAIR_HALVES 1
 #define TDP_POINT_MIDDLE 0
@@ -627,8 +628,8 @@ int tdp_rope_apply(const tdp_rope* rope, const tdp_seqs* seqs, const float* pos,
 
 /* Per-head norm of queries and keys and their rotation in one pass:
  *   y = turn(x * r * w),  r = 1 / sqrt(mean(x^2) + eps)
- * per row and head, w (head_dim) fp32, one for queries and one for keys
- * (NULL: ones).  q_out may be q and k_out k (same strides).  One launch. */
+ * per row and head (not over the heads of a row), w (head_dim) fp32, one for
+ * queries and one for keys, the same for all their heads (NULL: ones).  q_out may be q and k_out k (same strides).  One launch. */
 int tdp_qk_norm_rope(const tdp_rope* rope, const tdp_seqs* seqs, const float* pos, const tdp_heads* q,
                      const tdp_heads* k, const float* q_weight, const float* k_weight, const tdp_heads* q_out,
                      const tdp_heads* k_out, float eps, int32_t dtype, void* stream);

@@ -768,6 +768,11 @@ def tdp_pixel_blend(plan: PixelPlan, tiles, out, stream=None):
 
 # ---------------------------------------------------------------------------
 # The tile's attention: rotation, norms, attention and their gradients
+#
+# Like the rest of this module the calls write into the caller's tensors through
+# their addresses.  Autograd sees none of it, also for tensors that require
+# gradients: a program calls the backward entry points itself (as
+# examples/tile_attention.py does) or wraps the pairs in functions of its own.
 # ---------------------------------------------------------------------------
 
 class Sequences:
@@ -777,7 +782,8 @@ class Sequences:
     sequence s owns rows [row_start[s], row_start[s + 1]) (``row_start``: S + 1
     int64, ascending) or row_range[s] (``row_range``: (S, 2) int64), none longer
     than ``max_rows``.  ``seq_len`` (int32) holds the used rows, entry
-    s // len_group.  The tensors live on the GPU and are kept alive here.
+    s // len_group.  The tensors live on the GPU and are kept alive here;
+    ``row_start`` is turned into ranges on the current stream.
     """
 
     def __init__(self, num_seqs, max_rows, row_start=None, row_range=None, total_rows=None, seq_len=None,

@@ -25,6 +25,14 @@
 //
 // fp32 tensors run the same code on fp32 matrix instructions, eight
 // contractions of 2 for one of 16.
+//
+// Roundings.  Scores, maxima, sums, delta and every accumulator are fp32 for both
+// types.  For bf16 the weights p and the ds enter their second products as bf16
+// (at most half a step, 2^-8 of each, ties to even), because the bf16 matrix
+// instructions take nothing wider; the sum l is of the weights before that.  The
+// outputs then lie 0.0023 (rms, relative) from 64 bits, where rounding the output
+// alone gives 0.0017: two independent roundings of that size.  Weights in two bf16
+// parts would double those products.
 #include <hip/hip_runtime.h>
 #include <math.h>
 #include <stdint.h>
@@ -150,7 +158,10 @@ struct AttnArgs {
 
 // Workgroups are dealt round-robin to the eight XCDs; each gets a contiguous
 // range of the work items, which are ordered so that neighbours walk the same
-// keys, and these then stay in that XCD's L2.
+// keys, and these then stay in that XCD's L2.  Where slots are used unequally the
+// ranges are unequal work: the fullest XCD of the conditioned plan's gradients (36
+// sequences, a quarter to all of 1024 conditioning rows kept) holds 1.08 to 1.21
+// times the mean, counted over four sets of inputs.
 __device__ inline uint32_t xcd_item(uint32_t tiles) {
   const uint32_t per = (tiles + 7) / 8;
   return (blockIdx.x & 7) * per + (blockIdx.x >> 3);
@@ -586,11 +597,14 @@ __device__ inline float neg_lse(float lse) {
 // (a barrier for the scheduler, as in attn_dkv_kernel); two workgroups share a
 // CU and fill each other's waits.  delta = dout . out is made here, by the lanes
 // that hold dout, and left with lse for the dk and dv kernel.  On 4 x 2240 rows,
-// 16 heads of 128: 283 us, 0.87 PFLOP/s of its three products (324 us when it ran
-// its third product one block behind the scores, as the forward does).
+// 16 heads of 128: 280 us, 0.88 PFLOP/s of its three products (324 us when it ran
+// its third product one block behind the scores, as the forward does); its 1152
+// workgroups are 2.25 rounds of the 512 places, run as three, and at head_dim 128
+// it spills three registers.  Its keys are not split: few tiles of few heads leave
+// CUs idle (one of 2048 rows, 3 heads of 128: 48 workgroups).
 // The form with a bias takes one workgroup per CU at head_dim 128, where it would
-// spill in the loop (8 x 480 rows on 343 keys, 9 heads of 96: 74 us a backward
-// against 90).
+// spill in the loop (gradients of 8 x 480 rows on 343 keys, 9 heads of 96: 70 us
+// against 81; of 4 x 2240 rows on 512 keys, 16 heads of 128: 247 against 302).
 constexpr int kDqKeys = 64;
 template <int T, int DP, bool BIAS>
 __global__ __launch_bounds__(kTok, T == TDP_BF16 && !(BIAS && DP == 128) ? 2 : 1) void attn_dq_kernel(const AttnArgs A) {
@@ -744,9 +758,10 @@ __device__ inline void load_stats(const f32x2* from, int left, int wave, int lan
 // tiles, twice the size under matrix instructions of a sixteenth the rate, take
 // two buffers and one half after the other.  Where few key blocks meet many
 // rows, the blocks are split over workgroups, whose sums are joined by
-// attn_sum_kernel.  On 4 x 2240 rows, 16 heads of 128: 445 us, 0.74 PFLOP/s of its
-// four products; K, V and the sums fill the registers, so one wave per SIMD has
-// nothing but its own instructions to cover its waits.
+// attn_sum_kernel.  On 4 x 2240 rows, 16 heads of 128: 443 us, 0.74 PFLOP/s of its
+// four products; K, V and the sums fill all 512 registers (11 spill, 22 with a
+// bias), so one wave per SIMD has nothing but its own instructions to cover its
+// waits, and the 1152 workgroups are 4.5 rounds of the 256 places, run as five.
 constexpr int kDkvRows = 64;
 template <int T, int DP, bool BIAS>
 __global__ __launch_bounds__(kTok, T == TDP_BF16 && DP <= 64 ? 2 : 1) void attn_dkv_kernel(const AttnArgs A) {

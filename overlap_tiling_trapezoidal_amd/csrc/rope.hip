@@ -493,9 +493,12 @@ __global__ __launch_bounds__(kTok, 4) void rope_few_kernel(const RopeArgs A) {
 }
 
 // Gradient of the norm and rotation: dx per row, and each workgroup's sums of
-// the weight's gradient over its rows, in a fixed order.  A workgroup takes
+// the weight's gradient over its rows, fp32 in a fixed order.  A workgroup takes
 // queries or keys (the first q_wgs take queries), which keeps one tensor's sums
-// and weights in registers.
+// and weights in registers.  With three waves per SIMD, bf16 holds everything in
+// registers (16 + 16 heads of 128, 882 MB: 183 us); fp32 spills 6 to 14 of them
+// with interleaved pairs and 27 to 34 with half-split ones (16 + 16 heads of 128,
+// 1.76 GB: 347 and 357 us; 8 + 4 heads of 64, half-split, 1.18 GB: 517 us).
 template <int T, int G, bool HALVES, bool PART>
 __global__ __launch_bounds__(kTok, 3) void norm_backward_kernel(const RopeArgs A) {
   constexpr int kPer = 64 / G, U = 2;
