@@ -4,6 +4,8 @@ from __future__ import annotations
 import os
 import subprocess
 import sys
+import tempfile
+from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -27,7 +29,6 @@ HIPCC_FLAGS = [
     "-O3",
     "-std=c++17",
     "-fPIC",
-    "-shared",
     "-Wall",
     # keep fp32 division correctly rounded (window values must match the host plan)
     "-fhip-fp32-correctly-rounded-divide-sqrt",
@@ -44,15 +45,26 @@ def hipcc() -> str:
     return "hipcc"
 
 
-def _compile(sources, lib, verbose):
-    tmp = lib + ".tmp"
-    cmd = [hipcc(), *HIPCC_FLAGS, *sources, "-o", tmp]
+def _run(cmd, lib, verbose):
     if verbose:
         print(" ".join(cmd), flush=True)
     res = subprocess.run(cmd, capture_output=True, text=True)
     if res.returncode != 0:
         sys.stderr.write(res.stdout + res.stderr)
         raise RuntimeError(f"hipcc failed building {os.path.basename(lib)}")
+
+
+def _compile(sources, lib, verbose):
+    """Objects side by side, then one link; the library is replaced only when all is well."""
+    tmp = lib + ".tmp"
+    with tempfile.TemporaryDirectory(prefix="tdp_build_") as d:
+        objects = [os.path.join(d, os.path.basename(s) + ".o") for s in sources]
+        with ThreadPoolExecutor(min(len(sources), os.cpu_count() or 1, 8)) as pool:
+            jobs = [pool.submit(_run, [hipcc(), *HIPCC_FLAGS, "-c", s, "-o", o], lib, verbose)
+                    for s, o in zip(sources, objects)]
+            for j in jobs:
+                j.result()
+        _run([hipcc(), "--offload-arch=gfx950", "-fPIC", "-shared", *objects, "-o", tmp], lib, verbose)
     os.replace(tmp, lib)
     return lib
 
