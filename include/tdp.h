@@ -22,8 +22,8 @@
  * Around it: plan-quality figures (decoded area, seams, round-robin
  * imbalance), a streaming blend that takes one tile at a time, the blend
  * of decoded pixel tiles for a tiled VAE decode, and what a denoiser's
- * attention computes on a plan's slots (three-axis rotation, per-head norms,
- * attention, and their gradients).
+ * layer computes on a plan's slots (three-axis rotation, per-head norms,
+ * attention, layer norm, and their gradients).
  *
  * Conventions
  *   - Every function returns TDP_OK (0) or a negative status; the message of
@@ -690,6 +690,49 @@ int tdp_attention_backward(const tdp_seqs* q_seqs, const tdp_seqs* k_seqs, const
                            const tdp_heads* v, const float* key_bias, const tdp_heads* out, const float* lse,
                            const tdp_heads* dout, const tdp_heads* dq, const tdp_heads* dk, const tdp_heads* dv,
                            float scale, int32_t head_dim, int32_t dtype, void* workspace, void* stream);
+
+/* ---- the layer around the attention --------------------------------------- */
+
+/* What a denoising transformer's layer computes on the same rows before and
+ * after its attention.  The calls below take (rows, features) tensors over
+ * sequences as above: unused rows may hold anything in inputs and are 0 in
+ * outputs, rows outside every range are left alone.  Errors as tdp_rope_apply. */
+
+/* A (rows, features) tensor: element strides, features contiguous, placed as
+ * tdp_heads' rows.  data is 16-byte aligned and both strides are multiples of
+ * 16 bytes. */
+typedef struct {
+  void* data;
+  int64_t seq_stride, row_stride;
+} tdp_rows;
+
+/* Layer norm of each row's channels:
+ *   y = (x - mean) * r * w + b,  r = 1 / sqrt(mean((x - mean)^2) + eps).
+ * weight and bias are num_weights rows of `channels` fp32 (NULL: ones, zeros);
+ * sequence s takes row s mod num_weights, so one row serves all, and B rows
+ * give each batch element of a plan's slots its own (modulation by the
+ * timestep).  channels is a multiple of 8, at most TDP_MAX_CHANNELS;
+ * 1 <= num_weights <= num_seqs.  y may be x (same strides).  Sums are fp32: the
+ * squares of a row's differences from its mean have to stay in its range.  With
+ * eps 0 a row of equal values has no norm, as in the formula.  One launch. */
+#define TDP_MAX_CHANNELS 8192
+int tdp_layer_norm(const tdp_seqs* seqs, const tdp_rows* x, const float* weight, const float* bias,
+                   int32_t num_weights, const tdp_rows* y, float eps, int32_t channels, int32_t dtype,
+                   void* stream);
+
+/* Its gradient, from the input and the output's gradient (nothing is saved):
+ * with n = (x - mean) * r and g = dy * w,
+ *   dx = r * (g - mean(g) - n * mean(g * n)),
+ *   dweight = sum of dy * n,  dbias = sum of dy,
+ * the sums over the rows of the sequences that share a weight row.  dx may be
+ * dy or x (same strides).  dweight and dbias (num_weights, channels) fp32 are
+ * written, not added to (NULL: not wanted); the sums run in a fixed order, so
+ * results repeat bit for bit.  workspace as above, of tdp_layer_norm_workspace
+ * bytes. */
+int64_t tdp_layer_norm_workspace(const tdp_seqs* seqs, int32_t channels, int32_t num_weights);
+int tdp_layer_norm_backward(const tdp_seqs* seqs, const tdp_rows* x, const float* weight, int32_t num_weights,
+                            const tdp_rows* dy, const tdp_rows* dx, float* dweight, float* dbias, float eps,
+                            int32_t channels, int32_t dtype, void* workspace, void* stream);
 
 /* ---- errors ------------------------------------------------------------ */
 /* Errors are reported, never produced silently, and a guard violation names

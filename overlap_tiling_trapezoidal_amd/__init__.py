@@ -23,7 +23,8 @@ LIB_PATH = os.environ.get("TDP_LIBRARY") or DEFAULT_LIB_PATH
 DEVICE_FUNCTIONS = ("tdp_extract", "tdp_extract_noalloc", "tdp_set_lookback_polls", "tdp_pipeline_step",
                     "tdp_extract_positions", "tdp_extract_latent", "tdp_pipeline_latent_step", "tdp_blend",
                     "tdp_blend_tile", "tdp_blend_finish", "tdp_pixel_blend", "tdp_rope_apply", "tdp_qk_norm_rope",
-                    "tdp_qk_norm_rope_backward", "tdp_attention", "tdp_attention_backward")
+                    "tdp_qk_norm_rope_backward", "tdp_attention", "tdp_attention_backward", "tdp_layer_norm",
+                    "tdp_layer_norm_backward")
 HEADER_PATH = os.path.join(os.path.dirname(_HERE), "include", "tdp.h")
 
 # ---- constants (mirror include/tdp.h) --------------------------------------
@@ -44,6 +45,7 @@ TDP_POINT_MIDDLE = 0
 TDP_POINT_START = 1
 TDP_MAX_ROPE_DIM = 256
 TDP_MAX_ATTENTION_DIM = 128
+TDP_MAX_CHANNELS = 8192
 
 _DTYPES = {"f32": TDP_F32, "float32": TDP_F32, "bf16": TDP_BF16, "bfloat16": TDP_BF16}
 
@@ -153,6 +155,14 @@ class tdp_heads(ctypes.Structure):
     ]
 
 
+class tdp_rows(ctypes.Structure):
+    _fields_ = [
+        ("data", ctypes.c_void_p),
+        ("seq_stride", ctypes.c_int64),
+        ("row_stride", ctypes.c_int64),
+    ]
+
+
 class tdp_rope_config(ctypes.Structure):
     _fields_ = [
         ("head_dim", ctypes.c_int32),
@@ -183,6 +193,7 @@ def load_library(path: str = LIB_PATH):
     lib = ctypes.CDLL(path)
     vp, i32, i32p = ctypes.c_void_p, ctypes.c_int32, ctypes.POINTER(ctypes.c_int32)
     f32, sq, hd = ctypes.c_float, ctypes.POINTER(tdp_seqs), ctypes.POINTER(tdp_heads)
+    rw = ctypes.POINTER(tdp_rows)
     sig = {
         "tdp_plan_create": (ctypes.c_int, [ctypes.POINTER(tdp_config), ctypes.POINTER(vp)]),
         "tdp_plan_create_rank": (ctypes.c_int, [ctypes.POINTER(tdp_config), i32, i32, ctypes.POINTER(vp)]),
@@ -228,6 +239,9 @@ def load_library(path: str = LIB_PATH):
         "tdp_attention_backward_workspace": (ctypes.c_int64, [sq, sq, i32, i32, i32]),
         "tdp_attention_backward": (ctypes.c_int, [sq, sq, hd, hd, hd, vp, hd, vp, hd, hd, hd, hd, f32, i32, i32, vp,
                                                   vp]),
+        "tdp_layer_norm": (ctypes.c_int, [sq, rw, vp, vp, i32, rw, f32, i32, i32, vp]),
+        "tdp_layer_norm_workspace": (ctypes.c_int64, [sq, i32, i32]),
+        "tdp_layer_norm_backward": (ctypes.c_int, [sq, rw, vp, i32, rw, rw, vp, vp, f32, i32, i32, vp, vp]),
         "tdp_status_string": (ctypes.c_char_p, [ctypes.c_int]),
         "tdp_last_error": (ctypes.c_char_p, []),
     }
@@ -1057,3 +1071,115 @@ def tdp_attention_backward(q_seqs: Sequences, k_seqs: Sequences, q, k, v, out, l
         ref(_heads(dk, "dk", k_seqs, D, q, True)), ref(_heads(dv, "dv", k_seqs, D, q, True)),
         D ** -0.5 if scale is None else scale, D, _dtype_code(q, "q"),
         _ptr(workspace, "workspace", torch.uint8, need, dev), _stream_handle(stream, dev)))
+
+
+# ---------------------------------------------------------------------------
+# The layer around the attention: layer norm
+# ---------------------------------------------------------------------------
+
+def _rows_layout(t, name, seqs: Sequences, features, written):
+    """(seq, row strides) of a (total_rows, features) tensor, or of a (num_seqs, max_rows,
+    features) one for uniform sequences, after checking it."""
+    shape, stride = t.shape, t.stride()
+    if len(shape) == 3 and not seqs.c.row_range:
+        if shape[0] != seqs.num_seqs or shape[1] != seqs.max_rows:
+            raise ValueError(f"{name} is {tuple(shape)}, needs ({seqs.num_seqs}, {seqs.max_rows}, {features})")
+        seq_stride, row_stride = stride[:2]
+    elif len(shape) == 2:
+        if shape[0] != seqs.total_rows:
+            raise ValueError(f"{name} holds {shape[0]} rows, needs {seqs.total_rows}")
+        row_stride = stride[0]
+        seq_stride = seqs.max_rows * row_stride
+    else:
+        raise ValueError(f"{name} must be (rows, features), or (sequences, rows, features) without row ranges; got "
+                         f"{tuple(shape)}")
+    if shape[-1] != features or stride[-1] != 1:
+        raise ValueError(f"{name} needs {features} contiguous elements per row, got {tuple(shape)} with strides "
+                         f"{stride}")
+    if written:   # every element its own place
+        reach = 1
+        for st, n in sorted((st, n) for st, n in zip(stride, shape) if n > 1):
+            if st < reach:
+                raise ValueError(f"{name} is written and must not overlap itself (strides {stride})")
+            reach = st * (n - 1) + reach
+    if seqs.num_seqs == 1:
+        seq_stride = 0
+    return seq_stride, row_stride if shape[-2] > 1 else 0
+
+
+def _rows(t, name, seqs: Sequences, features, like, written=False):
+    """tdp_rows of a tensor after checking it against ``like``'s device and dtype."""
+    if t is None:
+        raise ValueError(f"{name} is required")
+    if t is not like:
+        if t.device != like.device:
+            raise ValueError(f"{name} must be on {like.device}, got {t.device}")
+        if t.dtype != like.dtype:
+            raise ValueError(f"{name} must be {like.dtype}, got {t.dtype}")
+    elif not t.is_cuda:
+        raise ValueError(f"{name} must be on a GPU, got {t.device}")
+    if seqs.device is not None and seqs.device != t.device:
+        raise ValueError(f"{name} is on {t.device}, its sequences on {seqs.device}")
+    key = (t.shape, t.stride(), features, written, "rows")
+    lay = seqs._layouts.get(key)
+    if lay is None:
+        lay = _rows_layout(t, name, seqs, features, written)
+        if len(seqs._layouts) < 64:
+            seqs._layouts[key] = lay
+    return tdp_rows(t.data_ptr(), *lay)
+
+
+def _on(device, call, *args):
+    """A library call with `device` current, as its launches need."""
+    import torch
+    if device.index is None or device.index == torch.cuda.current_device():
+        return _check(call(*args))
+    with torch.cuda.device(device):
+        return _check(call(*args))
+
+
+def _weight_sets(t, name, channels, sets, device):
+    """Pointer of (channels) or (sets, channels) fp32 weights (None: null)."""
+    import torch
+    if t is None:
+        return ctypes.c_void_p(None)
+    if tuple(t.shape) not in ((sets, channels),) + (((channels,),) if sets == 1 else ()):
+        raise ValueError(f"{name} is {tuple(t.shape)}, needs ({sets}, {channels})")
+    return _ptr(t, name, torch.float32, sets * channels, device)
+
+
+def _num_sets(*ts):
+    """Weight rows of the first tensor given: 1 for a vector."""
+    for t in ts:
+        if t is not None:
+            return t.shape[0] if t.dim() == 2 else 1
+    return 1
+
+
+def tdp_layer_norm(seqs: Sequences, x, weight, bias, y, eps=1e-5, stream=None):
+    """Enqueue the layer norm of every used row.  ``weight`` and ``bias``: (channels) fp32 for
+    all, or (n, channels), of which sequence s takes row s mod n (None: ones, zeros).  y may be x."""
+    ref, C, dev, n = ctypes.byref, x.shape[-1], x.device, _num_sets(weight, bias)
+    _on(dev, load_library().tdp_layer_norm, ref(seqs.c), ref(_rows(x, "x", seqs, C, x)),
+        _weight_sets(weight, "weight", C, n, dev), _weight_sets(bias, "bias", C, n, dev), n,
+        ref(_rows(y, "y", seqs, C, x, True)), eps, C, _dtype_code(x, "x"), _stream_handle(stream, dev))
+
+
+def allocate_layer_norm_workspace(seqs: Sequences, channels: int, num_weights: int = 1, device="cuda"):
+    import torch
+    n = load_library().tdp_layer_norm_workspace(ctypes.byref(seqs.c), channels, num_weights)
+    if n <= 0:
+        raise TdpError(TDP_EINVAL, tdp_last_error())
+    return torch.empty(n, dtype=torch.uint8, device=torch.device(device))
+
+
+def tdp_layer_norm_backward(seqs: Sequences, x, weight, dy, dx, dweight, dbias, workspace, eps=1e-5, stream=None):
+    """Enqueue the gradients of tdp_layer_norm (dx may be dy or x; dweight, dbias None: not wanted)."""
+    import torch
+    ref, C, dev, n = ctypes.byref, x.shape[-1], x.device, _num_sets(weight, dweight, dbias)
+    need = load_library().tdp_layer_norm_workspace(ref(seqs.c), C, n)
+    _on(dev, load_library().tdp_layer_norm_backward, ref(seqs.c), ref(_rows(x, "x", seqs, C, x)),
+        _weight_sets(weight, "weight", C, n, dev), n, ref(_rows(dy, "dy", seqs, C, x)),
+        ref(_rows(dx, "dx", seqs, C, x, True)), _weight_sets(dweight, "dweight", C, n, dev),
+        _weight_sets(dbias, "dbias", C, n, dev), eps, C, _dtype_code(x, "x"),
+        _ptr(workspace, "workspace", torch.uint8, need, dev), _stream_handle(stream, dev))

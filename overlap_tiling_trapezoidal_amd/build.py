@@ -11,7 +11,8 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 LIB = os.path.join(HERE, "libtdp.so")
 SOURCES = [os.path.join(HERE, "csrc", n) for n in (
-    "plan.cpp", "quality.cpp", "pixel_plan.cpp", "tokens.cpp", "kernels.hip", "pixel.hip", "rope.hip", "attention.hip")]
+    "plan.cpp", "quality.cpp", "pixel_plan.cpp", "tokens.cpp", "kernels.hip", "pixel.hip", "rope.hip", "attention.hip",
+    "layer_norm.hip")]
 # memory-system ceilings for the measurement script (not the hot path)
 CEILING_LIB = os.path.join(HERE, "libtdp_ceiling.so")
 CEILING_SOURCES = [os.path.join(HERE, "csrc", "ceiling.hip")]

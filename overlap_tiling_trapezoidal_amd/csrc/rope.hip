@@ -101,45 +101,13 @@ struct LaneTurns {
   }
 };
 
-// The dims of a lane: bf16, eight in a row; fp32, four in each half of the
-// head, so that each 16-byte access of neighbouring lanes is contiguous.
-template <int T>
-__device__ inline int lane_dim(int D, int chunk, int e) {
-  return T == TDP_BF16 ? chunk * 8 + e : chunk * 4 + (e & 3) + (e >> 2) * (D / 2);
-}
-// Inverse of it: the slot e * 64 + chunk of dim d in a wave's exchange buffer.
+// Inverse of lane_dim: the slot e * 64 + chunk of dim d in a wave's exchange buffer.
 template <int T>
 __device__ inline int dim_slot(int D, int d) {
   if (T == TDP_BF16) return (d & 7) * 64 + (d >> 3);
   const int up = d >= D / 2, q = d - up * (D / 2);
   return ((q & 3) + 4 * up) * 64 + (q >> 2);
 }
-
-template <int T>
-struct Raw {
-  u32x4 v[T == TDP_BF16 ? 1 : 2];
-  // p: the lane's first dim; half: bytes from the first quad to the second (fp32)
-  __device__ inline void load(const char* p, int half, bool on) {
-    v[0] = u32x4{0, 0, 0, 0};
-    if constexpr (T == TDP_F32) v[1] = u32x4{0, 0, 0, 0};
-    if (on) {
-      v[0] = ld_nt(reinterpret_cast<const u32x4*>(p));
-      if constexpr (T == TDP_F32) v[1] = ld_nt(reinterpret_cast<const u32x4*>(p + half));
-    }
-  }
-  __device__ inline void unpack(float* x) const {
-    InVec<T>::unpack(v[0], x);
-    if constexpr (T == TDP_F32) InVec<T>::unpack(v[1], x + 4);
-  }
-  __device__ static inline void store(char* p, int half, const float* x) {
-    if constexpr (T == TDP_BF16) {
-      store_out<TDP_BF16, 8>(p, 0, x);
-    } else {
-      st_nt(reinterpret_cast<f32x4*>(p), f32x4{x[0], x[1], x[2], x[3]});
-      st_nt(reinterpret_cast<f32x4*>(p + half), f32x4{x[4], x[5], x[6], x[7]});
-    }
-  }
-};
 
 // Where the partners of a lane's dims pass through a wave's exchange buffer
 // (half-split pairs; the other pairs lie in one lane), and with PART, for heads of
@@ -231,25 +199,6 @@ __device__ inline void rotate(const Partners<T, HALVES, PART>& pt, const LaneAng
         x[u][e] = pt.turns(e) ? fmaf(x[u][e], la.c[e], ex[u * 512 + pt.src[e]] * la.s[e]) : x[u][e];
     }
   }
-}
-
-template <int CTRL>
-__device__ inline float dpp(float v) {
-  return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), CTRL, 0xf, 0xf, true));
-}
-// Sum over aligned groups of G lanes: quads by permutes, then mirrors of 8 and
-// 16 lanes, then the swap of neighbouring rows of 16.
-template <int G>
-__device__ inline float group_sum(float v) {
-  if constexpr (G >= 2) v += dpp<0xB1>(v);
-  if constexpr (G >= 4) v += dpp<0x4E>(v);
-  if constexpr (G >= 8) v += dpp<0x141>(v);
-  if constexpr (G >= 16) v += dpp<0x140>(v);
-  if constexpr (G >= 32) {
-    const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
-    v = __uint_as_float(r[0]) + __uint_as_float(r[1]);
-  }
-  return v;
 }
 
 struct RopeArgs {

@@ -41,6 +41,7 @@ struct RopeDev {
 int check_seqs(const char* fn, const char* name, const tdp_seqs* s, SeqsDev* out);
 int check_heads(const char* fn, const char* name, const tdp_heads* t, const tdp_seqs* s, int32_t head_dim,
                 int32_t dtype, HeadsDev* out);
+int check_rows(const char* fn, const char* name, const tdp_rows* t, int32_t dtype, HeadsDev* out);
 // Workgroups of `rows`-row blocks over every sequence: S * ceil(max_rows / rows).
 inline int64_t seq_blocks(const tdp_seqs& s, int rows) {
   return (int64_t)s.num_seqs * ((s.max_rows + rows - 1) / rows);
@@ -128,6 +129,25 @@ inline int64_t backward_workspace(const tdp_seqs& q, const tdp_seqs& k, int32_t 
   const int n = dkv_splits(q, k, q_heads, k_heads);
   const int64_t parts = n == 1 ? 0 : (int64_t)n * k.num_seqs * k_heads * k.max_rows * attention_padded_dim(head_dim) * 8;
   return stats_bytes(q, q_heads) + align256(parts);
+}
+
+// Layer norm: lanes per row (the power of two that holds it in eight elements
+// each, up to a wave; wider rows take four passes of a wave, then the workgroup).
+inline int norm_rows_per_block(int32_t channels) {
+  const int chunks = channels / 8;
+  return chunks <= 8 ? 32 : chunks <= 16 ? 16 : chunks <= 32 ? 8 : chunks <= 256 ? 4 : 1;
+}
+inline int64_t norm_blocks(int32_t max_rows, int32_t channels) {
+  const int r = norm_rows_per_block(channels);
+  return ((int64_t)max_rows + r - 1) / r;
+}
+// Workgroups per set of weights in the backward launch; each leaves two partial
+// rows of sums, so more of them cost the join and fewer leave CUs idle.
+constexpr int kLayerNormParts = 512;
+inline int64_t layer_norm_parts(const tdp_seqs& s, int32_t channels, int32_t sets) {
+  const int64_t blocks = norm_blocks(s.max_rows, channels) * ((s.num_seqs + sets - 1) / sets);
+  int64_t n = (kLayerNormParts + sets - 1) / sets;
+  return n < blocks ? n : blocks;
 }
 
 }  // namespace tdp

@@ -56,6 +56,23 @@ int check_heads(const char* fn, const char* name, const tdp_heads* t, const tdp_
   return TDP_OK;
 }
 
+int check_rows(const char* fn, const char* name, const tdp_rows* t, int32_t dtype, HeadsDev* out) {
+  if (!t || !t->data) return fail(TDP_EINVAL, "%s: null %s", fn, name);
+  if (reinterpret_cast<uintptr_t>(t->data) & 15) return fail(TDP_EINVAL, "%s: %s must be 16-byte aligned", fn, name);
+  const int64_t unit = 16 / dtype_bytes(dtype);
+  const int64_t st[2] = {t->seq_stride, t->row_stride};
+  for (int i = 0; i < 2; ++i)
+    if (st[i] < 0 || st[i] % unit != 0 || st[i] > (int64_t)1 << 40)
+      return fail(TDP_EINVAL, "%s: %s's strides must be multiples of 16 bytes (%lld elements) in [0, 2^40], got %lld",
+                  fn, name, (long long)unit, (long long)st[i]);
+  out->data = static_cast<char*>(t->data);
+  out->seq_stride = t->seq_stride;
+  out->row_stride = t->row_stride;
+  out->head_stride = 0;
+  out->heads = 1;
+  return TDP_OK;
+}
+
 }  // namespace tdp
 
 using namespace tdp;
@@ -147,6 +164,17 @@ int64_t tdp_attention_backward_workspace(const tdp_seqs* q_seqs, const tdp_seqs*
       k_heads < 1 || q_heads % k_heads != 0 || head_dim < 8)
     return 0;
   return backward_workspace(*q_seqs, *k_seqs, q_heads, k_heads, head_dim);
+}
+
+int64_t tdp_layer_norm_workspace(const tdp_seqs* seqs, int32_t channels, int32_t num_weights) {
+  const char* fn = "tdp_layer_norm_workspace";
+  if (check_seqs(fn, "seqs", seqs, nullptr) != TDP_OK) return 0;
+  if (channels < 8 || channels % 8 != 0 || channels > TDP_MAX_CHANNELS || num_weights < 1 ||
+      num_weights > seqs->num_seqs) {
+    fail(TDP_ESHAPE, "%s: channels %d or num_weights %d out of range", fn, channels, num_weights);
+    return 0;
+  }
+  return align256(layer_norm_parts(*seqs, channels, num_weights) * num_weights * 2 * channels * 4);
 }
 
 }  // extern "C"
