@@ -691,6 +691,41 @@ int tdp_attention_backward(const tdp_seqs* q_seqs, const tdp_seqs* k_seqs, const
                            const tdp_heads* dout, const tdp_heads* dq, const tdp_heads* dk, const tdp_heads* dv,
                            float scale, int32_t head_dim, int32_t dtype, void* workspace, void* stream);
 
+/* Attention with a sliding window and first rows that stay visible, for rows
+ * that come in steps (the rows of a latent frame; step 1: tokens).  Queries are
+ * the newest rows: query i of a sequence with q used queries and n used keys
+ * stands at p = i + (n - q), in step t = floor(p / step), so q_seqs = k_seqs is a
+ * whole prompt or latent and one query per sequence is a new token over its
+ * cache.  Key j < n takes part when
+ *   j < (t + 1 + ahead) * step  and  (j >= (t - back) * step  or  j < sinks).
+ * back = TDP_WINDOW_ALL reaches to the first row, ahead = 0 sees no later step.
+ * A query that sees no key (p too far before the first) gives 0 and lse
+ * -infinity.  Keys that no query of the call sees (rows that a cache has let go)
+ * may hold anything; the others must be finite.  A slot's kept conditioning rows
+ * follow its generated rows and count as later steps.  Everything else, lse
+ * and the workspace included, is as for tdp_attention (no key_bias) and
+ * tdp_attention_backward. */
+#define TDP_WINDOW_ALL (1 << 30)
+typedef struct {
+  int32_t step;   /* rows per step, 1 .. 2^24                                   */
+  int32_t back;   /* earlier steps in view, 0 .. TDP_WINDOW_ALL                 */
+  int32_t ahead;  /* later steps in view, 0 .. TDP_WINDOW_ALL                   */
+  int32_t sinks;  /* first rows in view, 0 .. TDP_WINDOW_ALL                    */
+} tdp_window;
+int64_t tdp_window_attention_workspace(const tdp_seqs* q_seqs, const tdp_seqs* k_seqs, const tdp_window* window,
+                                       int32_t q_heads, int32_t k_heads, int32_t head_dim);
+int tdp_window_attention(const tdp_seqs* q_seqs, const tdp_seqs* k_seqs, const tdp_window* window, const tdp_heads* q,
+                         const tdp_heads* k, const tdp_heads* v, const tdp_heads* out, float* lse, float scale,
+                         int32_t head_dim, int32_t dtype, void* workspace, void* stream);
+int64_t tdp_window_attention_backward_workspace(const tdp_seqs* q_seqs, const tdp_seqs* k_seqs,
+                                                const tdp_window* window, int32_t q_heads, int32_t k_heads,
+                                                int32_t head_dim);
+int tdp_window_attention_backward(const tdp_seqs* q_seqs, const tdp_seqs* k_seqs, const tdp_window* window,
+                                  const tdp_heads* q, const tdp_heads* k, const tdp_heads* v, const tdp_heads* out,
+                                  const float* lse, const tdp_heads* dout, const tdp_heads* dq, const tdp_heads* dk,
+                                  const tdp_heads* dv, float scale, int32_t head_dim, int32_t dtype, void* workspace,
+                                  void* stream);
+
 /* ---- the layer around the attention --------------------------------------- */
 
 /* What a denoising transformer's layer computes on the same rows before and

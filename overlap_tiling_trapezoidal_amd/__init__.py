@@ -24,7 +24,7 @@ DEVICE_FUNCTIONS = ("tdp_extract", "tdp_extract_noalloc", "tdp_set_lookback_poll
                     "tdp_extract_positions", "tdp_extract_latent", "tdp_pipeline_latent_step", "tdp_blend",
                     "tdp_blend_tile", "tdp_blend_finish", "tdp_pixel_blend", "tdp_rope_apply", "tdp_qk_norm_rope",
                     "tdp_qk_norm_rope_backward", "tdp_attention", "tdp_attention_backward", "tdp_layer_norm",
-                    "tdp_layer_norm_backward")
+                    "tdp_layer_norm_backward", "tdp_window_attention", "tdp_window_attention_backward")
 HEADER_PATH = os.path.join(os.path.dirname(_HERE), "include", "tdp.h")
 
 # ---- constants (mirror include/tdp.h) --------------------------------------
@@ -46,6 +46,7 @@ TDP_POINT_START = 1
 TDP_MAX_ROPE_DIM = 256
 TDP_MAX_ATTENTION_DIM = 128
 TDP_MAX_CHANNELS = 8192
+TDP_WINDOW_ALL = 1 << 30
 
 _DTYPES = {"f32": TDP_F32, "float32": TDP_F32, "bf16": TDP_BF16, "bfloat16": TDP_BF16}
 
@@ -155,6 +156,10 @@ class tdp_heads(ctypes.Structure):
     ]
 
 
+class tdp_window(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("step", "back", "ahead", "sinks")]
+
+
 class tdp_rows(ctypes.Structure):
     _fields_ = [
         ("data", ctypes.c_void_p),
@@ -193,7 +198,7 @@ def load_library(path: str = LIB_PATH):
     lib = ctypes.CDLL(path)
     vp, i32, i32p = ctypes.c_void_p, ctypes.c_int32, ctypes.POINTER(ctypes.c_int32)
     f32, sq, hd = ctypes.c_float, ctypes.POINTER(tdp_seqs), ctypes.POINTER(tdp_heads)
-    rw = ctypes.POINTER(tdp_rows)
+    rw, wn = ctypes.POINTER(tdp_rows), ctypes.POINTER(tdp_window)
     sig = {
         "tdp_plan_create": (ctypes.c_int, [ctypes.POINTER(tdp_config), ctypes.POINTER(vp)]),
         "tdp_plan_create_rank": (ctypes.c_int, [ctypes.POINTER(tdp_config), i32, i32, ctypes.POINTER(vp)]),
@@ -239,6 +244,11 @@ def load_library(path: str = LIB_PATH):
         "tdp_attention_backward_workspace": (ctypes.c_int64, [sq, sq, i32, i32, i32]),
         "tdp_attention_backward": (ctypes.c_int, [sq, sq, hd, hd, hd, vp, hd, vp, hd, hd, hd, hd, f32, i32, i32, vp,
                                                   vp]),
+        "tdp_window_attention_workspace": (ctypes.c_int64, [sq, sq, wn, i32, i32, i32]),
+        "tdp_window_attention": (ctypes.c_int, [sq, sq, wn, hd, hd, hd, hd, vp, f32, i32, i32, vp, vp]),
+        "tdp_window_attention_backward_workspace": (ctypes.c_int64, [sq, sq, wn, i32, i32, i32]),
+        "tdp_window_attention_backward": (ctypes.c_int, [sq, sq, wn, hd, hd, hd, hd, vp, hd, hd, hd, hd, f32, i32, i32,
+                                                         vp, vp]),
         "tdp_layer_norm": (ctypes.c_int, [sq, rw, vp, vp, i32, rw, f32, i32, i32, vp]),
         "tdp_layer_norm_workspace": (ctypes.c_int64, [sq, i32, i32]),
         "tdp_layer_norm_backward": (ctypes.c_int, [sq, rw, vp, i32, rw, rw, vp, vp, f32, i32, i32, vp, vp]),
@@ -1073,6 +1083,73 @@ def tdp_attention_backward(q_seqs: Sequences, k_seqs: Sequences, q, k, v, out, l
         _ptr(workspace, "workspace", torch.uint8, need, dev), _stream_handle(stream, dev)))
 
 
+def make_window(step=1, back=None, ahead=0, sinks=0) -> tdp_window:
+    """A window over steps of ``step`` rows: ``back`` earlier and ``ahead`` later steps in view
+    (None: all of them), the first ``sinks`` rows always."""
+    every = lambda n: TDP_WINDOW_ALL if n is None else n  # noqa: E731
+    return tdp_window(step, every(back), every(ahead), sinks)
+
+
+def _on(device, call, *args):
+    """A library call with `device` current, as its launches need."""
+    import torch
+    if device.index is None or device.index == torch.cuda.current_device():
+        return _check(call(*args))
+    with torch.cuda.device(device):
+        return _check(call(*args))
+
+
+def allocate_window_attention_workspace(q_seqs: Sequences, k_seqs: Sequences, window: tdp_window, q_heads: int,
+                                        k_heads: int, head_dim: int, device="cuda"):
+    """Workspace of tdp_window_attention, or None where it needs none."""
+    import torch
+    n = load_library().tdp_window_attention_workspace(ctypes.byref(q_seqs.c), ctypes.byref(k_seqs.c),
+                                                      ctypes.byref(window), q_heads, k_heads, head_dim)
+    return torch.empty(n, dtype=torch.uint8, device=torch.device(device)) if n else None
+
+
+def allocate_window_attention_backward_workspace(q_seqs: Sequences, k_seqs: Sequences, window: tdp_window,
+                                                 q_heads: int, k_heads: int, head_dim: int, device="cuda"):
+    import torch
+    n = load_library().tdp_window_attention_backward_workspace(
+        ctypes.byref(q_seqs.c), ctypes.byref(k_seqs.c), ctypes.byref(window), q_heads, k_heads, head_dim)
+    if n <= 0:
+        raise TdpError(TDP_EINVAL, tdp_last_error())
+    return torch.empty(n, dtype=torch.uint8, device=torch.device(device))
+
+
+def tdp_window_attention(q_seqs: Sequences, k_seqs: Sequences, window: tdp_window, q, k, v, out, lse=None, scale=None,
+                         workspace=None, stream=None):
+    """Enqueue attention within a window (scale: 1 / sqrt(head_dim) by default); the queries are
+    the newest rows of each sequence.  ``lse`` (heads, rows) fp32 is wanted by the backward."""
+    import torch
+    lib, ref, D, dev = load_library(), ctypes.byref, q.shape[-1], q.device
+    sq, sk = _heads(q, "q", q_seqs, D, q), _heads(k, "k", k_seqs, D, q)
+    need = lib.tdp_window_attention_workspace(ref(q_seqs.c), ref(k_seqs.c), ref(window), sq.heads, sk.heads, D)
+    _on(dev, lib.tdp_window_attention, ref(q_seqs.c), ref(k_seqs.c), ref(window), ref(sq), ref(sk),
+        ref(_heads(v, "v", k_seqs, D, q)), ref(_heads(out, "out", q_seqs, D, q, True)),
+        _vec(lse, "lse", torch.float32, sq.heads * q_seqs.total_rows, dev), D ** -0.5 if scale is None else scale, D,
+        _dtype_code(q, "q"), _ptr(workspace, "workspace", torch.uint8, need, dev) if need else ctypes.c_void_p(None),
+        _stream_handle(stream, dev))
+
+
+def tdp_window_attention_backward(q_seqs: Sequences, k_seqs: Sequences, window: tdp_window, q, k, v, out, lse, dout,
+                                  dq, dk, dv, workspace, scale=None, stream=None):
+    """Enqueue the gradients of tdp_window_attention; ``out`` and ``lse`` are its results."""
+    import torch
+    lib, ref, D, dev = load_library(), ctypes.byref, q.shape[-1], q.device
+    sq, sk = _heads(q, "q", q_seqs, D, q), _heads(k, "k", k_seqs, D, q)
+    need = lib.tdp_window_attention_backward_workspace(ref(q_seqs.c), ref(k_seqs.c), ref(window), sq.heads, sk.heads,
+                                                       D)
+    _on(dev, lib.tdp_window_attention_backward, ref(q_seqs.c), ref(k_seqs.c), ref(window), ref(sq), ref(sk),
+        ref(_heads(v, "v", k_seqs, D, q)), ref(_heads(out, "out", q_seqs, D, q)),
+        _ptr(lse, "lse", torch.float32, sq.heads * q_seqs.total_rows, dev),
+        ref(_heads(dout, "dout", q_seqs, D, q)), ref(_heads(dq, "dq", q_seqs, D, q, True)),
+        ref(_heads(dk, "dk", k_seqs, D, q, True)), ref(_heads(dv, "dv", k_seqs, D, q, True)),
+        D ** -0.5 if scale is None else scale, D, _dtype_code(q, "q"),
+        _ptr(workspace, "workspace", torch.uint8, need, dev), _stream_handle(stream, dev))
+
+
 # ---------------------------------------------------------------------------
 # The layer around the attention: layer norm
 # ---------------------------------------------------------------------------
@@ -1127,15 +1204,6 @@ def _rows(t, name, seqs: Sequences, features, like, written=False):
         if len(seqs._layouts) < 64:
             seqs._layouts[key] = lay
     return tdp_rows(t.data_ptr(), *lay)
-
-
-def _on(device, call, *args):
-    """A library call with `device` current, as its launches need."""
-    import torch
-    if device.index is None or device.index == torch.cuda.current_device():
-        return _check(call(*args))
-    with torch.cuda.device(device):
-        return _check(call(*args))
 
 
 def _weight_sets(t, name, channels, sets, device):

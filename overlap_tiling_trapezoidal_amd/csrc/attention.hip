@@ -23,6 +23,11 @@
 // of the LDS tile (bf16: the transposing 64-bit LDS read, four rows of 16
 // columns per 16 lanes).
 //
+// With a window (WIN) each query sees an interval of keys and the first rows.  A
+// block of queries walks the key blocks that any of them sees, first rows first,
+// and only blocks that some of them do not see whole are masked; a block of keys
+// walks the rows that see any of them, which is an interval too.
+//
 // fp32 tensors run the same code on fp32 matrix instructions, eight
 // contractions of 2 for one of 16.
 //
@@ -154,6 +159,8 @@ struct AttnArgs {
   int32_t D, group, splits, m_max;  // m_max: query entries of the longest sequence
   FastDiv by_group;
   uint32_t blocks, tiles;  // row blocks per (sequence, key head); all work items
+  WindowDev win;
+  uint32_t split_blocks;   // WIN: leading blocks of keys whose rows are split (dk, dv)
 };
 
 // Workgroups are dealt round-robin to the eight XCDs; each gets a contiguous
@@ -209,6 +216,15 @@ struct Direct {
         __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (TDP_LDS void*)(lds + (n * kTok + wave * 64) * 16), 16,
                                                  EXACT && row_of(n) >= left ? 0xfffffff0u : off[n], 0, 0, 0);
 #endif
+  }
+  // Clear what this lane has loaded of keys that no row of a window sees.
+  template <typename S>
+  __device__ inline void clear_holes(const S& seen, int j0, char* lds) const {
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+      const int i = threadIdx.x + n * kTok;
+      if (i < kSlots && seen.hole(j0 + i / L::kChunks)) *reinterpret_cast<u32x4*>(lds + i * 16) = u32x4{0, 0, 0, 0};
+    }
   }
   // Clear what this lane has loaded of a block's keys that take no part: their
   // rows may hold anything, and a weight of zero would not remove a NaN.
@@ -314,6 +330,26 @@ __device__ inline Place place(const AttnArgs& A, uint32_t item) {
   return p;
 }
 
+// The same for dk and dv with a window: the first split_blocks blocks of a head's
+// keys, which hold the first rows and are seen by far more queries than the
+// others, are split, the others are not.
+__device__ inline Place place_split(const AttnArgs& A, uint32_t item) {
+  Place p;
+  const uint32_t lead = A.split_blocks * A.splits, per = lead + A.blocks - A.split_blocks;
+  const uint32_t sh = item / per, rest = item - sh * per;
+  p.split = rest < lead ? rest / A.split_blocks : 0;
+  p.blk = rest < lead ? rest - p.split * A.split_blocks : rest - lead + A.split_blocks;
+  p.s = sh / A.k.heads;
+  p.hk = sh - p.s * A.k.heads;
+  return p;
+}
+// Keys of a sequence whose sums pass through the workspace.
+template <bool WIN>
+__host__ __device__ inline int split_rows(const AttnArgs& A) {
+  return WIN && (int64_t)A.split_blocks * kAttnBlockQ < A.ks.max_rows ? (int)A.split_blocks * kAttnBlockQ
+                                                                     : A.ks.max_rows;
+}
+
 // A block's scores as the softmax takes them: with a bias in powers of two
 // (scaled and biased, the bias -infinity where a key takes no part), otherwise
 // raw, and -infinity for keys past the end.
@@ -329,6 +365,53 @@ __device__ inline void mask_scores(f32x16& st, const float* bl, float c, int j0,
   }
 }
 
+// What the rows of a query block see of the keys: rows [row0, row1] of a sequence,
+// and per lane its own row.  Keys [0, first) and [lo, hi) cover all that any of the
+// rows sees; `at(t)` is the t-th of the `n` key blocks that hold them.
+template <int KB>
+struct Seen {
+  int lo, hi, first;        // of all rows
+  int lo_max, hi_min;       // keys [lo_max, hi_min) and below first_min are seen by every row
+  int first_min;
+  int my_lo, my_hi, sinks;  // the lane's row
+  int lead, skip, n;        // blocks of first rows; blocks passed over behind them
+  __device__ inline void init(const WindowDev& w, int qlen, int klen, int row0, int row1, int row) {
+    const int off = klen - qlen;
+    sinks = w.sinks;
+    const KeySpan a = key_span(w, row0 + off, klen), b = key_span(w, row1 + off, klen),
+                  c = key_span(w, (row < row1 ? row : row1) + off, klen);
+    lo = a.lo;
+    hi = b.hi;
+    first = sinks < hi ? sinks : hi;
+    lo_max = b.lo;
+    hi_min = a.hi;
+    first_min = sinks < hi_min ? sinks : hi_min;
+    my_lo = c.lo;
+    my_hi = c.hi;
+    lead = ((first < lo ? first : lo) + KB - 1) / KB;
+    const int w0 = lo / KB > lead ? lo / KB : lead, w1 = (hi + KB - 1) / KB;
+    skip = w0 - lead;
+    n = lead + (w1 > w0 ? w1 - w0 : 0);
+  }
+  __device__ inline int at(int t) const { return t < lead ? t : t + skip; }
+  // some row does not see some key of the 64 from j0 on
+  __device__ inline bool edge(int j0, int keys) const {
+    return !((j0 >= lo_max && j0 + keys <= hi_min) || j0 + keys <= first_min);
+  }
+  __device__ inline void mask(f32x16& st, int j0, int h) const {
+    const int at = j0 + 4 * h, past = my_hi - at, from = my_lo - at, lead = sinks - at;
+#pragma unroll
+    for (int r = 0; r < 16; ++r) {
+      const int j = 8 * (r >> 2) + (r & 3);
+      st[r] = ((j >= past) | ((j < from) & (j >= lead))) ? -INFINITY : st[r];
+    }
+  }
+  // Keys of a block that no row sees lie before its window and behind the first
+  // rows, or past `hi`, where the loads end.  They may hold anything.
+  __device__ inline bool holes(int j0) const { return j0 < lo && j0 + KB > first; }
+  __device__ inline bool hole(int j) const { return j >= first && j < lo; }
+};
+
 // Forward: 128 query entries of one key head per workgroup, 32 per wave.  K and
 // V blocks of 64 keys come through two LDS buffers each, loaded one step ahead.
 // A step multiplies block b's scores while the softmax and the product with V
@@ -338,7 +421,7 @@ __device__ inline void mask_scores(f32x16& st, const float* bl, float c, int j0,
 // library product's rate; the matrix pipes are busy 68% of the time, at a clock
 // that the card lowers to about 1.7 GHz under this load.  Twice the query entries
 // per wave need all 512 registers and spill: 13.0 ms.
-template <int T, int DP, bool BIAS>
+template <int T, int DP, bool BIAS, bool WIN>
 __global__ __launch_bounds__(kTok, T != TDP_BF16 ? 1 : DP == 64 ? 3 : 2) void attn_forward_kernel(const AttnArgs A) {
   typedef Tile<T, DP> L;
   typedef typename Mat<T>::Frag Frag;
@@ -386,7 +469,14 @@ __global__ __launch_bounds__(kTok, T != TDP_BF16 ? 1 : DP == 64 ? 3 : 2) void at
   const int64_t krow = eb * A.k.row_stride, vrow = eb * A.v.row_stride;
   const int d_bytes = A.D * eb;
   Biases<kAttnBlockK> biases = {BIAS ? A.bias + kr.row0 : nullptr, bl, kr.len, 0.0f};
-  const int nb = (kr.len + kAttnBlockK - 1) / kAttnBlockK;
+  Seen<kAttnBlockK> seen;
+  if constexpr (WIN) {
+    const int end = (m0 + kAttnBlockQ < mlen ? m0 + kAttnBlockQ : mlen) - 1;
+    seen.init(A.win, qr.len, kr.len, (int)fastdiv((uint32_t)m0, A.by_group),
+              (int)fastdiv((uint32_t)(end < m0 ? m0 : end), A.by_group), row);
+  }
+  const int klen = WIN ? seen.hi : kr.len;
+  const int nb = WIN ? seen.n : (kr.len + kAttnBlockK - 1) / kAttnBlockK;
   const int per = (nb + A.splits - 1) / A.splits;
   const int b0 = pl.split * per;
   const int b1 = m0 >= mlen ? b0 : (b0 + per < nb ? b0 + per : nb);
@@ -423,9 +513,17 @@ __global__ __launch_bounds__(kTok, T != TDP_BF16 ? 1 : DP == 64 ? 3 : 2) void at
       }
     }
   };
+  // block b of the walk begins with this key
+  auto key0 = [&](int b) __attribute__((always_inline)) { return (WIN ? seen.at(b) : b) * kAttnBlockK; };
   // take block b's scores over: mask them, and move the maximum if they exceed it
   auto take = [&](int b, f32x16* sn) __attribute__((always_inline)) {
-    if (BIAS || (b + 1) * kAttnBlockK > kr.len) {
+    if constexpr (WIN) {
+      const int j0 = key0(b);
+      if (seen.edge(j0, kAttnBlockK)) {
+#pragma unroll
+        for (int kt = 0; kt < KT; ++kt) seen.mask(sn[kt], j0 + kt * 32, h);
+      }
+    } else if (BIAS || (b + 1) * kAttnBlockK > kr.len) {
 #pragma unroll
       for (int kt = 0; kt < KT; ++kt)
         mask_scores<BIAS>(sn[kt], biases.at(b) + kt * 32, c, b * kAttnBlockK + kt * 32, kr.len, h);
@@ -459,8 +557,8 @@ __global__ __launch_bounds__(kTok, T != TDP_BF16 ? 1 : DP == 64 ? 3 : 2) void at
   // block b: its K in kc, the block before's V in vp; K of b + 1 goes to kn, V of b to vc
   auto step = [&](int b, const char* kc, char* kn, char* vp, char* vc) __attribute__((always_inline)) {
     if constexpr (BIAS) biases.advance(b);
-    if (b + 1 < b1) kd.load(kb, krow, d_bytes, (b + 1) * kAttnBlockK, kr.len, wave, kn);
-    vd.load(vb, vrow, d_bytes, b * kAttnBlockK, kr.len, wave, vc);
+    if (b + 1 < b1) kd.load(kb, krow, d_bytes, key0(b + 1), klen, wave, kn);
+    vd.load(vb, vrow, d_bytes, key0(b), klen, wave, vc);
     f32x16 sn[KT];
     scores(kc, sn);
     if (b > b0) values(vp);
@@ -470,10 +568,13 @@ __global__ __launch_bounds__(kTok, T != TDP_BF16 ? 1 : DP == 64 ? 3 : 2) void at
       vd.clear(biases.at(b), vc);
       if (b + 1 < b1) kd.clear(biases.at(b + 1), kn);
     }
+    // of K they leave scores that are masked
+    if constexpr (WIN)
+      if (seen.holes(key0(b))) vd.clear_holes(seen, key0(b), vc);
     __syncthreads();
   };
   if (b0 < b1) {
-    kd.load(kb, krow, d_bytes, b0 * kAttnBlockK, kr.len, wave, k0);
+    kd.load(kb, krow, d_bytes, key0(b0), klen, wave, k0);
     if constexpr (BIAS) biases.start(b0);
     wait_loads();
     __syncthreads();
@@ -606,7 +707,7 @@ __device__ inline float neg_lse(float lse) {
 // spill in the loop (gradients of 8 x 480 rows on 343 keys, 9 heads of 96: 70 us
 // against 81; of 4 x 2240 rows on 512 keys, 16 heads of 128: 247 against 302).
 constexpr int kDqKeys = 64;
-template <int T, int DP, bool BIAS>
+template <int T, int DP, bool BIAS, bool WIN>
 __global__ __launch_bounds__(kTok, T == TDP_BF16 && !(BIAS && DP == 128) ? 2 : 1) void attn_dq_kernel(const AttnArgs A) {
   typedef Tile<T, DP> L;
   typedef typename Mat<T>::Frag Frag;
@@ -658,14 +759,22 @@ __global__ __launch_bounds__(kTok, T == TDP_BF16 && !(BIAS && DP == 128) ? 2 : 1
   const int64_t krow = eb * A.k.row_stride, vrow = eb * A.v.row_stride;
   const int d_bytes = A.D * eb;
   Biases<kDqKeys> biases = {BIAS ? A.bias + kr.row0 : nullptr, bl, kr.len, 0.0f};
-  const int nb = m0 >= mlen ? 0 : (kr.len + kDqKeys - 1) / kDqKeys;
+  Seen<kDqKeys> seen;
+  if constexpr (WIN) {
+    const int end = (m0 + kAttnBlockQ < mlen ? m0 + kAttnBlockQ : mlen) - 1;
+    seen.init(A.win, qr.len, kr.len, (int)fastdiv((uint32_t)m0, A.by_group),
+              (int)fastdiv((uint32_t)(end < m0 ? m0 : end), A.by_group), row);
+  }
+  const int klen = WIN ? seen.hi : kr.len;
+  const int nb = m0 >= mlen ? 0 : WIN ? seen.n : (kr.len + kDqKeys - 1) / kDqKeys;
+  auto key0 = [&](int b) __attribute__((always_inline)) { return (WIN ? seen.at(b) : b) * kDqKeys; };
 
   Direct<T, DP, kDqKeys> kd, vd;
   kd.init((uint32_t)krow, d_bytes);
   vd.init((uint32_t)vrow, d_bytes);
   auto load = [&](int b, char* kn, char* vn) __attribute__((always_inline)) {
-    kd.load(kb, krow, d_bytes, b * kDqKeys, kr.len, wave, kn);
-    vd.load(vb, vrow, d_bytes, b * kDqKeys, kr.len, wave, vn);
+    kd.load(kb, krow, d_bytes, key0(b), klen, wave, kn);
+    vd.load(vb, vrow, d_bytes, key0(b), klen, wave, vn);
   };
   // 32 keys from key k0 of the block in kl and vl
   auto part = [&](int b, int r0, char* kl, char* vl) __attribute__((always_inline)) {
@@ -680,7 +789,12 @@ __global__ __launch_bounds__(kTok, T == TDP_BF16 && !(BIAS && DP == 128) ? 2 : 1
     for (int kk = 0; kk < KD; ++kk) st = Mat<T>::mma(ka[kk], qf[kk], st);
 #pragma unroll
     for (int kk = 0; kk < KD; ++kk) dp = Mat<T>::mma(va[kk], gf[kk], dp);
-    if (!BIAS && b * kDqKeys + r0 + 32 > kr.len) mask_scores<false>(st, nullptr, c, b * kDqKeys + r0, kr.len, h);
+    if constexpr (WIN) {
+      const int j0 = key0(b) + r0;
+      if (seen.edge(j0, 32)) seen.mask(st, j0, h);
+    } else if (!BIAS && b * kDqKeys + r0 + 32 > kr.len) {
+      mask_scores<false>(st, nullptr, c, b * kDqKeys + r0, kr.len, h);
+    }
     float ds[16];
 #pragma unroll
     for (int r = 0; r < 16; ++r)
@@ -708,6 +822,12 @@ __global__ __launch_bounds__(kTok, T == TDP_BF16 && !(BIAS && DP == 128) ? 2 : 1
         vd.clear(biases.at(b + 1), vn);
       }
     }
+    if constexpr (WIN) {
+      if (b + 1 < nb && seen.holes(key0(b + 1))) {
+        kd.clear_holes(seen, key0(b + 1), kn);
+        vd.clear_holes(seen, key0(b + 1), vn);
+      }
+    }
     __syncthreads();
   };
   if (nb) {
@@ -719,6 +839,13 @@ __global__ __launch_bounds__(kTok, T == TDP_BF16 && !(BIAS && DP == 128) ? 2 : 1
       kd.clear(biases.at(0), k0);
       vd.clear(biases.at(0), v0);
       __syncthreads();
+    }
+    if constexpr (WIN) {
+      if (seen.holes(key0(0))) {
+        kd.clear_holes(seen, key0(0), k0);
+        vd.clear_holes(seen, key0(0), v0);
+        __syncthreads();
+      }
     }
     int b = 0;
     for (; b + 1 < nb; b += 2) {
@@ -763,7 +890,7 @@ __device__ inline void load_stats(const f32x2* from, int left, int wave, int lan
 // bias), so one wave per SIMD has nothing but its own instructions to cover its
 // waits, and the 1152 workgroups are 4.5 rounds of the 256 places, run as five.
 constexpr int kDkvRows = 64;
-template <int T, int DP, bool BIAS>
+template <int T, int DP, bool BIAS, bool WIN>
 __global__ __launch_bounds__(kTok, T == TDP_BF16 && DP <= 64 ? 2 : 1) void attn_dkv_kernel(const AttnArgs A) {
   typedef Tile<T, DP> L;
   typedef typename Mat<T>::Frag Frag;
@@ -780,7 +907,7 @@ __global__ __launch_bounds__(kTok, T == TDP_BF16 && DP <= 64 ? 2 : 1) void attn_
   __shared__ __align__(16) float s2[2 * kDkvRows];
   const uint32_t item = xcd_item(A.tiles);
   if (item >= A.tiles) return;
-  const Place pl = place(A, item);
+  const Place pl = WIN ? place_split(A, item) : place(A, item);
   const SeqRows qr = seq_rows(A.qs, pl.s), kr = seq_rows(A.ks, pl.s);
   const int j0 = pl.blk * kAttnBlockQ;
   if (j0 >= kr.cap) return;
@@ -793,6 +920,22 @@ __global__ __launch_bounds__(kTok, T == TDP_BF16 && DP <= 64 ? 2 : 1) void attn_
     bi = live ? A.bias[kr.row0 + j] : -INFINITY;
     bi = bi <= kBiasOut ? -INFINITY : bi * kLog2e;
     live = live && bi != -INFINITY;
+  }
+  // rows [ilo, ihi) see the lane's key; [all_lo, all_hi) the block's some key,
+  // [every_lo, every_hi) every one
+  int ilo = 0, ihi = 0, all_lo = 0, all_hi = qr.len, every_lo = 0, every_hi = 0;
+  if constexpr (WIN) {
+    const int off = kr.len - qr.len, jend = (j0 + kAttnBlockQ < kr.len ? j0 + kAttnBlockQ : kr.len) - 1;
+    const RowSpan me = row_span(A.win, j, off, qr.len), a = row_span(A.win, j0, off, qr.len),
+                  z = row_span(A.win, jend, off, qr.len);
+    ilo = me.lo;
+    ihi = me.hi;
+    live = live && ilo < ihi;
+    all_lo = a.lo;
+    all_hi = j0 < A.win.sinks ? qr.len : z.hi;
+    if (all_hi < all_lo) all_hi = all_lo;
+    every_lo = z.lo;
+    every_hi = jend < A.win.sinks ? qr.len : row_span(A.win, j0 > A.win.sinks ? j0 : A.win.sinks, off, qr.len).hi;
   }
   Frag kf[KD], vf[KD];
   load_frags<T, DP>(live ? A.k.data + eb * (seq_base(A.ks, A.k, pl.s, kr) + j * A.k.row_stride +
@@ -808,9 +951,11 @@ __global__ __launch_bounds__(kTok, T == TDP_BF16 && DP <= 64 ? 2 : 1) void attn_
 
   // blocks of all heads of the group in a row: block b is rows
   // (b mod per_head) * 64 of head b / per_head
-  const int per_head = (qr.len + kDkvRows - 1) / kDkvRows;
+  const int first = WIN ? all_lo / kDkvRows : 0;  // block of rows
+  const int per_head = (all_hi + kDkvRows - 1) / kDkvRows - first;
   const int all = j0 < kr.len ? per_head * A.group : 0;
-  const int per = (all + A.splits - 1) / A.splits;
+  const int splits = !WIN || (uint32_t)pl.blk < A.split_blocks ? A.splits : 1;
+  const int per = (all + splits - 1) / splits;
   const int b0 = pl.split * per, b1 = b0 + per < all ? b0 + per : all;
 
   Direct<T, DP, kDkvRows, true> qd, gd;
@@ -834,7 +979,7 @@ __global__ __launch_bounds__(kTok, T == TDP_BF16 && DP <= 64 ? 2 : 1) void attn_
     gd.load(ghead, grow, d_bytes, gr, qr.len, wave, gn);
     load_stats(shead + gr, left_next, wave, lane, sn);
     gr += kDkvRows;
-    if (gr >= qr.len) seek(1, 0);
+    if (gr >= all_hi) seek(1, first * kDkvRows);
   };
   // What a half needs from LDS is read ahead of its products, behind barriers
   // for the compiler's scheduler: left to itself it reads each operand right
@@ -863,10 +1008,25 @@ __global__ __launch_bounds__(kTok, T == TDP_BF16 && DP <= 64 ? 2 : 1) void attn_
   auto values = [&](char* ql, char* gl, const f32x4* x, int r0, int rows, const f32x16& st,
                     const f32x16& dp) __attribute__((always_inline)) {
     float p[16], ds[16];
+    const int row0 = qr.len - rows + r0;  // WIN: the half's first row
+    const bool edge = WIN && !(row0 >= every_lo && row0 + 32 <= every_hi);
+    float nl[16];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      nl[2 * i] = x[i][0];
+      nl[2 * i + 1] = x[i][2];
+    }
+    if (edge) {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const int row = 8 * (i >> 2) + (i & 3);
+        nl[i] = ((row < ilo - row0 - 4 * h) | (row >= ihi - row0 - 4 * h)) ? -INFINITY : nl[i];
+      }
+    }
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const int r = 2 * i, row = r0 + 8 * (i >> 1) + 4 * h + 2 * (i & 1);
-      float n0 = x[i][0], n1 = x[i][2];
+      float n0 = nl[r], n1 = nl[r + 1];
       if constexpr (BIAS) {
         // rows past the end have zeros for Q, dout and their statistics, which
         // a weight of one leaves at zero, but not one that a bias makes infinite
@@ -940,7 +1100,7 @@ __global__ __launch_bounds__(kTok, T == TDP_BF16 && DP <= 64 ? 2 : 1) void attn_
   };
   if (b0 < b1) {
     const int head0 = b0 / per_head;
-    seek(pl.hk * A.group + head0, (b0 - head0 * per_head) * kDkvRows);
+    seek(pl.hk * A.group + head0, (first + b0 - head0 * per_head) * kDkvRows);
     load(q0, g0, s0);
     wait_loads();
     __syncthreads();
@@ -986,9 +1146,9 @@ __global__ __launch_bounds__(kTok, T == TDP_BF16 && DP <= 64 ? 2 : 1) void attn_
 #pragma unroll
     for (int nd = 0; nd < ND; ++nd) dk[nd] = dv[nd] = zero16();
   }
-  if (A.splits > 1) {
-    const int64_t e = (((int64_t)pl.split * A.ks.S + pl.s) * A.k.heads + pl.hk) * A.ks.max_rows + j;
-    const int64_t n = (int64_t)A.splits * A.ks.S * A.k.heads * A.ks.max_rows;
+  if (splits > 1) {
+    const int64_t e = (((int64_t)pl.split * A.ks.S + pl.s) * A.k.heads + pl.hk) * split_rows<WIN>(A) + j;
+    const int64_t n = (int64_t)A.splits * A.ks.S * A.k.heads * split_rows<WIN>(A);
     store_column<TDP_F32, ND>(reinterpret_cast<char*>(A.ws + e * DP), h, DP, dk, A.scale);
     store_column<TDP_F32, ND>(reinterpret_cast<char*>(A.ws + (n + e) * DP), h, DP, dv, 1.0f);
     return;
@@ -1000,17 +1160,17 @@ __global__ __launch_bounds__(kTok, T == TDP_BF16 && DP <= 64 ? 2 : 1) void attn_
 }
 
 // Sum the parts of dk and dv in order: a thread per eight elements of a key.
-template <int T, int DP>
+template <int T, int DP, bool WIN>
 __global__ __launch_bounds__(kTok) void attn_sum_kernel(const AttnArgs A) {
   constexpr int kPer = DP / 8;
-  const int64_t n1 = (int64_t)A.ks.S * A.k.heads * A.ks.max_rows;
+  const int64_t n1 = (int64_t)A.ks.S * A.k.heads * split_rows<WIN>(A);
   const int64_t t = (int64_t)blockIdx.x * kTok + threadIdx.x;
   const int64_t which = t / (n1 * kPer);  // dk, then dv
   if (which > 1) return;
   const int64_t e = t / kPer - which * n1;
   const int d = (int)(t % kPer) * 8;
-  const int64_t sh = e / A.ks.max_rows;
-  const int j = (int)(e - sh * A.ks.max_rows), s = (int)(sh / A.k.heads), hk = (int)(sh - (int64_t)s * A.k.heads);
+  const int64_t sh = e / split_rows<WIN>(A);
+  const int j = (int)(e - sh * split_rows<WIN>(A)), s = (int)(sh / A.k.heads), hk = (int)(sh - (int64_t)s * A.k.heads);
   const SeqRows kr = seq_rows(A.ks, s);
   if (j >= kr.cap || d >= A.D) return;
   float x[8] = {0, 0, 0, 0, 0, 0, 0, 0};
@@ -1025,24 +1185,25 @@ __global__ __launch_bounds__(kTok) void attn_sum_kernel(const AttnArgs A) {
   store8<T>(out.data, seq_base(A.ks, out, s, kr) + j * out.row_stride + hk * out.head_stride + d, x);
 }
 
-template <int T, int DP, bool BIAS>
+template <int T, int DP, bool BIAS, bool WIN>
 void launch_forward(const AttnArgs& A, hipStream_t st) {
-  hipLaunchKernelGGL((attn_forward_kernel<T, DP, BIAS>), dim3(xcd_grid(A.tiles)), dim3(kTok), 0, st, A);
+  hipLaunchKernelGGL((attn_forward_kernel<T, DP, BIAS, WIN>), dim3(xcd_grid(A.tiles)), dim3(kTok), 0, st, A);
   if (A.splits > 1)
     hipLaunchKernelGGL((attn_join_kernel<T, DP>), dim3((unsigned)(A.qs.S * A.k.heads * A.m_max)), dim3(kTok), 0, st, A,
                        BIAS ? 1.0f : A.scale * kLog2e, BIAS ? kLn2 : A.scale);
 }
 
-template <int T, int DP, bool BIAS>
+template <int T, int DP, bool BIAS, bool WIN>
 void launch_backward(AttnArgs A, int splits, hipStream_t st) {
-  hipLaunchKernelGGL((attn_dq_kernel<T, DP, BIAS>), dim3(xcd_grid(A.tiles)), dim3(kTok), 0, st, A);
+  hipLaunchKernelGGL((attn_dq_kernel<T, DP, BIAS, WIN>), dim3(xcd_grid(A.tiles)), dim3(kTok), 0, st, A);
   A.blocks = (uint32_t)((A.ks.max_rows + kAttnBlockQ - 1) / kAttnBlockQ);
   A.splits = splits;
-  A.tiles = A.blocks * (uint32_t)A.ks.S * (uint32_t)A.k.heads * splits;
-  hipLaunchKernelGGL((attn_dkv_kernel<T, DP, BIAS>), dim3(xcd_grid(A.tiles)), dim3(kTok), 0, st, A);
+  if (!WIN) A.split_blocks = A.blocks;
+  A.tiles = (A.blocks + A.split_blocks * (splits - 1)) * (uint32_t)A.ks.S * (uint32_t)A.k.heads;
+  hipLaunchKernelGGL((attn_dkv_kernel<T, DP, BIAS, WIN>), dim3(xcd_grid(A.tiles)), dim3(kTok), 0, st, A);
   if (splits > 1) {
-    const int64_t n = (int64_t)A.ks.S * A.k.heads * A.ks.max_rows * 2 * (DP / 8);
-    hipLaunchKernelGGL((attn_sum_kernel<T, DP>), dim3((unsigned)((n + kTok - 1) / kTok)), dim3(kTok), 0, st, A);
+    const int64_t n = (int64_t)A.ks.S * A.k.heads * split_rows<WIN>(A) * 2 * (DP / 8);
+    hipLaunchKernelGGL((attn_sum_kernel<T, DP, WIN>), dim3((unsigned)((n + kTok - 1) / kTok)), dim3(kTok), 0, st, A);
   }
 }
 
@@ -1105,19 +1266,18 @@ int check_items(const char* fn, int64_t workgroups) {
 
 using namespace tdp;
 
+#define TDP_ATTN_KIND(call, T, DP)                \
+  do {                                            \
+    if (A.win.step) call(T, DP, false, true);     \
+    else if (A.bias) call(T, DP, true, false);    \
+    else call(T, DP, false, false);               \
+  } while (0)
 #define TDP_ATTN_DIMS(call, T)                    \
   do {                                            \
     const int dp = attention_padded_dim(head_dim); \
-    if (dp == 32) {                               \
-      if (key_bias) call(T, 32, true);            \
-      else call(T, 32, false);                    \
-    } else if (dp == 64) {                        \
-      if (key_bias) call(T, 64, true);            \
-      else call(T, 64, false);                    \
-    } else {                                      \
-      if (key_bias) call(T, 128, true);           \
-      else call(T, 128, false);                   \
-    }                                             \
+    if (dp == 32) TDP_ATTN_KIND(call, T, 32);     \
+    else if (dp == 64) TDP_ATTN_KIND(call, T, 64); \
+    else TDP_ATTN_KIND(call, T, 128);             \
   } while (0)
 #define TDP_ATTN_DISPATCH(call)                    \
   do {                                             \
@@ -1125,18 +1285,19 @@ using namespace tdp;
     else TDP_ATTN_DIMS(call, TDP_F32);             \
   } while (0)
 
-extern "C" {
+namespace tdp {
+namespace {
 
-int tdp_attention(const tdp_seqs* q_seqs, const tdp_seqs* k_seqs, const tdp_heads* q, const tdp_heads* k,
-                  const tdp_heads* v, const float* key_bias, const tdp_heads* out, float* lse, float scale,
-                  int32_t head_dim, int32_t dtype, void* workspace, void* stream) {
-  const char* fn = "tdp_attention";
+int forward(const char* fn, const tdp_seqs* q_seqs, const tdp_seqs* k_seqs, const tdp_window* window,
+            const tdp_heads* q, const tdp_heads* k, const tdp_heads* v, const float* key_bias, const tdp_heads* out,
+            float* lse, float scale, int32_t head_dim, int32_t dtype, void* workspace, void* stream) {
   AttnArgs A = {};
   int st = begin(fn, q_seqs, k_seqs, q, k, v, key_bias, out, lse, scale, head_dim, dtype, &A);
   if (st != TDP_OK) return st;
-  A.splits = attention_splits(*q_seqs, *k_seqs, q->heads, k->heads);
+  if (window) A.win = window_dev(*window);
+  A.splits = attention_splits(*q_seqs, window_keys(window, *q_seqs, *k_seqs), q->heads, k->heads);
   if (A.splits > 1 && (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 15)))
-    return fail(TDP_EINVAL, "%s: workspace must be a 16-byte aligned device pointer (tdp_attention_workspace)", fn);
+    return fail(TDP_EINVAL, "%s: workspace must be a 16-byte aligned device pointer (%s_workspace)", fn, fn);
   A.ws = static_cast<float*>(workspace);
   const int64_t tiles = (int64_t)A.blocks * q_seqs->num_seqs * k->heads * A.splits;
   const int64_t join = A.splits > 1 ? (int64_t)q_seqs->num_seqs * k->heads * A.m_max : 0;
@@ -1144,7 +1305,7 @@ int tdp_attention(const tdp_seqs* q_seqs, const tdp_seqs* k_seqs, const tdp_head
   if (st != TDP_OK) return st;
   A.tiles = (uint32_t)tiles;
   hipStream_t hs = reinterpret_cast<hipStream_t>(stream);
-#define CALL(T, DP, B) launch_forward<T, DP, B>(A, hs)
+#define CALL(T, DP, B, W) launch_forward<T, DP, B, W>(A, hs)
   TDP_ATTN_DISPATCH(CALL);
 #undef CALL
   const hipError_t e = hipGetLastError();
@@ -1152,11 +1313,10 @@ int tdp_attention(const tdp_seqs* q_seqs, const tdp_seqs* k_seqs, const tdp_head
   return TDP_OK;
 }
 
-int tdp_attention_backward(const tdp_seqs* q_seqs, const tdp_seqs* k_seqs, const tdp_heads* q, const tdp_heads* k,
-                           const tdp_heads* v, const float* key_bias, const tdp_heads* out, const float* lse,
-                           const tdp_heads* dout, const tdp_heads* dq, const tdp_heads* dk, const tdp_heads* dv,
-                           float scale, int32_t head_dim, int32_t dtype, void* workspace, void* stream) {
-  const char* fn = "tdp_attention_backward";
+int backward(const char* fn, const tdp_seqs* q_seqs, const tdp_seqs* k_seqs, const tdp_window* window,
+             const tdp_heads* q, const tdp_heads* k, const tdp_heads* v, const float* key_bias, const tdp_heads* out,
+             const float* lse, const tdp_heads* dout, const tdp_heads* dq, const tdp_heads* dk, const tdp_heads* dv,
+             float scale, int32_t head_dim, int32_t dtype, void* workspace, void* stream) {
   AttnArgs A = {};
   int st = begin(fn, q_seqs, k_seqs, q, k, v, key_bias, out, lse, scale, head_dim, dtype, &A);
   if (st == TDP_OK) st = check_heads(fn, "dout", dout, q_seqs, head_dim, dtype, &A.dout);
@@ -1171,22 +1331,65 @@ int tdp_attention_backward(const tdp_seqs* q_seqs, const tdp_seqs* k_seqs, const
     return fail(TDP_EINVAL, "%s: workspace must be a 16-byte aligned device pointer", fn);
   st = check_row_strides(fn, dtype, {dout});
   if (st != TDP_OK) return st;
+  if (window) A.win = window_dev(*window);
   A.stats = static_cast<f32x2*>(workspace);
   A.ws = reinterpret_cast<float*>(static_cast<char*>(workspace) + stats_bytes(*q_seqs, q->heads));
-  const int splits = dkv_splits(*q_seqs, *k_seqs, q->heads, k->heads);
-  const int64_t qt = A.blocks * ((int64_t)q_seqs->num_seqs * k->heads);
-  const int64_t kt = dkv_blocks(*k_seqs, k->heads) * splits;
-  const int64_t sum = splits > 1 ? ((int64_t)k_seqs->num_seqs * k->heads * k_seqs->max_rows * 32 + kTok - 1) / kTok : 0;
+  const DkvSplit sp = dkv_split(window, *q_seqs, *k_seqs, q->heads, k->heads);
+  A.split_blocks = (uint32_t)sp.blocks;
+  const int64_t heads = (int64_t)k_seqs->num_seqs * k->heads;
+  const int64_t qt = A.blocks * heads;
+  const int64_t kt = dkv_blocks(*k_seqs, k->heads) + sp.blocks * heads * (sp.n - 1);
+  const int64_t sum = sp.n > 1 ? (heads * sp.rows * 32 + kTok - 1) / kTok : 0;
   st = check_items(fn, qt > kt ? (qt > sum ? qt : sum) : (kt > sum ? kt : sum));
   if (st != TDP_OK) return st;
   A.tiles = (uint32_t)qt;
   hipStream_t hs = reinterpret_cast<hipStream_t>(stream);
-#define CALL(T, DP, B) launch_backward<T, DP, B>(A, splits, hs)
+#define CALL(T, DP, B, W) launch_backward<T, DP, B, W>(A, sp.n, hs)
   TDP_ATTN_DISPATCH(CALL);
 #undef CALL
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return fail(TDP_EHIP, "%s: kernel launch failed: %s", fn, hipGetErrorString(e));
   return TDP_OK;
+}
+
+}  // namespace
+}  // namespace tdp
+
+extern "C" {
+
+int tdp_attention(const tdp_seqs* q_seqs, const tdp_seqs* k_seqs, const tdp_heads* q, const tdp_heads* k,
+                  const tdp_heads* v, const float* key_bias, const tdp_heads* out, float* lse, float scale,
+                  int32_t head_dim, int32_t dtype, void* workspace, void* stream) {
+  return forward("tdp_attention", q_seqs, k_seqs, nullptr, q, k, v, key_bias, out, lse, scale, head_dim, dtype,
+                 workspace, stream);
+}
+
+int tdp_attention_backward(const tdp_seqs* q_seqs, const tdp_seqs* k_seqs, const tdp_heads* q, const tdp_heads* k,
+                           const tdp_heads* v, const float* key_bias, const tdp_heads* out, const float* lse,
+                           const tdp_heads* dout, const tdp_heads* dq, const tdp_heads* dk, const tdp_heads* dv,
+                           float scale, int32_t head_dim, int32_t dtype, void* workspace, void* stream) {
+  return backward("tdp_attention_backward", q_seqs, k_seqs, nullptr, q, k, v, key_bias, out, lse, dout, dq, dk, dv,
+                  scale, head_dim, dtype, workspace, stream);
+}
+
+int tdp_window_attention(const tdp_seqs* q_seqs, const tdp_seqs* k_seqs, const tdp_window* window, const tdp_heads* q,
+                         const tdp_heads* k, const tdp_heads* v, const tdp_heads* out, float* lse, float scale,
+                         int32_t head_dim, int32_t dtype, void* workspace, void* stream) {
+  const int st = check_window("tdp_window_attention", window);
+  if (st != TDP_OK) return st;
+  return forward("tdp_window_attention", q_seqs, k_seqs, window, q, k, v, nullptr, out, lse, scale, head_dim, dtype,
+                 workspace, stream);
+}
+
+int tdp_window_attention_backward(const tdp_seqs* q_seqs, const tdp_seqs* k_seqs, const tdp_window* window,
+                                  const tdp_heads* q, const tdp_heads* k, const tdp_heads* v, const tdp_heads* out,
+                                  const float* lse, const tdp_heads* dout, const tdp_heads* dq, const tdp_heads* dk,
+                                  const tdp_heads* dv, float scale, int32_t head_dim, int32_t dtype, void* workspace,
+                                  void* stream) {
+  const int st = check_window("tdp_window_attention_backward", window);
+  if (st != TDP_OK) return st;
+  return backward("tdp_window_attention_backward", q_seqs, k_seqs, window, q, k, v, nullptr, out, lse, dout, dq, dk,
+                  dv, scale, head_dim, dtype, workspace, stream);
 }
 
 }  // extern "C"

@@ -56,6 +56,17 @@ int check_heads(const char* fn, const char* name, const tdp_heads* t, const tdp_
   return TDP_OK;
 }
 
+int check_window(const char* fn, const tdp_window* w) {
+  if (!w) return fail(TDP_EINVAL, "%s: null window", fn);
+  if (w->step < 1 || w->step > (1 << 24))
+    return fail(TDP_ESHAPE, "%s: window.step %d outside [1, 2^24]", fn, w->step);
+  if (w->back < 0 || w->ahead < 0 || w->sinks < 0 || w->back > TDP_WINDOW_ALL || w->ahead > TDP_WINDOW_ALL ||
+      w->sinks > TDP_WINDOW_ALL)
+    return fail(TDP_EINVAL, "%s: window.back, ahead and sinks must be in [0, 2^30] (got %d, %d, %d)", fn, w->back,
+                w->ahead, w->sinks);
+  return TDP_OK;
+}
+
 int check_rows(const char* fn, const char* name, const tdp_rows* t, int32_t dtype, HeadsDev* out) {
   if (!t || !t->data) return fail(TDP_EINVAL, "%s: null %s", fn, name);
   if (reinterpret_cast<uintptr_t>(t->data) & 15) return fail(TDP_EINVAL, "%s: %s must be 16-byte aligned", fn, name);
@@ -154,7 +165,7 @@ int64_t tdp_attention_workspace(const tdp_seqs* q_seqs, const tdp_seqs* k_seqs, 
       check_seqs("tdp_attention_workspace", "k_seqs", k_seqs, nullptr) != TDP_OK || q_heads < 1 || k_heads < 1 ||
       q_heads % k_heads != 0 || head_dim < 8)
     return 0;
-  return attention_workspace(*q_seqs, *k_seqs, q_heads, k_heads, head_dim);
+  return attention_workspace(*q_seqs, *k_seqs, nullptr, q_heads, k_heads, head_dim);
 }
 
 int64_t tdp_attention_backward_workspace(const tdp_seqs* q_seqs, const tdp_seqs* k_seqs, int32_t q_heads,
@@ -163,7 +174,28 @@ int64_t tdp_attention_backward_workspace(const tdp_seqs* q_seqs, const tdp_seqs*
       check_seqs("tdp_attention_backward_workspace", "k_seqs", k_seqs, nullptr) != TDP_OK || q_heads < 1 ||
       k_heads < 1 || q_heads % k_heads != 0 || head_dim < 8)
     return 0;
-  return backward_workspace(*q_seqs, *k_seqs, q_heads, k_heads, head_dim);
+  return backward_workspace(*q_seqs, *k_seqs, nullptr, q_heads, k_heads, head_dim);
+}
+
+int64_t tdp_window_attention_workspace(const tdp_seqs* q_seqs, const tdp_seqs* k_seqs, const tdp_window* window,
+                                       int32_t q_heads, int32_t k_heads, int32_t head_dim) {
+  const char* fn = "tdp_window_attention_workspace";
+  if (check_window(fn, window) != TDP_OK || check_seqs(fn, "q_seqs", q_seqs, nullptr) != TDP_OK ||
+      check_seqs(fn, "k_seqs", k_seqs, nullptr) != TDP_OK || q_heads < 1 || k_heads < 1 || q_heads % k_heads != 0 ||
+      head_dim < 8)
+    return 0;
+  return attention_workspace(*q_seqs, *k_seqs, window, q_heads, k_heads, head_dim);
+}
+
+int64_t tdp_window_attention_backward_workspace(const tdp_seqs* q_seqs, const tdp_seqs* k_seqs,
+                                                const tdp_window* window, int32_t q_heads, int32_t k_heads,
+                                                int32_t head_dim) {
+  const char* fn = "tdp_window_attention_backward_workspace";
+  if (check_window(fn, window) != TDP_OK || check_seqs(fn, "q_seqs", q_seqs, nullptr) != TDP_OK ||
+      check_seqs(fn, "k_seqs", k_seqs, nullptr) != TDP_OK || q_heads < 1 || k_heads < 1 || q_heads % k_heads != 0 ||
+      head_dim < 8)
+    return 0;
+  return backward_workspace(*q_seqs, *k_seqs, window, q_heads, k_heads, head_dim);
 }
 
 int64_t tdp_layer_norm_workspace(const tdp_seqs* seqs, int32_t channels, int32_t num_weights) {

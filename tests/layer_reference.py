@@ -46,3 +46,52 @@ def layer_norm_backward(x, w, dy, eps, dtype):
     dw, db = (dy * n).sum(0), dy.sum(0)
     dwb = (dy.abs() * (dd * r + n.abs() * (dr + 103 * U32))).sum(0)
     return dx, bound, dw, dwb, db, 100 * U32 * dy.abs().sum(0)
+
+
+def visible(window, n, q):
+    """(q, n) truth: key j takes part for query i, straight from the definition."""
+    step, back, ahead, sinks = window
+    t = torch.div(torch.arange(q)[:, None] + (n - q), step, rounding_mode="floor")
+    j = torch.arange(n)[None, :]
+    return (j < (t + 1 + ahead) * step) & ((j >= (t - back) * step) | (j < sinks))
+
+
+def window_attention(q, k, v, seen, scale, dtype, o_given=None, dout=None):
+    """One head: q (m, D), k and v (n, D), seen (m, n).  Forward: (o, bound, lse, bound); with dout and the
+    forward's stored o the gradients: a dict of name -> (value, bound)."""
+    q, k, v = q.double(), k.double().clone(), v.double().clone()
+    D, (m, n) = q.shape[1], seen.shape
+    k[~seen.any(0)] = 0.0
+    v[~seen.any(0)] = 0.0
+    live = seen.any(1)
+    zero = torch.zeros(m, dtype=torch.float64)
+    s = torch.where(seen, scale * q @ k.T, -float("inf"))
+    top = torch.where(live, s.max(1).values if n else zero, zero)
+    e = torch.exp(s - top[:, None])
+    l = e.sum(1)
+    p = e / torch.where(live, l, torch.ones_like(l))[:, None]
+    lse = torch.where(live, top + torch.log(l), -float("inf"))
+    o = p @ v
+    # a weight before its normalisation: the score's dot product, its scaling and the exponent
+    sm = torch.where(seen, s.abs(), zero[:, None])
+    ds = (D + 4) * U32 * scale * (q.abs() @ k.abs().T) + 6 * U32 * (sm + top.abs()[:, None]) + 4 * U32
+    ds = torch.where(seen, ds, zero[:, None])
+    dmax = ds.max(1).values if n else zero
+    rnd = half_step(dtype) if dtype == torch.bfloat16 else 0.0
+    o_bound = (2 * dmax[:, None] + (n + 20) * U32 + rnd) * (p @ v.abs()) + half_step(dtype) * o.abs()
+    lse_bound = torch.where(live, dmax + (n + 20) * U32 + 2 * U32 * lse.abs(), zero)
+    if dout is None:
+        return o, o_bound, lse, lse_bound
+    g, og = dout.double(), o_given.double()
+    dp, delta = g @ v.T, (g * og).sum(1, keepdim=True)
+    z = p * (dp - delta)
+    pe = p * (ds + lse_bound[:, None])
+    ze = pe * (dp - delta).abs() + p * (D + 4) * U32 * (g.abs() @ v.abs().T + (g.abs() * og.abs()).sum(1, keepdim=True))
+    ze = ze + rnd * z.abs() + 2 * U32 * z.abs()
+    res = {}
+    for name, zz, ee, x, chain in (("dq", z, ze, k, n + 20), ("dk", z.T, ze.T, q, m + 20)):
+        val = scale * zz @ x
+        res[name] = (val, scale * (ee + chain * U32 * zz.abs()) @ x.abs() + half_step(dtype) * val.abs())
+    dv = p.T @ g
+    res["dv"] = (dv, (pe.T + (rnd + (m + 20) * U32) * p.T) @ g.abs() + half_step(dtype) * dv.abs())
+    return res

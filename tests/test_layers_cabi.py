@@ -77,3 +77,89 @@ def test_layer_norm_workspace():
     for c, n in ((0, 1), (12, 1), (tdp.TDP_MAX_CHANNELS + 8, 1), (128, 0), (128, 5)):
         assert size(seqs(), c, n) == 0, (c, n)
     assert size(seqs(num_seqs=0), 128, 1) == 0
+
+
+def window(**kw):
+    return tdp.tdp_window(*{**dict(step=1, back=7, ahead=0, sinks=2), **kw}.values())
+
+
+def heads32(n=2, **kw):
+    h = tdp.tdp_heads()
+    h.data, h.heads, h.head_stride, h.row_stride, h.seq_stride = P, n, 32, 32 * n, 75 * 32 * n
+    for k, v in kw.items():
+        setattr(h, k, v)
+    return h
+
+
+BAD_WINDOWS = [
+    (dict(step=0), tdp.TDP_ESHAPE), (dict(step=(1 << 24) + 1), tdp.TDP_ESHAPE), (dict(back=-1), tdp.TDP_EINVAL),
+    (dict(ahead=-1), tdp.TDP_EINVAL), (dict(sinks=-1), tdp.TDP_EINVAL),
+    (dict(back=tdp.TDP_WINDOW_ALL + 1), tdp.TDP_EINVAL), (dict(ahead=tdp.TDP_WINDOW_ALL + 1), tdp.TDP_EINVAL),
+    (dict(sinks=tdp.TDP_WINDOW_ALL + 1), tdp.TDP_EINVAL),
+]
+
+
+def window_call(qs=None, ks=None, w=None, q=None, k=None, v=None, out=None, lse=None, scale=0.1, D=32,
+                dtype=tdp.TDP_F32, ws=P):
+    return tdp.load_library().tdp_window_attention(
+        ref(qs, seqs()), ref(ks, seqs()), ref(w, window()), ref(q, heads32()), ref(k, heads32()), ref(v, heads32()),
+        ref(out, heads32(data=2 * P)), lse, scale, D, dtype, ws, NULL)
+
+
+def window_backward_call(qs=None, ks=None, w=None, q=None, k=None, v=None, out=None, lse=P, dout=None, dq=None,
+                         dk=None, dv=None, scale=0.1, D=32, dtype=tdp.TDP_F32, ws=P):
+    return tdp.load_library().tdp_window_attention_backward(
+        ref(qs, seqs()), ref(ks, seqs()), ref(w, window()), ref(q, heads32()), ref(k, heads32()), ref(v, heads32()),
+        ref(out, heads32(data=2 * P)), lse, ref(dout, heads32()), ref(dq, heads32(data=3 * P)),
+        ref(dk, heads32(data=4 * P)), ref(dv, heads32(data=5 * P)), scale, D, dtype, ws, NULL)
+
+
+@pytest.mark.device_abi
+@pytest.mark.parametrize("call", [window_call, window_backward_call], ids=["forward", "backward"])
+def test_window_attention_refusals(call):
+    for kw, status in BAD_WINDOWS:
+        assert call(w=window(**kw)) == status, kw
+    assert call(w="null") == tdp.TDP_EINVAL
+    for kw, status in BAD_SEQS:
+        assert call(qs=seqs(**kw)) == status, kw
+        assert call(ks=seqs(**kw)) == status, kw
+    for name in ("q", "k", "v", "out") if call is window_call else ("q", "k", "v", "out", "dout", "dq", "dk", "dv"):
+        for kw, status in [(dict(data=None), tdp.TDP_EINVAL), (dict(data=P + 8), tdp.TDP_EINVAL),
+                           (dict(heads=0), tdp.TDP_ESHAPE), (dict(head_stride=33), tdp.TDP_EINVAL),
+                           (dict(heads=3), tdp.TDP_EINVAL)]:
+            assert call(**{name: heads32(**kw)}) == status, (name, kw)
+    assert call(qs=seqs(num_seqs=2, total_rows=150)) == tdp.TDP_EINVAL
+    for kw, status in [(dict(D=0), tdp.TDP_ESHAPE), (dict(D=36), tdp.TDP_ESHAPE), (dict(D=136), tdp.TDP_ESHAPE),
+                       (dict(dtype=2), tdp.TDP_EINVAL), (dict(scale=0.0), tdp.TDP_EINVAL),
+                       (dict(scale=float("nan")), tdp.TDP_EINVAL), (dict(lse=P + 2), tdp.TDP_EINVAL),
+                       (dict(q=heads32(row_stride=(1 << 24))), tdp.TDP_ESHAPE)]:
+        assert call(**kw) == status, kw
+    if call is window_backward_call:
+        assert call(lse=None) == tdp.TDP_EINVAL
+        assert call(ws=None) == tdp.TDP_EINVAL and call(ws=P + 8) == tdp.TDP_EINVAL
+    else:   # one query per sequence over long keys: split, so a workspace is needed
+        one = dict(qs=seqs(max_rows=1, total_rows=4), ks=seqs(max_rows=4000, total_rows=16000),
+                   w=window(back=tdp.TDP_WINDOW_ALL))
+        assert call(**one, ws=None) == tdp.TDP_EINVAL and "workspace" in tdp.tdp_last_error()
+        assert call(**one, ws=P + 8) == tdp.TDP_EINVAL
+
+
+def test_window_attention_workspace():
+    lib, ref = tdp.load_library(), ctypes.byref
+    fwd = lambda q, k, w, hq=4, hk=2, D=64: lib.tdp_window_attention_workspace(ref(q), ref(k), ref(w), hq, hk, D)  # noqa: E731
+    bwd = lambda q, k, w, hq=4, hk=2, D=64: lib.tdp_window_attention_backward_workspace(  # noqa: E731
+        ref(q), ref(k), ref(w), hq, hk, D)
+    one, cache = seqs(max_rows=1, total_rows=4), seqs(max_rows=4000, total_rows=16000)
+    # a short window of a long cache is not worth splitting, a long one is, up to all of it
+    assert fwd(one, cache, window(back=100)) == 0
+    assert 0 < fwd(one, cache, window(back=1500)) < fwd(one, cache, window(back=tdp.TDP_WINDOW_ALL))
+    assert fwd(one, cache, window(back=tdp.TDP_WINDOW_ALL)) == lib.tdp_attention_workspace(ref(one), ref(cache), 4, 2, 64)
+    # of many key blocks only those of the first rows are split: their sums alone
+    long = seqs(num_seqs=2, max_rows=40000, total_rows=80000)
+    stats = 4 * 80000 * 8
+    assert bwd(long, long, window(back=1000, sinks=0)) == stats
+    got = bwd(long, long, window(back=1000, sinks=130)) - stats
+    assert got > 0 and got % (2 * 2 * 256 * 64 * 8) == 0
+    for kw, _ in BAD_WINDOWS:
+        assert fwd(one, cache, window(**kw)) == 0 and bwd(one, cache, window(**kw)) == 0
+    assert fwd(one, cache, window(), hq=3) == 0 and bwd(one, cache, window(), hq=3) == 0
