@@ -769,6 +769,37 @@ int tdp_layer_norm_backward(const tdp_seqs* seqs, const tdp_rows* x, const float
                             const tdp_rows* dy, const tdp_rows* dx, float* dweight, float* dbias, float eps,
                             int32_t channels, int32_t dtype, void* workspace, void* stream);
 
+/* Products of a sequence's rows with a weight of its own:
+ *   y = x W_e^T,  e = s mod num_weights for the rows of sequence s.
+ * weight is (num_weights, out_features, in_features) of dtype, contiguous and
+ * 16-byte aligned.  One weight gives a layer's projection of the used rows of
+ * every slot; as many weights as sequences give experts, whose rows (sorted by
+ * expert, as many as the router dealt them, none included) only row_range on
+ * the device need know: max_rows may be total_rows.  features are multiples of 8,
+ * at most TDP_MAX_FEATURES; 1 <= num_weights <= num_seqs; rows lie at most 2^23
+ * bytes apart.  Products accumulate in fp32 and are rounded once.  y
+ * overlaps no input.  workspace as above, of tdp_grouped_product_workspace
+ * bytes (0: NULL allowed): where few rows meet wide weights, the contraction is
+ * split over workgroups and joined from there. */
+#define TDP_MAX_FEATURES 65536
+int64_t tdp_grouped_product_workspace(const tdp_seqs* seqs, int32_t num_weights, int32_t in_features,
+                                      int32_t out_features, int32_t dtype);
+int tdp_grouped_product(const tdp_seqs* seqs, const tdp_rows* x, const void* weight, int32_t num_weights,
+                        const tdp_rows* y, int32_t in_features, int32_t out_features, int32_t dtype, void* workspace,
+                        void* stream);
+
+/* Its gradients: dx = dy W_e and, over the rows of the sequences that share
+ * weight e, dW_e = sum of dy^T x, (num_weights, out_features, in_features) fp32,
+ * written, not added to (zeros for a weight without rows).  dx or dweight may be
+ * NULL: not wanted.  Sums run in a fixed order, so results repeat bit for bit.
+ * dx overlaps no input.  workspace as above, of
+ * tdp_grouped_product_backward_workspace bytes. */
+int64_t tdp_grouped_product_backward_workspace(const tdp_seqs* seqs, int32_t num_weights, int32_t in_features,
+                                               int32_t out_features, int32_t dtype);
+int tdp_grouped_product_backward(const tdp_seqs* seqs, const tdp_rows* x, const void* weight, int32_t num_weights,
+                                 const tdp_rows* dy, const tdp_rows* dx, float* dweight, int32_t in_features,
+                                 int32_t out_features, int32_t dtype, void* workspace, void* stream);
+
 /* ---- errors ------------------------------------------------------------ */
 /* Errors are reported, never produced silently, and a guard violation names
  * the axis and the largest overlap it allows (mold #673, "A bug found while

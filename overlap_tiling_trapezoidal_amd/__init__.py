@@ -24,7 +24,8 @@ DEVICE_FUNCTIONS = ("tdp_extract", "tdp_extract_noalloc", "tdp_set_lookback_poll
                     "tdp_extract_positions", "tdp_extract_latent", "tdp_pipeline_latent_step", "tdp_blend",
                     "tdp_blend_tile", "tdp_blend_finish", "tdp_pixel_blend", "tdp_rope_apply", "tdp_qk_norm_rope",
                     "tdp_qk_norm_rope_backward", "tdp_attention", "tdp_attention_backward", "tdp_layer_norm",
-                    "tdp_layer_norm_backward", "tdp_window_attention", "tdp_window_attention_backward")
+                    "tdp_layer_norm_backward", "tdp_window_attention", "tdp_window_attention_backward",
+                    "tdp_grouped_product", "tdp_grouped_product_backward")
 HEADER_PATH = os.path.join(os.path.dirname(_HERE), "include", "tdp.h")
 
 # ---- constants (mirror include/tdp.h) --------------------------------------
@@ -47,6 +48,7 @@ TDP_MAX_ROPE_DIM = 256
 TDP_MAX_ATTENTION_DIM = 128
 TDP_MAX_CHANNELS = 8192
 TDP_WINDOW_ALL = 1 << 30
+TDP_MAX_FEATURES = 65536
 
 _DTYPES = {"f32": TDP_F32, "float32": TDP_F32, "bf16": TDP_BF16, "bfloat16": TDP_BF16}
 
@@ -252,6 +254,10 @@ def load_library(path: str = LIB_PATH):
         "tdp_layer_norm": (ctypes.c_int, [sq, rw, vp, vp, i32, rw, f32, i32, i32, vp]),
         "tdp_layer_norm_workspace": (ctypes.c_int64, [sq, i32, i32]),
         "tdp_layer_norm_backward": (ctypes.c_int, [sq, rw, vp, i32, rw, rw, vp, vp, f32, i32, i32, vp, vp]),
+        "tdp_grouped_product_workspace": (ctypes.c_int64, [sq, i32, i32, i32, i32]),
+        "tdp_grouped_product": (ctypes.c_int, [sq, rw, vp, i32, rw, i32, i32, i32, vp, vp]),
+        "tdp_grouped_product_backward_workspace": (ctypes.c_int64, [sq, i32, i32, i32, i32]),
+        "tdp_grouped_product_backward": (ctypes.c_int, [sq, rw, vp, i32, rw, rw, vp, i32, i32, i32, vp, vp]),
         "tdp_status_string": (ctypes.c_char_p, [ctypes.c_int]),
         "tdp_last_error": (ctypes.c_char_p, []),
     }
@@ -1151,7 +1157,7 @@ def tdp_window_attention_backward(q_seqs: Sequences, k_seqs: Sequences, window: 
 
 
 # ---------------------------------------------------------------------------
-# The layer around the attention: layer norm
+# The layer around the attention: layer norm and grouped products
 # ---------------------------------------------------------------------------
 
 def _rows_layout(t, name, seqs: Sequences, features, written):
@@ -1251,3 +1257,70 @@ def tdp_layer_norm_backward(seqs: Sequences, x, weight, dy, dx, dweight, dbias, 
         ref(_rows(dx, "dx", seqs, C, x, True)), _weight_sets(dweight, "dweight", C, n, dev),
         _weight_sets(dbias, "dbias", C, n, dev), eps, C, _dtype_code(x, "x"),
         _ptr(workspace, "workspace", torch.uint8, need, dev), _stream_handle(stream, dev))
+
+
+def _product_weight(t, name, dtype, device, shape=None):
+    """(pointer, (weights, out features, in features)) of an (out, in) or (weights, out, in) tensor."""
+    if t is None:
+        raise ValueError(f"{name} is required")
+    if t.dim() not in (2, 3):
+        raise ValueError(f"{name} must be (out features, in features) or (weights, out features, in features), got "
+                         f"{tuple(t.shape)}")
+    own = tuple(t.shape) if t.dim() == 3 else (1, *t.shape)
+    if shape is not None and own != shape:
+        raise ValueError(f"{name} is {tuple(t.shape)}, needs {shape}")
+    return _ptr(t, name, dtype, t.numel(), device), own
+
+
+def allocate_grouped_product_workspace(seqs: Sequences, num_weights: int, out_features: int, in_features: int,
+                                       dtype="bf16", device="cuda"):
+    """Workspace of tdp_grouped_product, or None where it needs none."""
+    import torch
+    n = load_library().tdp_grouped_product_workspace(ctypes.byref(seqs.c), num_weights, in_features, out_features,
+                                                     _product_dtype(dtype))
+    return torch.empty(n, dtype=torch.uint8, device=torch.device(device)) if n else None
+
+
+def allocate_grouped_product_backward_workspace(seqs: Sequences, num_weights: int, out_features: int,
+                                                in_features: int, dtype="bf16", device="cuda"):
+    """Workspace of tdp_grouped_product_backward, or None where it needs none."""
+    import torch
+    n = load_library().tdp_grouped_product_backward_workspace(ctypes.byref(seqs.c), num_weights, in_features,
+                                                              out_features, _product_dtype(dtype))
+    return torch.empty(n, dtype=torch.uint8, device=torch.device(device)) if n else None
+
+
+def _product_dtype(dtype) -> int:
+    import torch
+    code = {torch.float32: TDP_F32, torch.bfloat16: TDP_BF16}.get(dtype, dtype)
+    return _DTYPES[code] if isinstance(code, str) else code
+
+
+def tdp_grouped_product(seqs: Sequences, x, weight, y, workspace=None, stream=None):
+    """Enqueue y = x W^T for every used row: ``weight`` (out, in) for all, or (n, out, in), of which
+    the rows of sequence s take weight s mod n (experts: a sequence each)."""
+    import torch
+    lib, ref, dev = load_library(), ctypes.byref, x.device
+    code = _dtype_code(x, "x")
+    w, (n, N, K) = _product_weight(weight, "weight", x.dtype, dev)
+    need = lib.tdp_grouped_product_workspace(ref(seqs.c), n, K, N, code)
+    _on(dev, lib.tdp_grouped_product, ref(seqs.c), ref(_rows(x, "x", seqs, K, x)), w, n,
+        ref(_rows(y, "y", seqs, N, x, True)), K, N, code,
+        _ptr(workspace, "workspace", torch.uint8, need, dev) if need else ctypes.c_void_p(None),
+        _stream_handle(stream, dev))
+
+
+def tdp_grouped_product_backward(seqs: Sequences, x, weight, dy, dx, dweight, workspace=None, stream=None):
+    """Enqueue the gradients of tdp_grouped_product: ``dx`` like x, ``dweight`` like weight in fp32
+    (either None: not wanted)."""
+    import torch
+    lib, ref, dev = load_library(), ctypes.byref, x.device
+    code = _dtype_code(x, "x")
+    w, shape = _product_weight(weight, "weight", x.dtype, dev)
+    n, N, K = shape
+    need = lib.tdp_grouped_product_backward_workspace(ref(seqs.c), n, K, N, code)
+    _on(dev, lib.tdp_grouped_product_backward, ref(seqs.c), ref(_rows(x, "x", seqs, K, x)), w, n,
+        ref(_rows(dy, "dy", seqs, N, x)), None if dx is None else ref(_rows(dx, "dx", seqs, K, x, True)),
+        ctypes.c_void_p(None) if dweight is None else _product_weight(dweight, "dweight", torch.float32, dev, shape)[0],
+        K, N, code, _ptr(workspace, "workspace", torch.uint8, need, dev) if need else ctypes.c_void_p(None),
+        _stream_handle(stream, dev))

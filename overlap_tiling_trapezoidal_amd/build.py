@@ -12,7 +12,7 @@ ROOT = os.path.dirname(HERE)
 LIB = os.path.join(HERE, "libtdp.so")
 SOURCES = [os.path.join(HERE, "csrc", n) for n in (
     "plan.cpp", "quality.cpp", "pixel_plan.cpp", "tokens.cpp", "kernels.hip", "pixel.hip", "rope.hip", "attention.hip",
-    "layer_norm.hip")]
+    "layer_norm.hip", "product.hip")]
 # memory-system ceilings for the measurement script (not the hot path)
 CEILING_LIB = os.path.join(HERE, "libtdp_ceiling.so")
 CEILING_SOURCES = [os.path.join(HERE, "csrc", "ceiling.hip")]

@@ -1,0 +1,646 @@
+// Products of groups of rows with weights of their own, and their gradients
+// (gfx950 matrix instructions).
+//
+//   y_i = W_e x_i,  dx_i = W_e^T dy_i,  dW_e = sum_i dy_i x_i^T
+//
+// for the used rows i of the sequences that take weight e.  All three are tiles
+// of out[q][p] = sum_r P[p][r] Q[q][r] (p: output features, q: rows, or W's rows
+// for dW) in 32 x 32 tiles of the matrix instructions with fp32 accumulators.
+// Operands come in two layouts: the contraction along memory rows (x and W of
+// y, dy of dx) or across them (W of dx, both of dW); the second kind is read
+// from LDS by transposing reads (bf16) or column by column (fp32).
+//
+// Which rows a sequence has is known on the device only.  Every workgroup counts
+// the blocks of rows of all sequences (64 at a time, a lane each) and finds its
+// own, so the launch has one workgroup per possible block and those past the
+// count leave at once.
+#include <hip/hip_runtime.h>
+#include <math.h>
+#include <stdint.h>
+
+#include <initializer_list>
+#include <type_traits>
+
+#include "token_device.h"
+
+namespace tdp {
+namespace {
+
+typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef float f32x8 __attribute__((ext_vector_type(8)));
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+#define TDP_LDS __attribute__((address_space(3)))
+
+enum Kind { kForward, kInput, kWeight };  // y, dx, dW
+
+template <int T>
+struct Mat;
+template <>
+struct Mat<TDP_BF16> {
+  typedef bf16x8 Frag;
+  static constexpr int kBytes = 2;
+  __device__ static inline f32x16 mma(const Frag& a, const Frag& b, const f32x16& c) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
+  }
+};
+template <>
+struct Mat<TDP_F32> {
+  typedef f32x8 Frag;
+  static constexpr int kBytes = 4;
+  __device__ static inline f32x16 mma(const Frag& a, const Frag& b, f32x16 c) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) c = __builtin_amdgcn_mfma_f32_32x32x2f32(a[e], b[e], c, 0, 0, 0);
+    return c;
+  }
+};
+
+struct ProductArgs {
+  SeqsDev seqs;
+  HeadsDev x, y;      // y: its gradient for dx and dW
+  HeadsDev dx;
+  const char* w;      // (weights, N, K)
+  float *dw, *ws;
+  int32_t E, N, K;    // weights, output and input features
+  int32_t splits;     // of the contraction
+  uint32_t np;        // tiles of output features
+  uint32_t nq;        // dW: tiles of W's rows
+  FastDiv by_np;
+};
+
+// An operand whose contraction runs along its rows: ROWS rows of 128 bytes in
+// LDS, chunk c of row r at c ^ (r / 2 % 8), so that 16 lanes reading one chunk of
+// 16 rows meet every bank once.
+template <int T, int ROWS, int THREADS>
+struct Along {
+  typedef typename Mat<T>::Frag Frag;
+  static constexpr int kBytes = ROWS * 128, kLoads = ROWS * 8 / THREADS;
+  static_assert(ROWS * 8 % THREADS == 0 && THREADS / 8 % 16 == 0, "whole loads");
+  uint32_t off[kLoads];
+  int chunk16;  // bytes from the row's first to this lane's chunk
+  __device__ inline void init(uint32_t row_bytes) {
+    const int r = threadIdx.x / 8;
+    chunk16 = ((threadIdx.x % 8) ^ (r >> 1 & 7)) * 16;
+#pragma unroll
+    for (int n = 0; n < kLoads; ++n) off[n] = (r + n * (THREADS / 8)) * row_bytes + chunk16;
+  }
+  // `rows` rows from `base` on, of which `left` bytes remain
+  __device__ inline void load(const char* base, uint32_t row_bytes, int rows, int left, int wave, char* lds) const {
+#ifdef __HIP_DEVICE_COMPILE__
+    const uint32_t span = rows > 0 && left > 0 ? (uint32_t)((rows < ROWS ? rows : ROWS) - 1) * row_bytes + left : 0;
+    const __amdgpu_buffer_rsrc_t rs = __builtin_amdgcn_make_buffer_rsrc(
+        const_cast<char*>(base), 0, __builtin_amdgcn_readfirstlane(span), 0x00020000);
+    const bool in = chunk16 < left;
+#pragma unroll
+    for (int n = 0; n < kLoads; ++n)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (TDP_LDS void*)(lds + (n * THREADS + wave * 64) * 16), 16,
+                                               in ? off[n] : 0xfffffff0u, 0, 0, 0);
+#endif
+  }
+  // rows r0 + lane % 32, contractions 16 kk + 8h ..
+  __device__ static inline Frag frag(const char* lds, int r0, int kk, int lane) {
+    const int r = r0 + (lane & 31), h = lane >> 5, s = r >> 1 & 7;
+    const char* row = lds + r * 128;
+    if constexpr (T == TDP_BF16) {
+      return *reinterpret_cast<const bf16x8*>(row + ((2 * kk + h) ^ s) * 16);
+    } else {
+      const f32x4 a = *reinterpret_cast<const f32x4*>(row + ((4 * kk + 2 * h) ^ s) * 16);
+      const f32x4 b = *reinterpret_cast<const f32x4*>(row + ((4 * kk + 2 * h + 1) ^ s) * 16);
+      return f32x8{a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
+    }
+  }
+};
+
+// An operand whose contraction runs across its rows: 128 bytes' worth of rows of
+// COLS elements, chunk c of row r at c ^ 4 (r % 4): the four rows that a
+// transposing read touches lie in different quarters of the banks.
+template <int T, int COLS, int THREADS>
+struct Across {
+  typedef typename Mat<T>::Frag Frag;
+  static constexpr int kRow = COLS * Mat<T>::kBytes, kChunks = kRow / 16, kRows = 128 / Mat<T>::kBytes;
+  static constexpr int kBytes = kRows * kRow, kLoads = kBytes / 16 / THREADS;
+  static_assert(THREADS % kChunks == 0 && THREADS / kChunks % 4 == 0, "whole rows");
+  uint32_t off[kLoads];
+  int row;
+  __device__ inline void init(uint32_t row_bytes) {
+    row = threadIdx.x / kChunks;
+    const int c = (threadIdx.x % kChunks) ^ ((row & 3) << 2);
+#pragma unroll
+    for (int n = 0; n < kLoads; ++n) off[n] = (row + n * (THREADS / kChunks)) * row_bytes + c * 16;
+  }
+  // `rows` rows from `base` on, each with `left` bytes from there
+  __device__ inline void load(const char* base, uint32_t row_bytes, int rows, int left, int wave, char* lds) const {
+#ifdef __HIP_DEVICE_COMPILE__
+    const uint32_t span = rows > 0 ? (uint32_t)((rows < kRows ? rows : kRows) - 1) * row_bytes + left : 0;
+    const __amdgpu_buffer_rsrc_t rs = __builtin_amdgcn_make_buffer_rsrc(
+        const_cast<char*>(base), 0, __builtin_amdgcn_readfirstlane(span), 0x00020000);
+#pragma unroll
+    for (int n = 0; n < kLoads; ++n)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (TDP_LDS void*)(lds + (n * THREADS + wave * 64) * 16), 16,
+                                               row + n * (THREADS / kChunks) < rows ? off[n] : 0xfffffff0u, 0, 0, 0);
+#endif
+  }
+  __device__ static inline Frag frag(char* lds, int c0, int kk, int lane) {
+    const int h = lane >> 5;
+    if constexpr (T == TDP_BF16) {
+      const int r = 16 * kk + 8 * h + ((lane & 15) >> 2), c = c0 + (lane & 16) + 4 * (lane & 3);
+      const int at = r * kRow + (((c >> 3) ^ ((r & 3) << 2)) << 4) + (c & 7) * 2;
+      typedef TDP_LDS bf16x4* P;
+      const bf16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4bf16((P)(TDP_LDS char*)(lds + at));
+      const bf16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4bf16((P)(TDP_LDS char*)(lds + at + 4 * kRow));
+      return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
+    } else {
+      const int c = c0 + (lane & 31);
+      f32x8 v;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const int r = 16 * kk + 8 * h + e;
+        v[e] = *reinterpret_cast<const float*>(lds + r * kRow + (((c >> 2) ^ ((r & 3) << 2)) << 4) + (c & 3) * 4);
+      }
+      return v;
+    }
+  }
+};
+
+// Wait for this wave's loads into LDS, all but the last N of them, and for its
+// reads of LDS, then for the other waves.  The compiler moves no access of memory
+// across.
+template <int N>
+__device__ inline void wait_barrier() {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_waitcnt((N & 15) | 0x0070 | (N >> 4) << 14);  // vmcnt(N) lgkmcnt(0)
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+}
+
+__device__ inline int wave_prefix(int v, int lane) {  // inclusive
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const int t = __shfl_up(v, d);
+    if (lane >= d) v += t;
+  }
+  return v;
+}
+
+// Blocks of `rows` rows of every sequence in order, found by whole waves.
+struct RowBlocks {
+  const SeqsDev& q;
+  int rows, lane;
+  __device__ inline int count(int s) const {
+    if (s >= q.S) return 0;
+    return (seq_rows(q, s).cap + rows - 1) / rows;
+  }
+  __device__ inline int total() const {
+    if (!q.range) return q.S * ((q.max_rows + rows - 1) / rows);
+    int n = 0;
+    for (int s = 0; s < q.S; s += 64) n += __shfl(wave_prefix(count(s + lane), lane), 63);
+    return n;
+  }
+  // the sequence of block t, which becomes the block's number in it
+  __device__ inline int find(int& t) const {
+    if (!q.range) {
+      const int per = (q.max_rows + rows - 1) / rows, s = t / per;
+      t -= s * per;
+      return s;
+    }
+    for (int s = 0; s < q.S; s += 64) {
+      const int n = count(s + lane), end = wave_prefix(n, lane);
+      const uint64_t past = __ballot(end > t);
+      if (past) {
+        const int l = __builtin_ctzll(past);
+        t -= __shfl(end - n, l);
+        return s + l;
+      }
+      t -= __shfl(end, 63);
+    }
+    return 0;  // not reached: t is below the total
+  }
+};
+
+// Workgroups are dealt round-robin to the eight XCDs, each of which takes a
+// contiguous range of the tiles.  Runs of eight tiles along q share one of p, and
+// the tiles that an XCD's 32 CUs hold at a time are eight by four: they read
+// twelve panels of operands through its L2 instead of 64.
+__device__ inline bool tile_of(uint32_t nq, uint32_t np, uint32_t b, uint32_t& q, uint32_t& p) {
+  const uint32_t tiles = nq * np, per = (tiles + 7) / 8, slot = b >> 3, item = (b & 7) * per + slot;
+  if (slot >= per || item >= tiles) return false;
+  const uint32_t group = item / (8 * np), first = group * 8, rest = item - first * np;
+  const uint32_t n = nq - first < 8 ? nq - first : 8;
+  p = rest / n;
+  q = first + (rest - p * n);
+  return true;
+}
+
+__device__ inline f32x16 zero16() {
+  f32x16 z;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) z[i] = 0.0f;
+  return z;
+}
+
+// The wave's 32 rows of TP tiles of features, through 4 KB of LDS of its own so
+// that whole runs of features leave at once.  OUT: type written.  Rows at and
+// past `len` become zero, those past `cap` and features past `left` are not
+// written.
+template <int OUT, int TP>
+__device__ inline void store_tile(char* out, int64_t row_bytes, int len, int cap, int left, const f32x16* acc,
+                                  int lane, char* lds) {
+  constexpr int eb = OUT == TDP_BF16 ? 2 : 4;
+  constexpr int U = OUT == TDP_BF16 && TP > 1 ? 2 : 1;  // tiles side by side in a row of 128 bytes at most
+  constexpr int kChunks = U * 32 * eb / 16, kRowsAtOnce = 64 / kChunks;
+  const int r = lane & 31, h = lane >> 5;
+#pragma unroll
+  for (int u0 = 0; u0 < TP; u0 += U) {
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int r4 = 0; r4 < 4; ++r4) {
+        float x[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x[e] = r < len ? acc[u0 + u][r4 * 4 + e] : 0.0f;
+        const int f = u * 32 + r4 * 8 + h * 4, c = f * eb / 16;
+        char* at = lds + r * 128 + ((c ^ (r >> 1 & (kChunks - 1))) << 4) + f * eb % 16;
+        if constexpr (OUT == TDP_BF16) {
+          uint2 v;
+          v.x = pack_bf16x2(x[0], x[1]);
+          v.y = pack_bf16x2(x[2], x[3]);
+          *reinterpret_cast<uint2*>(at) = v;
+        } else {
+          *reinterpret_cast<f32x4*>(at) = f32x4{x[0], x[1], x[2], x[3]};
+        }
+      }
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+#pragma unroll
+    for (int i = 0; i < 32; i += kRowsAtOnce) {
+      const int row = i + lane / kChunks, c = lane % kChunks;
+      const u32x4 v = *reinterpret_cast<const u32x4*>(lds + row * 128 + ((c ^ (row >> 1 & (kChunks - 1))) << 4));
+      const int f = u0 * 32 + c * (16 / eb);
+      if (row < cap && f < left) *reinterpret_cast<u32x4*>(out + row * row_bytes + f * eb) = v;
+    }
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+  }
+}
+
+// BP x BQ output tile per workgroup of WP x WQ waves, 128 bytes of the
+// contraction at a time, two LDS buffers: the next step's operands are on their
+// way while this step's are multiplied.
+template <int T, int KIND, int BP, int BQ, int WP, int WQ>
+__global__ __launch_bounds__(64 * WP * WQ) void product_kernel(const ProductArgs A) {
+  constexpr int THREADS = 64 * WP * WQ, eb = Mat<T>::kBytes, kStep = 128 / eb, KK = kStep / 16;
+  constexpr int TP = BP / WP / 32, TQ = BQ / WQ / 32;
+  typedef typename Mat<T>::Frag Frag;
+  typedef std::conditional_t<KIND == kForward, Along<T, BP, THREADS>, Across<T, BP, THREADS>> OpP;
+  typedef std::conditional_t<KIND == kWeight, Across<T, BQ, THREADS>, Along<T, BQ, THREADS>> OpQ;
+  __shared__ __align__(16) char p0[OpP::kBytes];
+  __shared__ __align__(16) char q0[OpQ::kBytes];
+  __shared__ __align__(16) char p1[OpP::kBytes];
+  __shared__ __align__(16) char q1[OpQ::kBytes];
+  static_assert(OpP::kBytes >= 4096 * WP * WQ, "the epilogue's place");
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+  const int wp = wave % WP, wq = wave / WP;
+
+  // the tile: its block of rows, or of W's rows, and its features
+  uint32_t tq, tp;
+  int s = 0, blk = 0, e = 0;
+  SeqRows sr = {};
+  const int split = blockIdx.y;
+  if constexpr (KIND != kWeight) {
+    const RowBlocks rb = {A.seqs, BQ, lane};
+    if (!tile_of((uint32_t)rb.total(), A.np, blockIdx.x, tq, tp)) return;
+    blk = (int)tq;
+    s = __builtin_amdgcn_readfirstlane(rb.find(blk));
+    blk = __builtin_amdgcn_readfirstlane(blk);
+    sr = seq_rows(A.seqs, s);
+    e = s % A.E;
+  } else {
+    const uint32_t per = A.nq * A.np, grid = (per + 7) / 8 * 8;
+    e = blockIdx.x / grid;
+    if (!tile_of(A.nq, A.np, blockIdx.x - e * grid, tq, tp)) return;
+    blk = (int)tq;
+  }
+  const int f0 = (int)tp * BP, r0 = blk * BQ;
+  const char* w = A.w + (int64_t)e * A.N * A.K * eb;
+  const int features = KIND == kForward ? A.N : A.K;   // of the output
+  const int inner = KIND == kForward ? A.K : A.N;      // y and dx: the contraction's length
+  const int64_t xrow = A.x.row_stride * eb, yrow = A.y.row_stride * eb;
+
+  OpP P;
+  OpQ Q;
+  f32x16 acc[TQ][TP];
+#pragma unroll
+  for (int j = 0; j < TQ; ++j)
+#pragma unroll
+    for (int i = 0; i < TP; ++i) acc[j][i] = zero16();
+
+  // where the next loads begin
+  const char *pb, *qb;
+  uint32_t prow, qrow;
+  int t0, t1;  // steps
+  int seq = 0, left = 0;  // dW: the sequence being read and its rows not yet read
+  if constexpr (KIND != kWeight) {
+    const int steps = r0 < sr.len ? (inner + kStep - 1) / kStep : 0, per = (steps + A.splits - 1) / A.splits;
+    t0 = split * per;
+    t1 = t0 + per < steps ? t0 + per : steps;
+    const HeadsDev& in = KIND == kForward ? A.x : A.y;
+    qrow = (uint32_t)(in.row_stride * eb);
+    qb = in.data + eb * (seq_base(A.seqs, in, s, sr) + r0 * in.row_stride) + (int64_t)t0 * 128;
+    prow = (uint32_t)A.K * eb;
+    pb = KIND == kForward ? w + (int64_t)f0 * prow + (int64_t)t0 * 128 : w + (int64_t)t0 * kStep * prow + f0 * eb;
+  } else {
+    prow = (uint32_t)xrow;
+    qrow = (uint32_t)yrow;
+    // steps of all sequences of this weight, and the one that this part begins in
+    auto steps_of = [&](int sq) { return sq < A.seqs.S ? (seq_rows(A.seqs, sq).len + kStep - 1) / kStep : 0; };
+    int steps = 0;
+    for (int i = e; i < A.seqs.S; i += 64 * A.E) steps += __shfl(wave_prefix(steps_of(i + lane * A.E), lane), 63);
+    steps = __builtin_amdgcn_readfirstlane(steps);
+    const int per = (steps + A.splits - 1) / A.splits;
+    t0 = split * per;
+    t1 = t0 + per < steps ? t0 + per : steps;
+    int skip = t0;
+    seq = e;
+    if (t0 < t1)
+      for (int i = e; i < A.seqs.S; i += 64 * A.E) {
+        const int n = steps_of(i + lane * A.E), end = wave_prefix(n, lane);
+        const uint64_t past = __ballot(end > skip);
+        if (past) {
+          const int l = __builtin_ctzll(past);
+          skip -= __shfl(end - n, l);
+          seq = i + l * A.E;
+          break;
+        }
+        skip -= __shfl(end, 63);
+      }
+    seq = __builtin_amdgcn_readfirstlane(seq);
+    skip = __builtin_amdgcn_readfirstlane(skip);
+    sr = seq_rows(A.seqs, seq);
+    left = sr.len - skip * kStep;
+    pb = A.x.data + eb * seq_base(A.seqs, A.x, seq, sr) + (int64_t)skip * kStep * xrow + f0 * eb;
+    qb = A.y.data + eb * seq_base(A.seqs, A.y, seq, sr) + (int64_t)skip * kStep * yrow + r0 * eb;
+  }
+  P.init(prow);
+  Q.init(qrow);
+  int at = t0 * kStep;  // y and dx: the contraction's place
+  auto load = [&](char* pl, char* ql) __attribute__((always_inline)) {
+    if constexpr (KIND == kForward) {
+      P.load(pb, prow, A.N - f0, (inner - at) * eb, wave, pl);
+      pb += 128;
+    } else if constexpr (KIND == kInput) {
+      P.load(pb, prow, inner - at, (A.K - f0) * eb, wave, pl);
+      pb += (int64_t)kStep * prow;
+    }
+    if constexpr (KIND != kWeight) {
+      Q.load(qb, qrow, sr.len - r0, (inner - at) * eb, wave, ql);
+      qb += 128;
+      at += kStep;
+    } else {
+      while (left <= 0 && seq + A.E < A.seqs.S) {  // there is a step to load, so a later sequence holds it
+        seq += A.E;
+        sr = seq_rows(A.seqs, seq);
+        left = sr.len;
+        pb = A.x.data + eb * seq_base(A.seqs, A.x, seq, sr) + f0 * eb;
+        qb = A.y.data + eb * seq_base(A.seqs, A.y, seq, sr) + r0 * eb;
+      }
+      P.load(pb, prow, left, (A.K - f0) * eb, wave, pl);
+      Q.load(qb, qrow, left, (A.N - r0) * eb, wave, ql);
+      pb += (int64_t)kStep * xrow;
+      qb += (int64_t)kStep * yrow;
+      left -= kStep;
+    }
+  };
+  auto multiply = [&](char* pl, char* ql) __attribute__((always_inline)) {
+#pragma unroll
+    for (int kk = 0; kk < KK; ++kk) {
+      Frag a[TP], b[TQ];
+#pragma unroll
+      for (int i = 0; i < TP; ++i) a[i] = OpP::frag(pl, (wp * TP + i) * 32, kk, lane);
+#pragma unroll
+      for (int j = 0; j < TQ; ++j) b[j] = OpQ::frag(ql, (wq * TQ + j) * 32, kk, lane);
+#pragma unroll
+      for (int j = 0; j < TQ; ++j)
+#pragma unroll
+        for (int i = 0; i < TP; ++i) acc[j][i] = Mat<T>::mma(a[i], b[j], acc[j][i]);
+    }
+  };
+  if (t0 < t1) {
+    load(p0, q0);
+    int t = t0;
+    for (; t + 1 < t1; t += 2) {
+      wait_barrier<0>();
+      load(p1, q1);
+      multiply(p0, q0);
+      wait_barrier<0>();
+      if (t + 2 < t1) load(p0, q0);
+      multiply(p1, q1);
+    }
+    if (t < t1) {
+      wait_barrier<0>();
+      multiply(p0, q0);
+    }
+  }
+  __syncthreads();
+  // out
+  char* lds = p0 + wave * 4096;
+  const int wf = f0 + wp * TP * 32;
+#pragma unroll
+  for (int j = 0; j < TQ; ++j) {
+    const int row = r0 + (wq * TQ + j) * 32;
+    if constexpr (KIND == kWeight) {
+      float* out = (A.splits > 1 ? A.ws + (int64_t)split * A.E * A.N * A.K : A.dw) + ((int64_t)e * A.N + row) * A.K + wf;
+      store_tile<TDP_F32, TP>(reinterpret_cast<char*>(out), (int64_t)A.K * 4, A.N - row, A.N - row, A.K - wf, acc[j],
+                              lane, lds);
+    } else if (A.splits > 1) {
+      // parts lie by the tensor's rows: (splits, total rows, features)
+      float* out = A.ws + ((int64_t)split * A.seqs.total + sr.row0 + row) * features + wf;
+      store_tile<TDP_F32, TP>(reinterpret_cast<char*>(out), (int64_t)features * 4, sr.len - row, sr.cap - row,
+                              features - wf, acc[j], lane, lds);
+    } else {
+      const HeadsDev& o = KIND == kForward ? A.y : A.dx;
+      char* out = o.data + eb * (seq_base(A.seqs, o, s, sr) + row * o.row_stride + wf);
+      store_tile<T, TP>(out, o.row_stride * eb, sr.len - row, sr.cap - row, features - wf, acc[j], lane, lds);
+    }
+  }
+}
+
+constexpr int kJoin = 256;
+
+// Sum the parts of y or dx in order: a workgroup per block of rows and columns.
+template <int T>
+__global__ __launch_bounds__(kJoin) void product_join_kernel(const ProductArgs A, HeadsDev o, int features, int rows) {
+  const int lane = threadIdx.x & 63;
+  const RowBlocks rb = {A.seqs, rows, lane};
+  int blk = blockIdx.x;
+  if (blk >= rb.total()) return;
+  const int s = __builtin_amdgcn_readfirstlane(rb.find(blk));
+  const SeqRows sr = seq_rows(A.seqs, s);
+  const int per = features / 4, c = (blockIdx.y * kJoin + threadIdx.x) % per, r = (blockIdx.y * kJoin + threadIdx.x) / per;
+  const int row = blk * rows + r;
+  if (r >= rows || row >= sr.cap) return;
+  f32x4 v = {0.0f, 0.0f, 0.0f, 0.0f};
+  const float* from = A.ws + (sr.row0 + row) * features + c * 4;
+#pragma unroll 4
+  for (int i = 0; i < A.splits; ++i) v += *reinterpret_cast<const f32x4*>(from + (int64_t)i * A.seqs.total * features);
+  char* to = o.data + Mat<T>::kBytes * (seq_base(A.seqs, o, s, sr) + row * o.row_stride + c * 4);
+  if constexpr (T == TDP_BF16) {
+    uint2 b;
+    b.x = pack_bf16x2(v[0], v[1]);
+    b.y = pack_bf16x2(v[2], v[3]);
+    *reinterpret_cast<uint2*>(to) = b;
+  } else {
+    *reinterpret_cast<f32x4*>(to) = v;
+  }
+}
+
+__global__ __launch_bounds__(kJoin) void weight_join_kernel(const float* parts, float* dw, int64_t quads, int splits) {
+  const int64_t i = (int64_t)blockIdx.x * kJoin + threadIdx.x;
+  if (i >= quads) return;
+  f32x4 v = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 4
+  for (int k = 0; k < splits; ++k) v += reinterpret_cast<const f32x4*>(parts)[k * quads + i];
+  reinterpret_cast<f32x4*>(dw)[i] = v;
+}
+
+int check_items(const char* fn, int64_t workgroups, int threads) {
+  if (workgroups * threads > 0xffffffffLL - 8 * threads)
+    return fail(TDP_ESHAPE, "%s: %lld workgroups, more work-items than one HIP launch holds", fn, (long long)workgroups);
+  return TDP_OK;
+}
+
+int begin(const char* fn, const tdp_seqs* seqs, const tdp_rows* x, const void* weight, int32_t num_weights,
+          const tdp_rows* y, int32_t in_features, int32_t out_features, int32_t dtype, ProductArgs* A) {
+  if (!dtype_bytes(dtype)) return fail(TDP_EINVAL, "%s: dtype must be TDP_F32 or TDP_BF16 (got %d)", fn, dtype);
+  int st = check_product(fn, seqs, num_weights, in_features, out_features);
+  if (st == TDP_OK) st = check_seqs(fn, "seqs", seqs, &A->seqs);
+  if (st == TDP_OK) st = check_rows(fn, "x", x, dtype, &A->x);
+  if (st == TDP_OK) st = check_rows(fn, "y", y, dtype, &A->y);
+  if (st != TDP_OK) return st;
+  if (!weight || (reinterpret_cast<uintptr_t>(weight) & 15))
+    return fail(TDP_EINVAL, "%s: weight must be a 16-byte aligned device pointer", fn);
+  for (const tdp_rows* t : {x, y})
+    if (t->row_stride * dtype_bytes(dtype) > (1 << 23))
+      return fail(TDP_ESHAPE, "%s: a row stride of %lld elements exceeds 2^23 bytes", fn, (long long)t->row_stride);
+  A->w = static_cast<const char*>(weight);
+  A->E = num_weights;
+  A->N = out_features;
+  A->K = in_features;
+  return TDP_OK;
+}
+
+// A launch over blocks of rows: y or dx.  Without `enqueue` only its checks.
+template <int T, int KIND, int BP, int BQ, int WP, int WQ>
+int launch_rows(const char* fn, ProductArgs A, const tdp_seqs& seqs, const ProductShape& sh, bool enqueue,
+                hipStream_t st) {
+  const int features = KIND == kForward ? A.N : A.K;
+  A.np = (uint32_t)((features + BP - 1) / BP);
+  A.splits = sh.splits;
+  const int64_t blocks = row_blocks(seqs, BQ), tiles = (blocks * A.np + 7) / 8 * 8;
+  const int64_t join_y = ((int64_t)kJoinRows * (features / 4) + kJoin - 1) / kJoin, join_x = row_blocks(seqs, kJoinRows);
+  int rc = check_items(fn, tiles * sh.splits, 64 * WP * WQ);
+  if (rc == TDP_OK && sh.splits > 1) rc = check_items(fn, join_x * join_y, kJoin);
+  if (rc != TDP_OK || !enqueue) return rc;
+  hipLaunchKernelGGL((product_kernel<T, KIND, BP, BQ, WP, WQ>), dim3((unsigned)tiles, (unsigned)sh.splits),
+                     dim3(64 * WP * WQ), 0, st, A);
+  if (sh.splits > 1)
+    hipLaunchKernelGGL((product_join_kernel<T>), dim3((unsigned)join_x, (unsigned)join_y), dim3(kJoin), 0, st, A,
+                       KIND == kForward ? A.y : A.dx, features, kJoinRows);
+  return TDP_OK;
+}
+
+template <int T, int BP, int BQ, int WP, int WQ>
+int launch_weight(const char* fn, ProductArgs A, const ProductShape& sh, bool enqueue, hipStream_t st) {
+  A.np = (uint32_t)((A.K + BP - 1) / BP);
+  A.nq = (uint32_t)((A.N + BQ - 1) / BQ);
+  A.splits = sh.splits;
+  const int64_t tiles = ((int64_t)A.np * A.nq + 7) / 8 * 8 * A.E, quads = (int64_t)A.E * A.N * A.K / 4;
+  int rc = check_items(fn, tiles * sh.splits, 64 * WP * WQ);
+  if (rc == TDP_OK && sh.splits > 1) rc = check_items(fn, (quads + kJoin - 1) / kJoin, kJoin);
+  if (rc != TDP_OK || !enqueue) return rc;
+  hipLaunchKernelGGL((product_kernel<T, kWeight, BP, BQ, WP, WQ>), dim3((unsigned)tiles, (unsigned)sh.splits),
+                     dim3(64 * WP * WQ), 0, st, A);
+  if (sh.splits > 1)
+    hipLaunchKernelGGL(weight_join_kernel, dim3((unsigned)((quads + kJoin - 1) / kJoin)), dim3(kJoin), 0, st, A.ws, A.dw,
+                       quads, sh.splits);
+  return TDP_OK;
+}
+
+template <int KIND>
+int run_rows(const char* fn, const ProductArgs& A, const tdp_seqs& seqs, const ProductShape& sh, int32_t dtype,
+             bool enqueue, hipStream_t st) {
+  if (dtype == TDP_BF16) {
+    if (sh.rows == 256) return launch_rows<TDP_BF16, KIND, 256, 256, 4, 2>(fn, A, seqs, sh, enqueue, st);
+    if (sh.rows == 128) return launch_rows<TDP_BF16, KIND, 128, 128, 2, 2>(fn, A, seqs, sh, enqueue, st);
+    return launch_rows<TDP_BF16, KIND, 128, 32, 4, 1>(fn, A, seqs, sh, enqueue, st);
+  }
+  if (sh.rows == 128) return launch_rows<TDP_F32, KIND, 128, 128, 2, 2>(fn, A, seqs, sh, enqueue, st);
+  return launch_rows<TDP_F32, KIND, 128, 32, 4, 1>(fn, A, seqs, sh, enqueue, st);
+}
+
+int run_weight(const char* fn, const ProductArgs& A, const ProductShape& sh, int32_t dtype, bool enqueue,
+               hipStream_t st) {
+  if (dtype == TDP_F32) return launch_weight<TDP_F32, 128, 128, 2, 2>(fn, A, sh, enqueue, st);
+  if (sh.rows == 256) return launch_weight<TDP_BF16, 256, 256, 4, 2>(fn, A, sh, enqueue, st);
+  return launch_weight<TDP_BF16, 128, 128, 2, 2>(fn, A, sh, enqueue, st);
+}
+
+int check_workspace(const char* fn, const ProductShape& sh, const void* ws) {
+  if (sh.splits > 1 && (!ws || (reinterpret_cast<uintptr_t>(ws) & 15)))
+    return fail(TDP_EINVAL, "%s: workspace must be a 16-byte aligned device pointer (%s_workspace)", fn, fn);
+  return TDP_OK;
+}
+
+}  // namespace
+}  // namespace tdp
+
+using namespace tdp;
+
+extern "C" {
+
+int tdp_grouped_product(const tdp_seqs* seqs, const tdp_rows* x, const void* weight, int32_t num_weights,
+                        const tdp_rows* y, int32_t in_features, int32_t out_features, int32_t dtype, void* workspace,
+                        void* stream) {
+  const char* fn = "tdp_grouped_product";
+  ProductArgs A = {};
+  int st = begin(fn, seqs, x, weight, num_weights, y, in_features, out_features, dtype, &A);
+  if (st != TDP_OK) return st;
+  const ProductShape sh = rows_shape(*seqs, out_features, in_features, dtype);
+  st = check_workspace(fn, sh, workspace);
+  if (st != TDP_OK) return st;
+  A.ws = static_cast<float*>(workspace);
+  st = run_rows<kForward>(fn, A, *seqs, sh, dtype, true, reinterpret_cast<hipStream_t>(stream));
+  if (st != TDP_OK) return st;
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return fail(TDP_EHIP, "%s: kernel launch failed: %s", fn, hipGetErrorString(e));
+  return TDP_OK;
+}
+
+int tdp_grouped_product_backward(const tdp_seqs* seqs, const tdp_rows* x, const void* weight, int32_t num_weights,
+                                 const tdp_rows* dy, const tdp_rows* dx, float* dweight, int32_t in_features,
+                                 int32_t out_features, int32_t dtype, void* workspace, void* stream) {
+  const char* fn = "tdp_grouped_product_backward";
+  ProductArgs A = {};
+  int st = begin(fn, seqs, x, weight, num_weights, dy, in_features, out_features, dtype, &A);
+  if (st == TDP_OK && dx) st = check_rows(fn, "dx", dx, dtype, &A.dx);
+  if (st != TDP_OK) return st;
+  if (reinterpret_cast<uintptr_t>(dweight) & 15)
+    return fail(TDP_EINVAL, "%s: dweight must be 16-byte aligned", fn);
+  const ProductShape si = rows_shape(*seqs, in_features, out_features, dtype);
+  const ProductShape sw = weight_shape(*seqs, num_weights, in_features, out_features, dtype);
+  if (dx) st = check_workspace(fn, si, workspace);
+  if (st == TDP_OK && dweight) st = check_workspace(fn, sw, workspace);
+  if (st != TDP_OK) return st;
+  A.ws = static_cast<float*>(workspace);
+  A.dw = dweight;
+  hipStream_t hs = reinterpret_cast<hipStream_t>(stream);
+  for (const bool enqueue : {false, true}) {
+    if (st == TDP_OK && dx) st = run_rows<kInput>(fn, A, *seqs, si, dtype, enqueue, hs);
+    if (st == TDP_OK && dweight) st = run_weight(fn, A, sw, dtype, enqueue, hs);
+  }
+  if (st != TDP_OK) return st;
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return fail(TDP_EHIP, "%s: kernel launch failed: %s", fn, hipGetErrorString(e));
+  return TDP_OK;
+}
+
+}  // extern "C"

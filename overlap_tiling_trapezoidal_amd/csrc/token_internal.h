@@ -224,6 +224,60 @@ inline int64_t layer_norm_parts(const tdp_seqs& s, int32_t channels, int32_t set
   return n < blocks ? n : blocks;
 }
 
+// Grouped products.  Blocks of `rows` rows that the sequences may have in all:
+// exactly where they are uniform, else at most one unfinished block each.
+inline int64_t row_blocks(const tdp_seqs& s, int rows) {
+  if (!s.row_range) return seq_blocks(s, rows);
+  return s.total_rows / rows + (s.num_seqs < s.total_rows ? s.num_seqs : s.total_rows);
+}
+struct ProductShape {
+  int rows;    // of the output tile: 256 (by 256 features), 128 (by 128) or 32 (by 128)
+  int splits;  // of the contraction
+};
+constexpr int kJoinRows = 8;
+constexpr int kProductMaxSplits = 16;
+// Splits of the contraction where the tiles are too few for the places that the
+// GPU has for them, none shorter than `least` of its `steps`.
+inline int product_splits(int64_t tiles, int64_t places, int64_t steps, int64_t least) {
+  int64_t n = places / tiles;
+  if (n > steps / least) n = steps / least;
+  if (n > kProductMaxSplits) n = kProductMaxSplits;
+  return n < 2 ? 1 : (int)n;
+}
+inline int64_t tiles_across(int64_t n, int64_t tile) { return (n + tile - 1) / tile; }
+// y (features = N, inner = K) and dx (the other way round).
+inline ProductShape rows_shape(const tdp_seqs& s, int32_t features, int32_t inner, int32_t dtype) {
+  const int64_t mean = s.row_range ? s.total_rows / s.num_seqs : s.max_rows;
+  const int64_t big = row_blocks(s, 256) * tiles_across(features, 256);
+  ProductShape sh = {mean <= 48 ? 32 : 128, 1};
+  if (dtype == TDP_BF16 && mean >= 192 && big >= 192) sh.rows = 256;
+  const int64_t tiles = row_blocks(s, sh.rows) * tiles_across(features, sh.rows == 256 ? 256 : 128);
+  const int64_t places = sh.rows == 256 ? 256 : sh.rows == 128 ? 512 : 1024;
+  sh.splits = product_splits(tiles, places, inner * dtype_bytes(dtype) / 128, 4);
+  return sh;
+}
+// dW: its tile of W's rows is `rows` too, the contraction the rows of a weight's sequences.
+inline ProductShape weight_shape(const tdp_seqs& s, int32_t weights, int32_t in_features, int32_t out_features,
+                                 int32_t dtype) {
+  const int64_t big = weights * tiles_across(in_features, 256) * tiles_across(out_features, 256);
+  ProductShape sh = {dtype == TDP_BF16 && big >= 192 ? 256 : 128, 1};
+  const int64_t tiles = weights * tiles_across(in_features, sh.rows) * tiles_across(out_features, sh.rows);
+  sh.splits = product_splits(tiles, sh.rows == 256 ? 256 : 512,
+                             s.total_rows / weights * dtype_bytes(dtype) / 128, 8);
+  return sh;
+}
+inline int64_t rows_workspace(const tdp_seqs& s, int32_t features, int32_t inner, int32_t dtype) {
+  const ProductShape sh = rows_shape(s, features, inner, dtype);
+  return sh.splits == 1 ? 0 : align256(sh.splits * s.total_rows * features * 4);
+}
+inline int64_t weight_workspace(const tdp_seqs& s, int32_t weights, int32_t in_features, int32_t out_features,
+                                int32_t dtype) {
+  const ProductShape sh = weight_shape(s, weights, in_features, out_features, dtype);
+  return sh.splits == 1 ? 0 : align256((int64_t)sh.splits * weights * in_features * out_features * 4);
+}
+int check_product(const char* fn, const tdp_seqs* seqs, int32_t num_weights, int32_t in_features,
+                  int32_t out_features);
+
 }  // namespace tdp
 
 struct tdp_rope {

@@ -5,6 +5,7 @@
 #include <stdint.h>
 #include <string.h>
 
+#include <initializer_list>
 #include <new>
 
 #include "token_internal.h"
@@ -53,6 +54,20 @@ int check_heads(const char* fn, const char* name, const tdp_heads* t, const tdp_
   out->row_stride = t->row_stride;
   out->head_stride = t->head_stride;
   out->heads = t->heads;
+  return TDP_OK;
+}
+
+int check_product(const char* fn, const tdp_seqs* seqs, int32_t num_weights, int32_t in_features,
+                  int32_t out_features) {
+  const int st = check_seqs(fn, "seqs", seqs, nullptr);
+  if (st != TDP_OK) return st;
+  for (const int32_t f : {in_features, out_features})
+    if (f < 8 || f % 8 != 0 || f > TDP_MAX_FEATURES)
+      return fail(TDP_ESHAPE, "%s: features must be multiples of 8 in [8, %d] (got %d and %d)", fn, TDP_MAX_FEATURES,
+                  in_features, out_features);
+  if (num_weights < 1 || num_weights > seqs->num_seqs)
+    return fail(TDP_EINVAL, "%s: num_weights must be in [1, num_seqs] (got %d of %d)", fn, num_weights,
+                seqs->num_seqs);
   return TDP_OK;
 }
 
@@ -207,6 +222,22 @@ int64_t tdp_layer_norm_workspace(const tdp_seqs* seqs, int32_t channels, int32_t
     return 0;
   }
   return align256(layer_norm_parts(*seqs, channels, num_weights) * num_weights * 2 * channels * 4);
+}
+
+int64_t tdp_grouped_product_workspace(const tdp_seqs* seqs, int32_t num_weights, int32_t in_features,
+                                      int32_t out_features, int32_t dtype) {
+  const char* fn = "tdp_grouped_product_workspace";
+  if (check_product(fn, seqs, num_weights, in_features, out_features) != TDP_OK || !dtype_bytes(dtype)) return 0;
+  return rows_workspace(*seqs, out_features, in_features, dtype);
+}
+
+int64_t tdp_grouped_product_backward_workspace(const tdp_seqs* seqs, int32_t num_weights, int32_t in_features,
+                                               int32_t out_features, int32_t dtype) {
+  const char* fn = "tdp_grouped_product_backward_workspace";
+  if (check_product(fn, seqs, num_weights, in_features, out_features) != TDP_OK || !dtype_bytes(dtype)) return 0;
+  const int64_t a = rows_workspace(*seqs, in_features, out_features, dtype);
+  const int64_t b = weight_workspace(*seqs, num_weights, in_features, out_features, dtype);
+  return a > b ? a : b;  // dx and dW take turns
 }
 
 }  // extern "C"

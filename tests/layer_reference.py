@@ -95,3 +95,10 @@ def window_attention(q, k, v, seen, scale, dtype, o_given=None, dout=None):
     dv = p.T @ g
     res["dv"] = (dv, (pe.T + (rnd + (m + 20) * U32) * p.T) @ g.abs() + half_step(dtype) * dv.abs())
     return res
+
+
+def product(x, w, dtype):
+    """x (m, K) times w (N, K) transposed: (y, bound).  K products and sums in one chain, a join's at most 16."""
+    x, w = x.double(), w.double()
+    y = x @ w.T
+    return y, (x.shape[1] + 24) * U32 * (x.abs() @ w.abs().T) + half_step(dtype) * y.abs()

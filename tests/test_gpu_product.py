@@ -1,0 +1,155 @@
+"""GPU parity of the grouped products and their gradients with the 64-bit
+reference (tests/layer_reference.py), within its derived bounds.
+
+Every unused row of every input holds NaN and every output starts as NaN, so a
+row that leaks in or is not written shows.  Inputs are seeded.
+"""
+import pytest
+import torch
+
+import layer_reference as L
+import overlap_tiling_trapezoidal_amd as tdp
+from harness import note
+from test_gpu_layer_norm import flat, rows_like
+from test_gpu_tokens import DT, NAN, check, check_rest, layout
+from token_reference import U32
+
+pytestmark = pytest.mark.gpu
+
+CASES = [
+    # in, out features, caps, lens, ragged ranges, weights, layout
+    (8, 8, (1,), (1,), False, 1, "rows"),
+    (128, 384, (75,) * 4, (75,) * 4, False, 1, "rows"),
+    (72, 40, (33, 20, 64), (33, 0, 63), True, 3, "wide"),
+    (136, 264, (130,) * 2, (130, 1), False, 2, "seqs"),
+    (64, 64, (300, 5, 200), (299, 5, 130), True, 1, "wide"),
+    (1000, 72, (20, 31), (20, 30), True, 2, "rows"),                        # few rows: the contraction split
+    (520, 2056, (3, 0, 40, 7, 0, 1, 2), (3, 0, 40, 7, 0, 1, 2), True, 7, "wide"),   # experts, some without rows
+    (264, 1032, (70,) * 6, (70, 69, 0, 1, 70, 64), False, 2, "rows"),
+    (2048, 136, (500,), (490,), False, 1, "rows"),                          # dW split over rows
+    (72, 328, (90,) * 70, tuple(90 if i % 3 else i for i in range(70)), False, 1, "rows"),     # more than 64 sequences
+    (72, 328, (9,) * 130, tuple(9 if i % 3 else i % 9 for i in range(130)), True, 5, "wide"),
+]
+IDS = [f"{c[0]}to{c[1]}-{len(c[2])}x{c[2][0]}-w{c[5]}-{c[6]}" for c in CASES]
+# tiles of 256 by 256 rows and features
+BIG = [
+    (72, 4104, (1500, 900, 700), (1500, 899, 1), True, 3, "wide"),
+    (328, 4096, (3400,), (3333,), False, 1, "rows"),
+]
+BIG_IDS = [f"{c[0]}to{c[1]}" for c in BIG]
+
+
+def setup(case, dtype, cuda, seed):
+    K, N, caps, lens, ragged, E, kind = case
+    gen = torch.Generator().manual_seed(seed)
+    seqs, rows = layout(caps, lens, cuda, ragged)
+    if ragged:   # experts' rows are known on the device only: any may hold all
+        seqs = tdp.Sequences(len(caps), seqs.total_rows, row_range=seqs._keep[0], total_rows=seqs.total_rows,
+                             seq_len=seqs._keep[1])
+    def values(width):
+        x = torch.randn(seqs.total_rows, width, generator=gen).to(DT[dtype])
+        keep = torch.zeros(seqs.total_rows, dtype=torch.bool)
+        for a, _, n in rows:
+            keep[a:a + n] = True
+        x[~keep] = NAN
+        return x
+    w = (torch.randn(E, N, K, generator=gen) * K ** -0.5).to(DT[dtype])
+    return seqs, rows, values, w
+
+
+def check_forward(case, dtype, cuda, seed):
+    K, N, caps, lens, ragged, E, kind = case
+    seqs, rows, values, w = setup(case, dtype, cuda, seed)
+    x = values(K)
+    xd, y = rows_like(seqs, x, cuda, kind), rows_like(seqs, torch.full((seqs.total_rows, N), NAN, dtype=x.dtype), cuda, kind)
+    ws = tdp.allocate_grouped_product_workspace(seqs, E, N, K, DT[dtype], cuda)
+    if ws is not None:
+        ws.fill_(0xff)
+    note(f"product {case[:2]} {case[5:]} {dtype} workspace {0 if ws is None else len(ws)}")
+    tdp.tdp_grouped_product(seqs, xd, w.to(cuda), y, workspace=ws)
+    torch.cuda.synchronize()
+    check_rest("y", flat(y), rows)
+    for s, (a, c, n) in enumerate(rows):
+        check("y", flat(y)[a:a + n], *L.product(x[a:a + n], w[s % E], DT[dtype]))
+
+
+def check_backward(case, dtype, cuda, seed):
+    K, N, caps, lens, ragged, E, kind = case
+    dt = DT[dtype]
+    seqs, rows, values, w = setup(case, dtype, cuda, seed)
+    x, dy = values(K), values(N)
+    xd, gd = rows_like(seqs, x, cuda, kind), rows_like(seqs, dy, cuda, kind)
+    dx, dw = rows_like(seqs, torch.full_like(x, NAN), cuda, kind), torch.full((E, N, K), NAN, device=cuda)
+    ws = tdp.allocate_grouped_product_backward_workspace(seqs, E, N, K, dt, cuda)
+    if ws is not None:
+        ws.fill_(0xff)
+    wd = w.to(cuda)
+    note(f"product gradients {case[:2]} {case[5:]} {dtype} workspace {0 if ws is None else len(ws)}")
+    tdp.tdp_grouped_product_backward(seqs, xd, wd, gd, dx, dw, ws)
+    torch.cuda.synchronize()
+    check_rest("dx", flat(dx), rows)
+    want, bound = torch.zeros(E, N, K, dtype=torch.float64), torch.zeros(E, N, K, dtype=torch.float64)
+    for s, (a, c, n) in enumerate(rows):
+        check("dx", flat(dx)[a:a + n], *L.product(dy[a:a + n], w[s % E].T, dt))
+        xs, gs = x[a:a + n].double(), dy[a:a + n].double()
+        want[s % E] += gs.T @ xs
+        bound[s % E] += gs.abs().T @ xs.abs()
+    # a chain of all rows of a weight and a join's 16
+    check("dw", dw, want, (sum(lens) + 24) * U32 * bound)
+    # one at a time: the same, bit for bit
+    dx2, dw2 = torch.empty_like(dx), torch.empty_like(dw)
+    if kind == "rows":
+        tdp.tdp_grouped_product_backward(seqs, xd, wd, gd, dx2, None, ws)
+        tdp.tdp_grouped_product_backward(seqs, xd, wd, gd, None, dw2, ws)
+        torch.cuda.synchronize()
+        assert torch.equal(dw, dw2)
+        for a, c, n in rows:
+            assert torch.equal(dx[a:a + c], dx2[a:a + c])
+
+
+@pytest.mark.parametrize("dtype", list(DT))
+@pytest.mark.parametrize("case", CASES, ids=IDS)
+def test_grouped_product(case, dtype, cuda):
+    check_forward(case, dtype, cuda, 41)
+
+
+@pytest.mark.parametrize("dtype", list(DT))
+@pytest.mark.parametrize("case", CASES, ids=IDS)
+def test_grouped_product_backward(case, dtype, cuda):
+    check_backward(case, dtype, cuda, 42)
+
+
+@pytest.mark.parametrize("case", BIG, ids=BIG_IDS)
+def test_grouped_product_large_tiles(case, cuda):
+    check_forward(case, "bf16", cuda, 43)
+    K, N, *rest = case
+    check_backward((N, K, *rest), "bf16", cuda, 44)      # dx of many features
+
+
+def test_grouped_product_large_tiles_of_weights(cuda):
+    check_backward((1032, 1000, (70, 300, 1, 65, 130, 90, 80, 0, 3, 64, 66, 20), (70, 299, 1, 65, 130, 90, 80, 0, 3, 64, 66, 20),
+                    True, 12, "wide"), "bf16", cuda, 45)
+
+
+@pytest.mark.parametrize("dtype", list(DT))
+def test_broadcast_rows(dtype, cuda):
+    """Inputs whose rows are one row (stride 0): the end of a sequence repeats nothing."""
+    K, N, n = 72, 40, 37
+    gen = torch.Generator().manual_seed(46)
+    seqs = tdp.Sequences(1, n, seq_len=torch.tensor([n - 2], dtype=torch.int32, device=cuda))
+    x, dy = (torch.randn(1, k, generator=gen).to(DT[dtype]) for k in (K, N))
+    w = torch.randn(N, K, generator=gen).to(DT[dtype])
+    xd, gd = x.to(cuda).expand(n, K), dy.to(cuda).expand(n, N)
+    y, dx = torch.full((n, N), NAN, dtype=x.dtype, device=cuda), torch.full((n, K), NAN, dtype=x.dtype, device=cuda)
+    dw = torch.empty(N, K, device=cuda)
+    note(f"broadcast rows {dtype}")
+    ws = tdp.allocate_grouped_product_workspace(seqs, 1, N, K, DT[dtype], cuda)
+    tdp.tdp_grouped_product(seqs, xd, w.to(cuda), y, workspace=ws)
+    ws = tdp.allocate_grouped_product_backward_workspace(seqs, 1, N, K, DT[dtype], cuda)
+    tdp.tdp_grouped_product_backward(seqs, xd, w.to(cuda), gd, dx, dw, ws)
+    torch.cuda.synchronize()
+    for got, want in ((y, L.product(x, w, DT[dtype])), (dx, L.product(dy, w.T, DT[dtype]))):
+        check("rows", got[:n - 2], want[0].expand(n - 2, -1), want[1].expand(n - 2, -1))
+        assert (got[n - 2:] == 0).all()
+    one = dy.double().T @ x.double()
+    check("dw", dw, (n - 2) * one, (n + 24) * U32 * n * one.abs())

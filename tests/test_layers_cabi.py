@@ -163,3 +163,55 @@ def test_window_attention_workspace():
     for kw, _ in BAD_WINDOWS:
         assert fwd(one, cache, window(**kw)) == 0 and bwd(one, cache, window(**kw)) == 0
     assert fwd(one, cache, window(), hq=3) == 0 and bwd(one, cache, window(), hq=3) == 0
+
+
+def product_call(s=None, x=None, w=P, n=1, y=None, K=128, N=128, dtype=tdp.TDP_F32, ws=P):
+    return tdp.load_library().tdp_grouped_product(ref(s, seqs()), ref(x, rows()), w, n, ref(y, rows(data=2 * P)), K, N,
+                                                  dtype, ws, NULL)
+
+
+def product_backward_call(s=None, x=None, w=P, n=1, dy=None, dx=None, dw=P, K=128, N=128, dtype=tdp.TDP_F32, ws=P):
+    return tdp.load_library().tdp_grouped_product_backward(
+        ref(s, seqs()), ref(x, rows()), w, n, ref(dy, rows(data=2 * P)), ref(dx, rows(data=3 * P)), dw, K, N, dtype, ws,
+        NULL)
+
+
+@pytest.mark.device_abi
+@pytest.mark.parametrize("call", [product_call, product_backward_call], ids=["forward", "backward"])
+def test_grouped_product_refusals(call):
+    for kw, status in BAD_SEQS:
+        assert call(s=seqs(**kw)) == status, kw
+    assert call(s="null") == tdp.TDP_EINVAL
+    for name in ("x", "y") if call is product_call else ("x", "dy", "dx"):
+        for kw, status in BAD_ROWS:
+            assert call(**{name: rows(**kw)}) == status, (name, kw)
+    for kw, status in [(dict(x="null"), tdp.TDP_EINVAL), (dict(w=None), tdp.TDP_EINVAL), (dict(w=P + 8), tdp.TDP_EINVAL),
+                       (dict(K=0), tdp.TDP_ESHAPE), (dict(N=12), tdp.TDP_ESHAPE),
+                       (dict(K=tdp.TDP_MAX_FEATURES + 8), tdp.TDP_ESHAPE), (dict(N=tdp.TDP_MAX_FEATURES + 8), tdp.TDP_ESHAPE),
+                       (dict(n=0), tdp.TDP_EINVAL), (dict(n=5), tdp.TDP_EINVAL), (dict(dtype=2), tdp.TDP_EINVAL),
+                       (dict(x=rows(row_stride=(1 << 21) + 4)), tdp.TDP_ESHAPE)]:
+        assert call(**kw) == status, kw
+    # few rows of wide features: the contraction is split, so a workspace is needed
+    few = dict(s=seqs(max_rows=2, total_rows=8), K=4096, N=4096)
+    for ws in (None, P + 8):
+        assert call(**few, ws=ws) == tdp.TDP_EINVAL and "workspace" in tdp.tdp_last_error()
+    # 2^24 rows of 65536 features: more tiles than a launch holds
+    many = seqs(num_seqs=100, max_rows=1 << 24, total_rows=100 << 24)
+    assert call(s=many, K=65536, N=65536) == tdp.TDP_ESHAPE and "work-items" in tdp.tdp_last_error()
+    if call is product_backward_call:
+        assert call(dw=P + 4) == tdp.TDP_EINVAL
+
+
+def test_grouped_product_workspace():
+    lib = tdp.load_library()
+    fwd = lambda s, n, K, N, dt=tdp.TDP_BF16: lib.tdp_grouped_product_workspace(ctypes.byref(s), n, K, N, dt)  # noqa: E731
+    bwd = lambda s, n, K, N, dt=tdp.TDP_BF16: lib.tdp_grouped_product_backward_workspace(  # noqa: E731
+        ctypes.byref(s), n, K, N, dt)
+    few, many = seqs(max_rows=2, total_rows=8), seqs(max_rows=20000, total_rows=80000)
+    assert fwd(few, 1, 4096, 4096) % (8 * 4096 * 4) == 0 and fwd(few, 1, 4096, 4096) > 0
+    assert fwd(many, 1, 4096, 4096) == 0 and bwd(many, 1, 4096, 4096) == 0
+    assert bwd(many, 1, 128, 128) >= 2 * 128 * 128 * 4     # one tile of weights, its rows split
+    assert bwd(few, 1, 4096, 4096) >= fwd(few, 1, 4096, 4096)
+    for args in ((0, 128, 128), (5, 128, 128), (1, 0, 128), (1, 128, 12), (1, 128, tdp.TDP_MAX_FEATURES + 8)):
+        assert fwd(few, *args) == 0 and bwd(few, *args) == 0
+    assert fwd(few, 1, 4096, 4096, 7) == 0
