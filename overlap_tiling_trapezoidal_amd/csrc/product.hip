@@ -182,6 +182,8 @@ __device__ inline int wave_prefix(int v, int lane) {  // inclusive
   return v;
 }
 
+__device__ inline int last_lane(int v) { return __builtin_amdgcn_readlane(v, 63); }
+
 // Blocks of `rows` rows of every sequence in order, found by whole waves.
 struct RowBlocks {
   const SeqsDev& q;
@@ -193,7 +195,7 @@ struct RowBlocks {
   __device__ inline int total() const {
     if (!q.range) return q.S * ((q.max_rows + rows - 1) / rows);
     int n = 0;
-    for (int s = 0; s < q.S; s += 64) n += __shfl(wave_prefix(count(s + lane), lane), 63);
+    for (int s = 0; s < q.S; s += 64) n += last_lane(wave_prefix(count(s + lane), lane));
     return n;
   }
   // the sequence of block t, which becomes the block's number in it
@@ -208,10 +210,10 @@ struct RowBlocks {
       const uint64_t past = __ballot(end > t);
       if (past) {
         const int l = __builtin_ctzll(past);
-        t -= __shfl(end - n, l);
+        t -= __builtin_amdgcn_readlane(end - n, l);
         return s + l;
       }
-      t -= __shfl(end, 63);
+      t -= last_lane(end);
     }
     return 0;  // not reached: t is below the total
   }
@@ -310,8 +312,7 @@ __global__ __launch_bounds__(64 * WP * WQ) void product_kernel(const ProductArgs
     const RowBlocks rb = {A.seqs, BQ, lane};
     if (!tile_of((uint32_t)rb.total(), A.np, blockIdx.x, tq, tp)) return;
     blk = (int)tq;
-    s = __builtin_amdgcn_readfirstlane(rb.find(blk));
-    blk = __builtin_amdgcn_readfirstlane(blk);
+    s = rb.find(blk);
     sr = seq_rows(A.seqs, s);
     e = s % A.E;
   } else {
@@ -354,8 +355,7 @@ __global__ __launch_bounds__(64 * WP * WQ) void product_kernel(const ProductArgs
     // steps of all sequences of this weight, and the one that this part begins in
     auto steps_of = [&](int sq) { return sq < A.seqs.S ? (seq_rows(A.seqs, sq).len + kStep - 1) / kStep : 0; };
     int steps = 0;
-    for (int i = e; i < A.seqs.S; i += 64 * A.E) steps += __shfl(wave_prefix(steps_of(i + lane * A.E), lane), 63);
-    steps = __builtin_amdgcn_readfirstlane(steps);
+    for (int i = e; i < A.seqs.S; i += 64 * A.E) steps += last_lane(wave_prefix(steps_of(i + lane * A.E), lane));
     const int per = (steps + A.splits - 1) / A.splits;
     t0 = split * per;
     t1 = t0 + per < steps ? t0 + per : steps;
@@ -367,14 +367,12 @@ __global__ __launch_bounds__(64 * WP * WQ) void product_kernel(const ProductArgs
         const uint64_t past = __ballot(end > skip);
         if (past) {
           const int l = __builtin_ctzll(past);
-          skip -= __shfl(end - n, l);
+          skip -= __builtin_amdgcn_readlane(end - n, l);
           seq = i + l * A.E;
           break;
         }
-        skip -= __shfl(end, 63);
+        skip -= last_lane(end);
       }
-    seq = __builtin_amdgcn_readfirstlane(seq);
-    skip = __builtin_amdgcn_readfirstlane(skip);
     sr = seq_rows(A.seqs, seq);
     left = sr.len - skip * kStep;
     pb = A.x.data + eb * seq_base(A.seqs, A.x, seq, sr) + (int64_t)skip * kStep * xrow + f0 * eb;
@@ -382,19 +380,15 @@ __global__ __launch_bounds__(64 * WP * WQ) void product_kernel(const ProductArgs
   }
   P.init(prow);
   Q.init(qrow);
-  int at = t0 * kStep;  // y and dx: the contraction's place
-  auto load = [&](char* pl, char* ql) __attribute__((always_inline)) {
+  int p_at = t0 * kStep, q_at = p_at;  // y and dx: the contraction's place
+  // the next step's operands; of dW, P's goes first and both from the same rows
+  auto load_p = [&](char* pl) __attribute__((always_inline)) {
     if constexpr (KIND == kForward) {
-      P.load(pb, prow, A.N - f0, (inner - at) * eb, wave, pl);
+      P.load(pb, prow, A.N - f0, (inner - p_at) * eb, wave, pl);
       pb += 128;
     } else if constexpr (KIND == kInput) {
-      P.load(pb, prow, inner - at, (A.K - f0) * eb, wave, pl);
+      P.load(pb, prow, inner - p_at, (A.K - f0) * eb, wave, pl);
       pb += (int64_t)kStep * prow;
-    }
-    if constexpr (KIND != kWeight) {
-      Q.load(qb, qrow, sr.len - r0, (inner - at) * eb, wave, ql);
-      qb += 128;
-      at += kStep;
     } else {
       while (left <= 0 && seq + A.E < A.seqs.S) {  // there is a step to load, so a later sequence holds it
         seq += A.E;
@@ -404,40 +398,75 @@ __global__ __launch_bounds__(64 * WP * WQ) void product_kernel(const ProductArgs
         qb = A.y.data + eb * seq_base(A.seqs, A.y, seq, sr) + r0 * eb;
       }
       P.load(pb, prow, left, (A.K - f0) * eb, wave, pl);
-      Q.load(qb, qrow, left, (A.N - r0) * eb, wave, ql);
       pb += (int64_t)kStep * xrow;
+    }
+    p_at += kStep;
+  };
+  auto load_q = [&](char* ql) __attribute__((always_inline)) {
+    if constexpr (KIND != kWeight) {
+      Q.load(qb, qrow, sr.len - r0, (inner - q_at) * eb, wave, ql);
+      qb += 128;
+      q_at += kStep;
+    } else {
+      Q.load(qb, qrow, left, (A.N - r0) * eb, wave, ql);
       qb += (int64_t)kStep * yrow;
       left -= kStep;
     }
   };
-  auto multiply = [&](char* pl, char* ql) __attribute__((always_inline)) {
+  Frag a[2][TP], b[2][TQ];
+  auto read = [&](char* pl, char* ql, int kk, int set) __attribute__((always_inline)) {
 #pragma unroll
-    for (int kk = 0; kk < KK; ++kk) {
-      Frag a[TP], b[TQ];
+    for (int i = 0; i < TP; ++i) a[set][i] = OpP::frag(pl, (wp * TP + i) * 32, kk, lane);
 #pragma unroll
-      for (int i = 0; i < TP; ++i) a[i] = OpP::frag(pl, (wp * TP + i) * 32, kk, lane);
+    for (int j = 0; j < TQ; ++j) b[set][j] = OpQ::frag(ql, (wq * TQ + j) * 32, kk, lane);
+  };
+  auto multiply = [&](int set) __attribute__((always_inline)) {
 #pragma unroll
-      for (int j = 0; j < TQ; ++j) b[j] = OpQ::frag(ql, (wq * TQ + j) * 32, kk, lane);
+    for (int j = 0; j < TQ; ++j)
 #pragma unroll
-      for (int j = 0; j < TQ; ++j)
+      for (int i = 0; i < TP; ++i) acc[j][i] = Mat<T>::mma(a[set][i], b[set][j], acc[j][i]);
+  };
+  // A step is taken in two parts.  Each 16 of the contraction are read while those
+  // before them are multiplied; before the last, the step's buffers are read whole
+  // and the next step's are filled, so the waves meet there, with products still to
+  // do.  No load is under way at that point, which is where the loop closes: the
+  // compiler then knows of every read which loads it need not wait for.
+  auto head = [&](int t, char* pl, char* ql, char* qn) __attribute__((always_inline)) {
 #pragma unroll
-        for (int i = 0; i < TP; ++i) acc[j][i] = Mat<T>::mma(a[i], b[j], acc[j][i]);
+    for (int kk = 0; kk < KK - 1; ++kk) {
+      read(pl, ql, kk + 1, (kk + 1) & 1);
+      if (kk == 0 && t + 1 < t1) load_q(qn);
+      __builtin_amdgcn_sched_barrier(0);
+      multiply(kk & 1);
+      __builtin_amdgcn_sched_barrier(0);
     }
+    wait_barrier<0>();
+  };
+  auto tail = [&](int t, char* pl, char* pn, char* qn) __attribute__((always_inline)) {
+    if (t + 1 < t1) read(pn, qn, 0, 0);
+    if (t + 2 < t1) load_p(pl);
+    __builtin_amdgcn_sched_barrier(0);
+    multiply(1);
+    __builtin_amdgcn_sched_barrier(0);
   };
   if (t0 < t1) {
-    load(p0, q0);
+    load_p(p0);
+    load_q(q0);
+    if (t0 + 1 < t1) load_p(p1);
+    wait_barrier<0>();
+    read(p0, q0, 0, 0);
     int t = t0;
-    for (; t + 1 < t1; t += 2) {
-      wait_barrier<0>();
-      load(p1, q1);
-      multiply(p0, q0);
-      wait_barrier<0>();
-      if (t + 2 < t1) load(p0, q0);
-      multiply(p1, q1);
+    head(t, p0, q0, q1);
+    for (; t + 2 < t1; t += 2) {
+      tail(t, p0, p1, q1);
+      head(t + 1, p1, q1, q0);
+      tail(t + 1, p1, p0, q0);
+      head(t + 2, p0, q0, q1);
     }
-    if (t < t1) {
-      wait_barrier<0>();
-      multiply(p0, q0);
+    tail(t, p0, p1, q1);
+    if (t + 1 < t1) {
+      head(t + 1, p1, q1, q0);
+      tail(t + 1, p1, p0, q0);
     }
   }
   __syncthreads();
@@ -473,7 +502,7 @@ __global__ __launch_bounds__(kJoin) void product_join_kernel(const ProductArgs A
   const RowBlocks rb = {A.seqs, rows, lane};
   int blk = blockIdx.x;
   if (blk >= rb.total()) return;
-  const int s = __builtin_amdgcn_readfirstlane(rb.find(blk));
+  const int s = rb.find(blk);
   const SeqRows sr = seq_rows(A.seqs, s);
   const int per = features / 4, c = (blockIdx.y * kJoin + threadIdx.x) % per, r = (blockIdx.y * kJoin + threadIdx.x) / per;
   const int row = blk * rows + r;
