@@ -68,39 +68,62 @@ struct ProductArgs {
   FastDiv by_np;
 };
 
-// An operand whose contraction runs along its rows: ROWS rows of 128 bytes in
-// LDS, chunk c of row r at c ^ (r / 2 % 8), so that 16 lanes reading one chunk of
-// 16 rows meet every bank once.
+// 16 bytes per lane from a buffer straight into 1 KB of LDS.  Written out because
+// the compiler, which cannot tell the stages of a ring of buffers apart around a
+// loop, makes reads of one wait for loads into the others; wait_barrier says what
+// has to be there.  Nothing is returned in registers.  `lds` and the descriptor
+// are the same in all lanes.
+__device__ inline void load_lds(const u32x4& buffer, uint32_t lds, uint32_t off) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
+               :
+               : "s"(lds), "v"(off), "s"(buffer)
+               : "memory", "m0");
+}
+__device__ inline uint32_t lds_address(const char* p) { return (uint32_t)(uintptr_t)(TDP_LDS const char*)p; }
+// Bytes past `span` read as zeros.
+__device__ inline u32x4 buffer_of(const char* base, uint32_t span) {
+  const uint64_t a = reinterpret_cast<uintptr_t>(base);
+  return u32x4{(uint32_t)__builtin_amdgcn_readfirstlane((int)a),
+               (uint32_t)__builtin_amdgcn_readfirstlane((int)(a >> 32)) & 0xffffu,
+               (uint32_t)__builtin_amdgcn_readfirstlane((int)span), 0x00020000u};
+}
+
+// A stage is 128 bytes of the contraction: whole cache lines where it runs along
+// the operand's rows.  Half of that makes every line cross from L2 twice (256 by
+// 256 tiles of 8192 x 8192 x 8192: 884 us against 7xx).
+constexpr int kStageBytes = 128;
+
+// An operand whose contraction runs along its rows: ROWS rows in LDS, chunk c of
+// row r at c ^ swizzle(r), so that 16 lanes reading one chunk of 16 rows meet
+// every bank once.
 template <int T, int ROWS, int THREADS>
 struct Along {
   typedef typename Mat<T>::Frag Frag;
-  static constexpr int kBytes = ROWS * 128, kLoads = ROWS * 8 / THREADS;
-  static_assert(ROWS * 8 % THREADS == 0 && THREADS / 8 % 16 == 0, "whole loads");
+  static constexpr int kChunks = kStageBytes / 16, kBytes = ROWS * kStageBytes, kLoads = kBytes / 16 / THREADS;
+  static_assert(kBytes % (16 * THREADS) == 0 && THREADS / kChunks % 16 == 0, "whole loads");
   uint32_t off[kLoads];
   int chunk16;  // bytes from the row's first to this lane's chunk
+  u32x4 buffer;
+  bool in;
+  __device__ static inline int swizzle(int r) { return r >> 1 & 7; }
   __device__ inline void init(uint32_t row_bytes) {
-    const int r = threadIdx.x / 8;
-    chunk16 = ((threadIdx.x % 8) ^ (r >> 1 & 7)) * 16;
+    const int r = threadIdx.x / kChunks;
+    chunk16 = ((threadIdx.x % kChunks) ^ swizzle(r)) * 16;
 #pragma unroll
-    for (int n = 0; n < kLoads; ++n) off[n] = (r + n * (THREADS / 8)) * row_bytes + chunk16;
+    for (int n = 0; n < kLoads; ++n) off[n] = (r + n * (THREADS / kChunks)) * row_bytes + chunk16;
   }
-  // `rows` rows from `base` on, of which `left` bytes remain
-  __device__ inline void load(const char* base, uint32_t row_bytes, int rows, int left, int wave, char* lds) const {
-#ifdef __HIP_DEVICE_COMPILE__
-    const uint32_t span = rows > 0 && left > 0 ? (uint32_t)((rows < ROWS ? rows : ROWS) - 1) * row_bytes + left : 0;
-    const __amdgpu_buffer_rsrc_t rs = __builtin_amdgcn_make_buffer_rsrc(
-        const_cast<char*>(base), 0, __builtin_amdgcn_readfirstlane(span), 0x00020000);
-    const bool in = chunk16 < left;
-#pragma unroll
-    for (int n = 0; n < kLoads; ++n)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (TDP_LDS void*)(lds + (n * THREADS + wave * 64) * 16), 16,
-                                               in ? off[n] : 0xfffffff0u, 0, 0, 0);
-#endif
+  // the next loads: `rows` rows from `base` on, of which `left` bytes remain
+  __device__ inline void seek(const char* base, uint32_t row_bytes, int rows, int left) {
+    buffer = buffer_of(base, rows > 0 && left > 0 ? (uint32_t)((rows < ROWS ? rows : ROWS) - 1) * row_bytes + left : 0);
+    in = chunk16 < left;
+  }
+  __device__ inline void load(int n, uint32_t lds, int wave) const {
+    load_lds(buffer, lds + (n * THREADS + wave * 64) * 16, in ? off[n] : 0xfffffff0u);
   }
   // rows r0 + lane % 32, contractions 16 kk + 8h ..
   __device__ static inline Frag frag(const char* lds, int r0, int kk, int lane) {
-    const int r = r0 + (lane & 31), h = lane >> 5, s = r >> 1 & 7;
-    const char* row = lds + r * 128;
+    const int r = r0 + (lane & 31), h = lane >> 5, s = swizzle(r);
+    const char* row = lds + r * kStageBytes;
     if constexpr (T == TDP_BF16) {
       return *reinterpret_cast<const bf16x8*>(row + ((2 * kk + h) ^ s) * 16);
     } else {
@@ -111,34 +134,32 @@ struct Along {
   }
 };
 
-// An operand whose contraction runs across its rows: 128 bytes' worth of rows of
-// COLS elements, chunk c of row r at c ^ 4 (r % 4): the four rows that a
-// transposing read touches lie in different quarters of the banks.
+// An operand whose contraction runs across its rows, which hold COLS elements,
+// chunk c of row r at c ^ 4 (r % 4): the four rows that a transposing read touches
+// lie in different quarters of the banks.
 template <int T, int COLS, int THREADS>
 struct Across {
   typedef typename Mat<T>::Frag Frag;
-  static constexpr int kRow = COLS * Mat<T>::kBytes, kChunks = kRow / 16, kRows = 128 / Mat<T>::kBytes;
+  static constexpr int kRow = COLS * Mat<T>::kBytes, kChunks = kRow / 16, kRows = kStageBytes / Mat<T>::kBytes;
   static constexpr int kBytes = kRows * kRow, kLoads = kBytes / 16 / THREADS;
-  static_assert(THREADS % kChunks == 0 && THREADS / kChunks % 4 == 0, "whole rows");
+  static_assert(kBytes % (16 * THREADS) == 0 && THREADS % kChunks == 0 && THREADS / kChunks % 4 == 0, "whole rows");
   uint32_t off[kLoads];
-  int row;
+  int row, rows_left;
+  u32x4 buffer;
   __device__ inline void init(uint32_t row_bytes) {
     row = threadIdx.x / kChunks;
     const int c = (threadIdx.x % kChunks) ^ ((row & 3) << 2);
 #pragma unroll
     for (int n = 0; n < kLoads; ++n) off[n] = (row + n * (THREADS / kChunks)) * row_bytes + c * 16;
   }
-  // `rows` rows from `base` on, each with `left` bytes from there
-  __device__ inline void load(const char* base, uint32_t row_bytes, int rows, int left, int wave, char* lds) const {
-#ifdef __HIP_DEVICE_COMPILE__
-    const uint32_t span = rows > 0 ? (uint32_t)((rows < kRows ? rows : kRows) - 1) * row_bytes + left : 0;
-    const __amdgpu_buffer_rsrc_t rs = __builtin_amdgcn_make_buffer_rsrc(
-        const_cast<char*>(base), 0, __builtin_amdgcn_readfirstlane(span), 0x00020000);
-#pragma unroll
-    for (int n = 0; n < kLoads; ++n)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (TDP_LDS void*)(lds + (n * THREADS + wave * 64) * 16), 16,
-                                               row + n * (THREADS / kChunks) < rows ? off[n] : 0xfffffff0u, 0, 0, 0);
-#endif
+  // the next loads: `rows` rows from `base` on, each with `left` bytes from there
+  __device__ inline void seek(const char* base, uint32_t row_bytes, int rows, int left) {
+    buffer = buffer_of(base, rows > 0 ? (uint32_t)((rows < kRows ? rows : kRows) - 1) * row_bytes + left : 0);
+    rows_left = rows;
+  }
+  __device__ inline void load(int n, uint32_t lds, int wave) const {
+    load_lds(buffer, lds + (n * THREADS + wave * 64) * 16,
+             row + n * (THREADS / kChunks) < rows_left ? off[n] : 0xfffffff0u);
   }
   __device__ static inline Frag frag(char* lds, int c0, int kk, int lane) {
     const int h = lane >> 5;
@@ -162,15 +183,24 @@ struct Across {
   }
 };
 
-// Wait for this wave's loads into LDS, all but the last N of them, and for its
-// reads of LDS, then for the other waves.  The compiler moves no access of memory
+// Wait for this wave's loads into LDS, all but the last N of them (63: none), and
+// for its reads of LDS, then for the other waves.  The compiler moves no access of memory
 // across.
 template <int N>
 __device__ inline void wait_barrier() {
+  static_assert(N < 64, "six bits");
   asm volatile("" ::: "memory");
   __builtin_amdgcn_s_waitcnt((N & 15) | 0x0070 | (N >> 4) << 14);  // vmcnt(N) lgkmcnt(0)
   __builtin_amdgcn_s_barrier();
   asm volatile("" ::: "memory");
+}
+
+// The same where only some waves wait for loads.
+template <int N>
+__device__ inline void wait_barrier_if(bool loads) {
+  asm volatile("" ::: "memory");
+  if (loads) __builtin_amdgcn_s_waitcnt((N & 15) | 0x0f70 | (N >> 4) << 14);
+  wait_barrier<63>();
 }
 
 __device__ inline int wave_prefix(int v, int lane) {  // inclusive
@@ -285,21 +315,46 @@ __device__ inline void store_tile(char* out, int64_t row_bytes, int len, int cap
   }
 }
 
-// BP x BQ output tile per workgroup of WP x WQ waves, 128 bytes of the
-// contraction at a time, two LDS buffers: the next step's operands are on their
-// way while this step's are multiplied.
-template <int T, int KIND, int BP, int BQ, int WP, int WQ>
+// Where an operand of dW reads next: rows of the sequences e, e + step, ... that
+// share a weight, one sequence after another.
+struct RowCursor {
+  int seq, left;  // rows not yet read of the sequence
+  const char* at;
+  __device__ inline void begin(const SeqsDev& q, const HeadsDev& t, int s, int skip, int eb, int64_t offset) {
+    const SeqRows r = seq_rows(q, s);
+    seq = s;
+    left = r.len - skip;
+    at = t.data + eb * (seq_base(q, t, s, r) + skip * t.row_stride) + offset;
+  }
+  // to a sequence with rows left, if there is one
+  __device__ inline void settle(const SeqsDev& q, const HeadsDev& t, int step, int eb, int64_t offset) {
+    while (left <= 0 && seq + step < q.S) begin(q, t, seq + step, 0, eb, offset);
+  }
+};
+
+// BP x BQ output tile per workgroup of WP x WQ waves, in one of two ways.
+//
+// Eight waves, 256 by 256 (bf16): two waves share a SIMD and take turns, one
+// multiplying 32 of the contraction (16 matrix instructions back to back) while
+// the other reads its next operands from LDS and sends loads out; a barrier ends
+// each turn.  P has three buffers of a stage and Q two, all of the 160 KB: loads
+// have a whole stage's products to arrive behind.
+//
+// Four waves: STAGES buffers of both, each 16 of the contraction read while the
+// 16 before are multiplied; two workgroups or more share a CU and fill each
+// other's waits.
+template <int T, int KIND, int BP, int BQ, int WP, int WQ, int STAGES>
 __global__ __launch_bounds__(64 * WP * WQ) void product_kernel(const ProductArgs A) {
-  constexpr int THREADS = 64 * WP * WQ, eb = Mat<T>::kBytes, kStep = 128 / eb, KK = kStep / 16;
+  constexpr int THREADS = 64 * WP * WQ, eb = Mat<T>::kBytes, kStep = kStageBytes / eb, KK = kStep / 16;
   constexpr int TP = BP / WP / 32, TQ = BQ / WQ / 32;
+  constexpr bool kTurns = WP * WQ == 8;
   typedef typename Mat<T>::Frag Frag;
   typedef std::conditional_t<KIND == kForward, Along<T, BP, THREADS>, Across<T, BP, THREADS>> OpP;
   typedef std::conditional_t<KIND == kWeight, Across<T, BQ, THREADS>, Along<T, BQ, THREADS>> OpQ;
-  __shared__ __align__(16) char p0[OpP::kBytes];
-  __shared__ __align__(16) char q0[OpQ::kBytes];
-  __shared__ __align__(16) char p1[OpP::kBytes];
-  __shared__ __align__(16) char q1[OpQ::kBytes];
-  static_assert(OpP::kBytes >= 4096 * WP * WQ, "the epilogue's place");
+  constexpr int kP = kTurns ? 3 : STAGES, kQ = kTurns ? 2 : STAGES;  // buffers
+  __shared__ __align__(1024) char lds_p[kP * OpP::kBytes];
+  __shared__ __align__(1024) char lds_q[kQ * OpQ::kBytes];
+  static_assert(kP * OpP::kBytes >= 4096 * WP * WQ, "the epilogue's place");
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
   const int wp = wave % WP, wq = wave / WP;
 
@@ -336,19 +391,19 @@ __global__ __launch_bounds__(64 * WP * WQ) void product_kernel(const ProductArgs
     for (int i = 0; i < TP; ++i) acc[j][i] = zero16();
 
   // where the next loads begin
-  const char *pb, *qb;
   uint32_t prow, qrow;
   int t0, t1;  // steps
-  int seq = 0, left = 0;  // dW: the sequence being read and its rows not yet read
+  RowCursor pc, qc;  // dW; y and dx use `at` alone
   if constexpr (KIND != kWeight) {
     const int steps = r0 < sr.len ? (inner + kStep - 1) / kStep : 0, per = (steps + A.splits - 1) / A.splits;
     t0 = split * per;
     t1 = t0 + per < steps ? t0 + per : steps;
     const HeadsDev& in = KIND == kForward ? A.x : A.y;
     qrow = (uint32_t)(in.row_stride * eb);
-    qb = in.data + eb * (seq_base(A.seqs, in, s, sr) + r0 * in.row_stride) + (int64_t)t0 * 128;
+    qc.at = in.data + eb * (seq_base(A.seqs, in, s, sr) + r0 * in.row_stride) + (int64_t)t0 * kStageBytes;
     prow = (uint32_t)A.K * eb;
-    pb = KIND == kForward ? w + (int64_t)f0 * prow + (int64_t)t0 * 128 : w + (int64_t)t0 * kStep * prow + f0 * eb;
+    pc.at = KIND == kForward ? w + (int64_t)f0 * prow + (int64_t)t0 * kStageBytes
+                             : w + (int64_t)t0 * kStep * prow + f0 * eb;
   } else {
     prow = (uint32_t)xrow;
     qrow = (uint32_t)yrow;
@@ -359,8 +414,7 @@ __global__ __launch_bounds__(64 * WP * WQ) void product_kernel(const ProductArgs
     const int per = (steps + A.splits - 1) / A.splits;
     t0 = split * per;
     t1 = t0 + per < steps ? t0 + per : steps;
-    int skip = t0;
-    seq = e;
+    int skip = t0, seq = e;
     if (t0 < t1)
       for (int i = e; i < A.seqs.S; i += 64 * A.E) {
         const int n = steps_of(i + lane * A.E), end = wave_prefix(n, lane);
@@ -373,105 +427,184 @@ __global__ __launch_bounds__(64 * WP * WQ) void product_kernel(const ProductArgs
         }
         skip -= last_lane(end);
       }
-    sr = seq_rows(A.seqs, seq);
-    left = sr.len - skip * kStep;
-    pb = A.x.data + eb * seq_base(A.seqs, A.x, seq, sr) + (int64_t)skip * kStep * xrow + f0 * eb;
-    qb = A.y.data + eb * seq_base(A.seqs, A.y, seq, sr) + (int64_t)skip * kStep * yrow + r0 * eb;
+    pc.begin(A.seqs, A.x, seq, skip * kStep, eb, f0 * eb);
+    qc.begin(A.seqs, A.y, seq, skip * kStep, eb, r0 * eb);
   }
   P.init(prow);
   Q.init(qrow);
   int p_at = t0 * kStep, q_at = p_at;  // y and dx: the contraction's place
-  // the next step's operands; of dW, P's goes first and both from the same rows
-  auto load_p = [&](char* pl) __attribute__((always_inline)) {
+  // Set an operand's next stage up.  Past the last step it holds zeros, or rows of
+  // the next part.
+  auto seek_p = [&]() __attribute__((always_inline)) {
     if constexpr (KIND == kForward) {
-      P.load(pb, prow, A.N - f0, (inner - p_at) * eb, wave, pl);
-      pb += 128;
+      P.seek(pc.at, prow, A.N - f0, (inner - p_at) * eb);
+      pc.at += kStageBytes;
     } else if constexpr (KIND == kInput) {
-      P.load(pb, prow, inner - p_at, (A.K - f0) * eb, wave, pl);
-      pb += (int64_t)kStep * prow;
+      P.seek(pc.at, prow, inner - p_at, (A.K - f0) * eb);
+      pc.at += (int64_t)kStep * prow;
     } else {
-      while (left <= 0 && seq + A.E < A.seqs.S) {  // there is a step to load, so a later sequence holds it
-        seq += A.E;
-        sr = seq_rows(A.seqs, seq);
-        left = sr.len;
-        pb = A.x.data + eb * seq_base(A.seqs, A.x, seq, sr) + f0 * eb;
-        qb = A.y.data + eb * seq_base(A.seqs, A.y, seq, sr) + r0 * eb;
-      }
-      P.load(pb, prow, left, (A.K - f0) * eb, wave, pl);
-      pb += (int64_t)kStep * xrow;
+      pc.settle(A.seqs, A.x, A.E, eb, f0 * eb);
+      P.seek(pc.at, prow, pc.left, (A.K - f0) * eb);
+      pc.at += (int64_t)kStep * xrow;
+      pc.left -= kStep;
     }
     p_at += kStep;
   };
-  auto load_q = [&](char* ql) __attribute__((always_inline)) {
+  auto seek_q = [&]() __attribute__((always_inline)) {
     if constexpr (KIND != kWeight) {
-      Q.load(qb, qrow, sr.len - r0, (inner - q_at) * eb, wave, ql);
-      qb += 128;
-      q_at += kStep;
+      Q.seek(qc.at, qrow, sr.len - r0, (inner - q_at) * eb);
+      qc.at += kStageBytes;
     } else {
-      Q.load(qb, qrow, left, (A.N - r0) * eb, wave, ql);
-      qb += (int64_t)kStep * yrow;
-      left -= kStep;
+      qc.settle(A.seqs, A.y, A.E, eb, r0 * eb);
+      Q.seek(qc.at, qrow, qc.left, (A.N - r0) * eb);
+      qc.at += (int64_t)kStep * yrow;
+      qc.left -= kStep;
     }
+    q_at += kStep;
+  };
+  const uint32_t p0 = lds_address(lds_p), q0 = lds_address(lds_q);
+  auto load_p = [&](int buf, int n) __attribute__((always_inline)) { P.load(n, p0 + buf * OpP::kBytes, wave); };
+  auto load_q = [&](int buf, int n) __attribute__((always_inline)) { Q.load(n, q0 + buf * OpQ::kBytes, wave); };
+  auto fill_p = [&](int buf) __attribute__((always_inline)) {
+    seek_p();
+#pragma unroll
+    for (int n = 0; n < OpP::kLoads; ++n) load_p(buf, n);
+  };
+  auto fill_q = [&](int buf) __attribute__((always_inline)) {
+    seek_q();
+#pragma unroll
+    for (int n = 0; n < OpQ::kLoads; ++n) load_q(buf, n);
   };
   Frag a[2][TP], b[2][TQ];
-  auto read = [&](char* pl, char* ql, int kk, int set) __attribute__((always_inline)) {
+  auto read = [&](int pbuf, int qbuf, int kk, int set) __attribute__((always_inline)) {
 #pragma unroll
-    for (int i = 0; i < TP; ++i) a[set][i] = OpP::frag(pl, (wp * TP + i) * 32, kk, lane);
+    for (int i = 0; i < TP; ++i) a[set][i] = OpP::frag(lds_p + pbuf * OpP::kBytes, (wp * TP + i) * 32, kk, lane);
 #pragma unroll
-    for (int j = 0; j < TQ; ++j) b[set][j] = OpQ::frag(ql, (wq * TQ + j) * 32, kk, lane);
+    for (int j = 0; j < TQ; ++j) b[set][j] = OpQ::frag(lds_q + qbuf * OpQ::kBytes, (wq * TQ + j) * 32, kk, lane);
   };
-  auto multiply = [&](int set) __attribute__((always_inline)) {
+  if constexpr (kTurns) {
+    static_assert(KK == 4, "two turns of 32");
+    // The first four waves run a turn ahead of the others, whose SIMDs they share.
+    // A buffer is free once the second four have read it, one turn behind the first;
+    // these fill Q's in the reading turn after that, the second four already while
+    // they multiply in that time.  What a stage needs of a wave has arrived when the
+    // turn before its first reading ends: the first four wait as they end their
+    // multiplying turn, the others as they end their reading one.
+    const bool ahead = wave < 4;
+    auto products = [&](int buf) __attribute__((always_inline)) {  // buf >= 0: fill Q's meanwhile
+      if (buf >= 0 && !ahead) seek_q();
+      __builtin_amdgcn_s_setprio(1);
 #pragma unroll
-    for (int j = 0; j < TQ; ++j)
+      for (int k = 0; k < 2; ++k)
 #pragma unroll
-      for (int i = 0; i < TP; ++i) acc[j][i] = Mat<T>::mma(a[set][i], b[set][j], acc[j][i]);
-  };
-  // A step is taken in two parts.  Each 16 of the contraction are read while those
-  // before them are multiplied; before the last, the step's buffers are read whole
-  // and the next step's are filled, so the waves meet there, with products still to
-  // do.  No load is under way at that point, which is where the loop closes: the
-  // compiler then knows of every read which loads it need not wait for.
-  auto head = [&](int t, char* pl, char* ql, char* qn) __attribute__((always_inline)) {
+        for (int j = 0; j < TQ; ++j) {
 #pragma unroll
-    for (int kk = 0; kk < KK - 1; ++kk) {
-      read(pl, ql, kk + 1, (kk + 1) & 1);
-      if (kk == 0 && t + 1 < t1) load_q(qn);
+          for (int i = 0; i < TP; ++i) acc[j][i] = Mat<T>::mma(a[k][i], b[k][j], acc[j][i]);
+          if (buf >= 0 && k == 0 && j < OpQ::kLoads) {
+            __builtin_amdgcn_sched_barrier(0);
+            if (!ahead) load_q(buf, j);
+            __builtin_amdgcn_sched_barrier(0);
+          }
+        }
+      __builtin_amdgcn_s_setprio(0);
       __builtin_amdgcn_sched_barrier(0);
-      multiply(kk & 1);
-      __builtin_amdgcn_sched_barrier(0);
+    };
+    static_assert(OpQ::kLoads <= TQ, "a load after each row of products");
+    auto stage = [&](int pbuf, int qbuf) __attribute__((always_inline)) {
+      read(pbuf, qbuf, 0, 0);
+      read(pbuf, qbuf, 1, 1);
+      if (ahead) fill_q(qbuf ^ 1);
+      wait_barrier<63>();
+      products(-1);
+      wait_barrier<63>();
+      read(pbuf, qbuf, 2, 0);
+      read(pbuf, qbuf, 3, 1);
+      fill_p((pbuf + 2) % 3);
+      wait_barrier_if<OpP::kLoads>(!ahead);
+      products(qbuf);
+      wait_barrier_if<OpP::kLoads>(ahead);
+    };
+    if (t0 < t1) {
+      fill_p(0);
+      fill_q(0);
+      fill_p(1);
+      if (ahead) {
+        wait_barrier<OpP::kLoads>();
+      } else {
+        fill_q(1);
+        wait_barrier<OpP::kLoads + OpQ::kLoads>();
+        wait_barrier<63>();
+      }
+      for (int t = t0;;) {
+        stage(0, 0);
+        if (++t >= t1) break;
+        stage(1, 1);
+        if (++t >= t1) break;
+        stage(2, 0);
+        if (++t >= t1) break;
+        stage(0, 1);
+        if (++t >= t1) break;
+        stage(1, 0);
+        if (++t >= t1) break;
+        stage(2, 1);
+        if (++t >= t1) break;
+      }
+      if (ahead) wait_barrier<63>();
     }
-    wait_barrier<0>();
-  };
-  auto tail = [&](int t, char* pl, char* pn, char* qn) __attribute__((always_inline)) {
-    if (t + 1 < t1) read(pn, qn, 0, 0);
-    if (t + 2 < t1) load_p(pl);
-    __builtin_amdgcn_sched_barrier(0);
-    multiply(1);
-    __builtin_amdgcn_sched_barrier(0);
-  };
-  if (t0 < t1) {
-    load_p(p0);
-    load_q(q0);
-    if (t0 + 1 < t1) load_p(p1);
-    wait_barrier<0>();
-    read(p0, q0, 0, 0);
-    int t = t0;
-    head(t, p0, q0, q1);
-    for (; t + 2 < t1; t += 2) {
-      tail(t, p0, p1, q1);
-      head(t + 1, p1, q1, q0);
-      tail(t + 1, p1, p0, q0);
-      head(t + 2, p0, q0, q1);
-    }
-    tail(t, p0, p1, q1);
-    if (t + 1 < t1) {
-      head(t + 1, p1, q1, q0);
-      tail(t + 1, p1, p0, q0);
+  } else {
+    // Ahead of a stage's last 16 its buffers are read whole and the next stage is
+    // there: the waves meet with products still to do, then the buffers are filled
+    // again.  Loads go out one by one between the products, as fast as they are
+    // taken (back to back they hold the wave up).
+    constexpr int kLoads = OpP::kLoads + OpQ::kLoads;
+    static_assert(KK % 2 == 0, "the sets take turns");
+    auto stage = [&](int buf) __attribute__((always_inline)) {
+#pragma unroll
+      for (int kk = 0; kk < KK; ++kk) {
+        const bool last = kk == KK - 1, first = kk == 0;
+        if (last) wait_barrier<(STAGES - 2) * kLoads>();
+        const int next = (buf + 1) % STAGES, before = (buf + STAGES - 1) % STAGES;
+        read(last ? next : buf, last ? next : buf, last ? 0 : kk + 1, ~kk & 1);
+        if (first) seek_q();
+        if (last) seek_p();
+#pragma unroll
+        for (int j = 0; j < TQ; ++j) {
+          __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+          for (int i = 0; i < TP; ++i) acc[j][i] = Mat<T>::mma(a[kk & 1][i], b[kk & 1][j], acc[j][i]);
+          __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+          for (int n = 0; n < OpP::kLoads; ++n)
+            if (last && n * TQ / OpP::kLoads == j) load_p(buf, n);
+#pragma unroll
+          for (int n = 0; n < OpQ::kLoads; ++n)
+            if (first && n * TQ / OpQ::kLoads == j) load_q(before, n);
+        }
+      }
+    };
+    if (t0 < t1) {
+#pragma unroll
+      for (int i = 0; i < STAGES; ++i) {
+        fill_p(i);
+        if (i < STAGES - 1) fill_q(i);
+      }
+      wait_barrier<(STAGES - 1) * kLoads - OpQ::kLoads>();
+      read(0, 0, 0, 0);
+      for (int t = t0;;) {
+        stage(0);
+        if (++t >= t1) break;
+        stage(1);
+        if (++t >= t1) break;
+        if constexpr (STAGES == 3) {
+          stage(2);
+          if (++t >= t1) break;
+        }
+      }
     }
   }
-  __syncthreads();
+  wait_barrier<0>();
   // out
-  char* lds = p0 + wave * 4096;
+  char* lds = lds_p + wave * 4096;
   const int wf = f0 + wp * TP * 32;
 #pragma unroll
   for (int j = 0; j < TQ; ++j) {
@@ -558,7 +691,7 @@ int begin(const char* fn, const tdp_seqs* seqs, const tdp_rows* x, const void* w
 }
 
 // A launch over blocks of rows: y or dx.  Without `enqueue` only its checks.
-template <int T, int KIND, int BP, int BQ, int WP, int WQ>
+template <int T, int KIND, int BP, int BQ, int WP, int WQ, int STAGES>
 int launch_rows(const char* fn, ProductArgs A, const tdp_seqs& seqs, const ProductShape& sh, bool enqueue,
                 hipStream_t st) {
   const int features = KIND == kForward ? A.N : A.K;
@@ -569,7 +702,7 @@ int launch_rows(const char* fn, ProductArgs A, const tdp_seqs& seqs, const Produ
   int rc = check_items(fn, tiles * sh.splits, 64 * WP * WQ);
   if (rc == TDP_OK && sh.splits > 1) rc = check_items(fn, join_x * join_y, kJoin);
   if (rc != TDP_OK || !enqueue) return rc;
-  hipLaunchKernelGGL((product_kernel<T, KIND, BP, BQ, WP, WQ>), dim3((unsigned)tiles, (unsigned)sh.splits),
+  hipLaunchKernelGGL((product_kernel<T, KIND, BP, BQ, WP, WQ, STAGES>), dim3((unsigned)tiles, (unsigned)sh.splits),
                      dim3(64 * WP * WQ), 0, st, A);
   if (sh.splits > 1)
     hipLaunchKernelGGL((product_join_kernel<T>), dim3((unsigned)join_x, (unsigned)join_y), dim3(kJoin), 0, st, A,
@@ -586,7 +719,7 @@ int launch_weight(const char* fn, ProductArgs A, const ProductShape& sh, bool en
   int rc = check_items(fn, tiles * sh.splits, 64 * WP * WQ);
   if (rc == TDP_OK && sh.splits > 1) rc = check_items(fn, (quads + kJoin - 1) / kJoin, kJoin);
   if (rc != TDP_OK || !enqueue) return rc;
-  hipLaunchKernelGGL((product_kernel<T, kWeight, BP, BQ, WP, WQ>), dim3((unsigned)tiles, (unsigned)sh.splits),
+  hipLaunchKernelGGL((product_kernel<T, kWeight, BP, BQ, WP, WQ, 2>), dim3((unsigned)tiles, (unsigned)sh.splits),
                      dim3(64 * WP * WQ), 0, st, A);
   if (sh.splits > 1)
     hipLaunchKernelGGL(weight_join_kernel, dim3((unsigned)((quads + kJoin - 1) / kJoin)), dim3(kJoin), 0, st, A.ws, A.dw,
@@ -598,12 +731,12 @@ template <int KIND>
 int run_rows(const char* fn, const ProductArgs& A, const tdp_seqs& seqs, const ProductShape& sh, int32_t dtype,
              bool enqueue, hipStream_t st) {
   if (dtype == TDP_BF16) {
-    if (sh.rows == 256) return launch_rows<TDP_BF16, KIND, 256, 256, 4, 2>(fn, A, seqs, sh, enqueue, st);
-    if (sh.rows == 128) return launch_rows<TDP_BF16, KIND, 128, 128, 2, 2>(fn, A, seqs, sh, enqueue, st);
-    return launch_rows<TDP_BF16, KIND, 128, 32, 4, 1>(fn, A, seqs, sh, enqueue, st);
+    if (sh.rows == 256) return launch_rows<TDP_BF16, KIND, 256, 256, 4, 2, 2>(fn, A, seqs, sh, enqueue, st);
+    if (sh.rows == 128) return launch_rows<TDP_BF16, KIND, 128, 128, 2, 2, 2>(fn, A, seqs, sh, enqueue, st);
+    return launch_rows<TDP_BF16, KIND, 128, 32, 4, 1, 3>(fn, A, seqs, sh, enqueue, st);
   }
-  if (sh.rows == 128) return launch_rows<TDP_F32, KIND, 128, 128, 2, 2>(fn, A, seqs, sh, enqueue, st);
-  return launch_rows<TDP_F32, KIND, 128, 32, 4, 1>(fn, A, seqs, sh, enqueue, st);
+  if (sh.rows == 128) return launch_rows<TDP_F32, KIND, 128, 128, 2, 2, 2>(fn, A, seqs, sh, enqueue, st);
+  return launch_rows<TDP_F32, KIND, 128, 32, 4, 1, 3>(fn, A, seqs, sh, enqueue, st);
 }
 
 int run_weight(const char* fn, const ProductArgs& A, const ProductShape& sh, int32_t dtype, bool enqueue,
