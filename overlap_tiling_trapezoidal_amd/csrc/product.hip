@@ -62,7 +62,7 @@ struct ProductArgs {
   const char* w;      // (weights, N, K)
   float *dw, *ws;
   int32_t E, N, K;    // weights, output and input features
-  int32_t splits;     // of the contraction
+  int32_t splits;     // y, dx: of the contraction; dW: weight_places
   uint32_t np;        // tiles of output features
   uint32_t nq;        // dW: tiles of W's rows
   FastDiv by_np;
@@ -315,6 +315,39 @@ __device__ inline void store_tile(char* out, int64_t row_bytes, int len, int cap
   }
 }
 
+// dW's work: the steps of each weight's rows, in parts of at most about a
+// `places`-th of all steps, so that a weight with many rows does not outlast the
+// others; the longest parts first, which leaves the short ones to fill the gaps.
+// Weights of one part are written directly, the others' parts go to slots of
+// the workspace: fewer than 2 places, as a weight of n > 1 parts has more than n - 1
+// and so at least n / 2 times a part's steps.  More than 64 weights are taken
+// whole, in order.  All lanes of all waves call it, `lds` has room for 64 numbers.
+struct WeightParts {
+  int steps, n, from, slot;  // a lane's weight: its steps, parts, place among all parts, slot of its first (n > 1)
+  int total;                 // parts of all weights
+  __device__ inline void count(const ProductArgs& A, int step_rows, int lane, int* lds) {
+    if (threadIdx.x < 64) lds[threadIdx.x] = 0;
+    __syncthreads();
+    for (int s = threadIdx.x; s < A.seqs.S; s += blockDim.x)
+      atomicAdd(lds + s % A.E, (seq_rows(A.seqs, s).len + step_rows - 1) / step_rows);  // whole numbers: any order
+    __syncthreads();
+    steps = lane < A.E ? lds[lane] : 0;
+    __syncthreads();
+    const int all = last_lane(wave_prefix(steps, lane)), even = (all + A.splits - 1) / A.splits;
+    const int most = even < kWeightSteps ? kWeightSteps : even;
+    n = lane < A.E ? (steps <= most ? 1 : (steps + most - 1) / most) : 0;
+    const int length = n ? (steps + n - 1) / n : 0;
+    from = 0;
+    for (int j = 0; j < A.E; ++j) {
+      const int lj = __builtin_amdgcn_readlane(length, j), nj = __builtin_amdgcn_readlane(n, j);
+      if (lj > length || (lj == length && j < lane)) from += nj;
+    }
+    const int slots = n > 1 ? n : 0;
+    slot = wave_prefix(slots, lane) - slots;
+    total = last_lane(wave_prefix(n, lane));
+  }
+};
+
 // Where an operand of dW reads next: rows of the sequences e, e + step, ... that
 // share a weight, one sequence after another.
 struct RowCursor {
@@ -362,7 +395,8 @@ __global__ __launch_bounds__(64 * WP * WQ) void product_kernel(const ProductArgs
   uint32_t tq, tp;
   int s = 0, blk = 0, e = 0;
   SeqRows sr = {};
-  const int split = blockIdx.y;
+  const int split = KIND == kWeight ? 0 : blockIdx.y;
+  int w_part = 0, w_parts = 1, w_steps = 0, w_slot = -1;  // dW
   if constexpr (KIND != kWeight) {
     const RowBlocks rb = {A.seqs, BQ, lane};
     if (!tile_of((uint32_t)rb.total(), A.np, blockIdx.x, tq, tp)) return;
@@ -371,10 +405,28 @@ __global__ __launch_bounds__(64 * WP * WQ) void product_kernel(const ProductArgs
     sr = seq_rows(A.seqs, s);
     e = s % A.E;
   } else {
-    const uint32_t per = A.nq * A.np, grid = (per + 7) / 8 * 8;
-    e = blockIdx.x / grid;
-    if (!tile_of(A.nq, A.np, blockIdx.x - e * grid, tq, tp)) return;
+    const uint32_t grid = (A.nq * A.np + 7) / 8 * 8;
+    const int part = blockIdx.x / grid;
+    if (!tile_of(A.nq, A.np, blockIdx.x - part * grid, tq, tp)) return;
     blk = (int)tq;
+    if (A.E <= 64) {
+      WeightParts wp;
+      wp.count(A, kStep, lane, reinterpret_cast<int*>(lds_p));
+      if (part >= wp.total) return;
+      const int l = __builtin_ctzll(__ballot(part >= wp.from && part < wp.from + wp.n));
+      e = l;
+      w_part = part - __builtin_amdgcn_readlane(wp.from, l);
+      w_parts = __builtin_amdgcn_readlane(wp.n, l);
+      w_steps = __builtin_amdgcn_readlane(wp.steps, l);
+      if (w_parts > 1) w_slot = __builtin_amdgcn_readlane(wp.slot, l) + w_part;
+    } else {
+      e = part;
+      for (int i = e; i < A.seqs.S; i += 64 * A.E) {
+        const int sq = i + lane * A.E;
+        const int n = sq < A.seqs.S ? (seq_rows(A.seqs, sq).len + kStep - 1) / kStep : 0;
+        w_steps += last_lane(wave_prefix(n, lane));
+      }
+    }
   }
   const int f0 = (int)tp * BP, r0 = blk * BQ;
   const char* w = A.w + (int64_t)e * A.N * A.K * eb;
@@ -407,13 +459,11 @@ __global__ __launch_bounds__(64 * WP * WQ) void product_kernel(const ProductArgs
   } else {
     prow = (uint32_t)xrow;
     qrow = (uint32_t)yrow;
-    // steps of all sequences of this weight, and the one that this part begins in
+    // the sequence that this part begins in
     auto steps_of = [&](int sq) { return sq < A.seqs.S ? (seq_rows(A.seqs, sq).len + kStep - 1) / kStep : 0; };
-    int steps = 0;
-    for (int i = e; i < A.seqs.S; i += 64 * A.E) steps += last_lane(wave_prefix(steps_of(i + lane * A.E), lane));
-    const int per = (steps + A.splits - 1) / A.splits;
-    t0 = split * per;
-    t1 = t0 + per < steps ? t0 + per : steps;
+    const int per = (w_steps + w_parts - 1) / w_parts;
+    t0 = w_part * per;
+    t1 = t0 + per < w_steps ? t0 + per : w_steps;
     int skip = t0, seq = e;
     if (t0 < t1)
       for (int i = e; i < A.seqs.S; i += 64 * A.E) {
@@ -610,7 +660,8 @@ __global__ __launch_bounds__(64 * WP * WQ) void product_kernel(const ProductArgs
   for (int j = 0; j < TQ; ++j) {
     const int row = r0 + (wq * TQ + j) * 32;
     if constexpr (KIND == kWeight) {
-      float* out = (A.splits > 1 ? A.ws + (int64_t)split * A.E * A.N * A.K : A.dw) + ((int64_t)e * A.N + row) * A.K + wf;
+      float* out = (w_slot >= 0 ? A.ws + (int64_t)w_slot * A.N * A.K : A.dw + (int64_t)e * A.N * A.K) +
+                   (int64_t)row * A.K + wf;
       store_tile<TDP_F32, TP>(reinterpret_cast<char*>(out), (int64_t)A.K * 4, A.N - row, A.N - row, A.K - wf, acc[j],
                               lane, lds);
     } else if (A.splits > 1) {
@@ -655,13 +706,27 @@ __global__ __launch_bounds__(kJoin) void product_join_kernel(const ProductArgs A
   }
 }
 
-__global__ __launch_bounds__(kJoin) void weight_join_kernel(const float* parts, float* dw, int64_t quads, int splits) {
-  const int64_t i = (int64_t)blockIdx.x * kJoin + threadIdx.x;
-  if (i >= quads) return;
-  f32x4 v = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll 4
-  for (int k = 0; k < splits; ++k) v += reinterpret_cast<const f32x4*>(parts)[k * quads + i];
-  reinterpret_cast<f32x4*>(dw)[i] = v;
+// dW of the weights of several parts, summed in order: a workgroup per weight and
+// 16 quads per thread.
+constexpr int kJoinQuads = 16;
+__global__ __launch_bounds__(kJoin) void weight_join_kernel(const ProductArgs A, int step_rows) {
+  __shared__ int counts[64];
+  const int lane = threadIdx.x & 63, e = blockIdx.y;
+  WeightParts wp;
+  wp.count(A, step_rows, lane, counts);
+  const int n = __builtin_amdgcn_readlane(wp.n, e);
+  if (n == 1) return;
+  const int64_t quads = (int64_t)A.N * A.K / 4;
+  const f32x4* parts = reinterpret_cast<const f32x4*>(A.ws) + __builtin_amdgcn_readlane(wp.slot, e) * quads;
+  f32x4* out = reinterpret_cast<f32x4*>(A.dw) + e * quads;
+#pragma unroll 2
+  for (int k = 0; k < kJoinQuads; ++k) {
+    const int64_t i = ((int64_t)blockIdx.x * kJoinQuads + k) * kJoin + threadIdx.x;
+    if (i >= quads) return;
+    f32x4 v = parts[i];
+    for (int j = 1; j < n; ++j) v += parts[j * quads + i];
+    out[i] = v;
+  }
 }
 
 int check_items(const char* fn, int64_t workgroups, int threads) {
@@ -715,15 +780,18 @@ int launch_weight(const char* fn, ProductArgs A, const ProductShape& sh, bool en
   A.np = (uint32_t)((A.K + BP - 1) / BP);
   A.nq = (uint32_t)((A.N + BQ - 1) / BQ);
   A.splits = sh.splits;
-  const int64_t tiles = ((int64_t)A.np * A.nq + 7) / 8 * 8 * A.E, quads = (int64_t)A.E * A.N * A.K / 4;
-  int rc = check_items(fn, tiles * sh.splits, 64 * WP * WQ);
-  if (rc == TDP_OK && sh.splits > 1) rc = check_items(fn, (quads + kJoin - 1) / kJoin, kJoin);
+  // of weights split at `places`: at most one part more each than `places` in all
+  const int64_t parts = A.E + (sh.splits > 1 ? sh.splits : 0), quads = (int64_t)A.N * A.K / 4;
+  const int64_t tiles = ((int64_t)A.np * A.nq + 7) / 8 * 8 * parts;
+  const int64_t join = (quads + kJoin * kJoinQuads - 1) / (kJoin * kJoinQuads);
+  int rc = check_items(fn, tiles, 64 * WP * WQ);
+  if (rc == TDP_OK && sh.splits > 1) rc = check_items(fn, join * A.E, kJoin);
   if (rc != TDP_OK || !enqueue) return rc;
-  hipLaunchKernelGGL((product_kernel<T, kWeight, BP, BQ, WP, WQ, 2>), dim3((unsigned)tiles, (unsigned)sh.splits),
-                     dim3(64 * WP * WQ), 0, st, A);
+  hipLaunchKernelGGL((product_kernel<T, kWeight, BP, BQ, WP, WQ, 2>), dim3((unsigned)tiles), dim3(64 * WP * WQ), 0, st,
+                     A);
   if (sh.splits > 1)
-    hipLaunchKernelGGL(weight_join_kernel, dim3((unsigned)((quads + kJoin - 1) / kJoin)), dim3(kJoin), 0, st, A.ws, A.dw,
-                       quads, sh.splits);
+    hipLaunchKernelGGL(weight_join_kernel, dim3((unsigned)join, (unsigned)A.E), dim3(kJoin), 0, st, A,
+                       kStageBytes / Mat<T>::kBytes);
   return TDP_OK;
 }
 

@@ -256,14 +256,23 @@ inline ProductShape rows_shape(const tdp_seqs& s, int32_t features, int32_t inne
   sh.splits = product_splits(tiles, places, inner * dtype_bytes(dtype) / 128, 4);
   return sh;
 }
-// dW: its tile of W's rows is `rows` too, the contraction the rows of a weight's sequences.
+// dW: its tile of W's rows is `rows` too, the contraction the rows of a weight's
+// sequences.  How many rows a weight has is known on the device only, so `splits`
+// says in how many parts the rows of all weights are cut where one has them all
+// (parts of less than kWeightSteps steps are not worth a slot).
+constexpr int kWeightSteps = 8;
+constexpr int kWeightMaxPlaces = 64;
 inline ProductShape weight_shape(const tdp_seqs& s, int32_t weights, int32_t in_features, int32_t out_features,
                                  int32_t dtype) {
   const int64_t big = weights * tiles_across(in_features, 256) * tiles_across(out_features, 256);
   ProductShape sh = {dtype == TDP_BF16 && big >= 192 ? 256 : 128, 1};
-  const int64_t tiles = weights * tiles_across(in_features, sh.rows) * tiles_across(out_features, sh.rows);
-  sh.splits = product_splits(tiles, sh.rows == 256 ? 256 : 512,
-                             s.total_rows / weights * dtype_bytes(dtype) / 128, 8);
+  if (weights > 64) return sh;
+  const int64_t tiles = tiles_across(in_features, sh.rows) * tiles_across(out_features, sh.rows);
+  int64_t n = (sh.rows == 256 ? 256 : 512) / tiles;
+  const int64_t steps = s.total_rows * dtype_bytes(dtype) / 128;
+  if (n > steps / kWeightSteps) n = steps / kWeightSteps;
+  if (n > kWeightMaxPlaces) n = kWeightMaxPlaces;
+  sh.splits = n < 2 ? 1 : (int)n;
   return sh;
 }
 inline int64_t rows_workspace(const tdp_seqs& s, int32_t features, int32_t inner, int32_t dtype) {
@@ -273,7 +282,7 @@ inline int64_t rows_workspace(const tdp_seqs& s, int32_t features, int32_t inner
 inline int64_t weight_workspace(const tdp_seqs& s, int32_t weights, int32_t in_features, int32_t out_features,
                                 int32_t dtype) {
   const ProductShape sh = weight_shape(s, weights, in_features, out_features, dtype);
-  return sh.splits == 1 ? 0 : align256((int64_t)sh.splits * weights * in_features * out_features * 4);
+  return sh.splits == 1 ? 0 : align256((int64_t)2 * sh.splits * in_features * out_features * 4);
 }
 int check_product(const char* fn, const tdp_seqs* seqs, int32_t num_weights, int32_t in_features,
                   int32_t out_features);
