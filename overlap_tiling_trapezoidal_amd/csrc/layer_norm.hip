@@ -9,7 +9,8 @@
 // costs no digits), and is written once.  G lanes share a row, eight elements of
 // it per lane NV times; rows wider than one wave holds take the workgroup.  A
 // workgroup takes several blocks of rows, the next one's loads in flight while
-// this one is worked on, and keeps the weights in registers.
+// this one is worked on, and keeps the weights in registers.  247296 rows of 2048
+// bf16 (2.03 GB) take 357 us, 5.7 TB/s of the 5.96 that a plain copy reaches.
 #include <hip/hip_runtime.h>
 #include <math.h>
 #include <stdint.h>
@@ -169,7 +170,9 @@ __global__ __launch_bounds__(kTok) void layer_norm_kernel(const NormArgs A) {
 }
 
 // dx, and each workgroup's sums of dw and db over its rows, fp32 in a fixed
-// order.  A workgroup keeps to one set of weights.
+// order.  A workgroup keeps to one set of weights.  On 35840 rows of 2048 bf16
+// (440 MB) 81 us with the join, 5.4 TB/s; a workgroup per row, whose eight elements
+// per lane need fewer registers, takes 99 for the barriers of its sums.
 template <int T, int G, int NV>
 __global__ __launch_bounds__(kTok) void layer_norm_backward_kernel(const NormArgs A) {
   typedef Lane<T, G, NV> L;
@@ -279,6 +282,7 @@ __global__ __launch_bounds__(kTok) void layer_norm_join_kernel(const float* part
   const int col = threadIdx.x & 15, row = threadIdx.x >> 4, c = (blockIdx.x - set * per) * 16 + col;
   float v = 0.0f;
   if (c < 2 * C)
+#pragma unroll 8
     for (int r = row; r < nparts; r += 16) v += parts[((int64_t)set * nparts + r) * 2 * C + c];
   red[row][col] = v;
   __syncthreads();
@@ -350,8 +354,11 @@ int tdp_layer_norm(const tdp_seqs* seqs, const tdp_rows* x, const float* weight,
   if (reinterpret_cast<uintptr_t>(bias) & 3) return fail(TDP_EINVAL, "%s: bias must be 4-byte aligned", fn);
   A.b = bias;
   const int64_t blocks = (int64_t)A.blocks * seqs->num_seqs;
+  // Blocks per workgroup, as long as 16 workgroups per CU remain: one leaves the
+  // weights to be read again for every row, many leave few workgroups to even out
+  // (247296 rows of 2048 bf16: 446 us with 1, 382 with 2, 357 with 4, 375 with 8).
   int64_t per = blocks / 4096;
-  per = per < 1 ? 1 : per > 8 ? 8 : per;
+  per = per < 1 ? 1 : per > 4 ? 4 : per;
   A.per_wg = (uint32_t)per;
   const int64_t grid = (blocks + per - 1) / per;
   if (blocks > INT32_MAX || grid * kTok > 0xffffffffLL)

@@ -73,12 +73,15 @@ struct ProductArgs {
 // loop, makes reads of one wait for loads into the others; wait_barrier says what
 // has to be there.  Nothing is returned in registers.  `lds` and the descriptor
 // are the same in all lanes.
+#pragma clang diagnostic push
+#pragma clang diagnostic ignored "-Winline-asm"  // that m0 is not kept, which nothing here relies on
 __device__ inline void load_lds(const u32x4& buffer, uint32_t lds, uint32_t off) {
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
                :
                : "s"(lds), "v"(off), "s"(buffer)
                : "memory", "m0");
 }
+#pragma clang diagnostic pop
 __device__ inline uint32_t lds_address(const char* p) { return (uint32_t)(uintptr_t)(TDP_LDS const char*)p; }
 // Bytes past `span` read as zeros.
 __device__ inline u32x4 buffer_of(const char* base, uint32_t span) {
@@ -142,6 +145,7 @@ struct Across {
   typedef typename Mat<T>::Frag Frag;
   static constexpr int kRow = COLS * Mat<T>::kBytes, kChunks = kRow / 16, kRows = kStageBytes / Mat<T>::kBytes;
   static constexpr int kBytes = kRows * kRow, kLoads = kBytes / 16 / THREADS;
+  static_assert(kChunks % 16 == 0, "room for the swizzle");
   static_assert(kBytes % (16 * THREADS) == 0 && THREADS % kChunks == 0 && THREADS / kChunks % 4 == 0, "whole rows");
   uint32_t off[kLoads];
   int row, rows_left;
@@ -798,13 +802,14 @@ int launch_weight(const char* fn, ProductArgs A, const ProductShape& sh, bool en
 template <int KIND>
 int run_rows(const char* fn, const ProductArgs& A, const tdp_seqs& seqs, const ProductShape& sh, int32_t dtype,
              bool enqueue, hipStream_t st) {
+  constexpr int NB = KIND == kForward ? kNarrowY : kNarrowDx;
   if (dtype == TDP_BF16) {
     if (sh.rows == 256) return launch_rows<TDP_BF16, KIND, 256, 256, 4, 2, 2>(fn, A, seqs, sh, enqueue, st);
     if (sh.rows == 128) return launch_rows<TDP_BF16, KIND, 128, 128, 2, 2, 2>(fn, A, seqs, sh, enqueue, st);
-    return launch_rows<TDP_BF16, KIND, 128, 32, 4, 1, 3>(fn, A, seqs, sh, enqueue, st);
+    return launch_rows<TDP_BF16, KIND, NB, 32, NB / 32, 1, 2>(fn, A, seqs, sh, enqueue, st);
   }
   if (sh.rows == 128) return launch_rows<TDP_F32, KIND, 128, 128, 2, 2, 2>(fn, A, seqs, sh, enqueue, st);
-  return launch_rows<TDP_F32, KIND, 128, 32, 4, 1, 3>(fn, A, seqs, sh, enqueue, st);
+  return launch_rows<TDP_F32, KIND, NB, 32, NB / 32, 1, 2>(fn, A, seqs, sh, enqueue, st);
 }
 
 int run_weight(const char* fn, const ProductArgs& A, const ProductShape& sh, int32_t dtype, bool enqueue,
@@ -834,7 +839,7 @@ int tdp_grouped_product(const tdp_seqs* seqs, const tdp_rows* x, const void* wei
   ProductArgs A = {};
   int st = begin(fn, seqs, x, weight, num_weights, y, in_features, out_features, dtype, &A);
   if (st != TDP_OK) return st;
-  const ProductShape sh = rows_shape(*seqs, out_features, in_features, dtype);
+  const ProductShape sh = rows_shape(*seqs, out_features, in_features, dtype, kNarrowY);
   st = check_workspace(fn, sh, workspace);
   if (st != TDP_OK) return st;
   A.ws = static_cast<float*>(workspace);
@@ -855,7 +860,7 @@ int tdp_grouped_product_backward(const tdp_seqs* seqs, const tdp_rows* x, const 
   if (st != TDP_OK) return st;
   if (reinterpret_cast<uintptr_t>(dweight) & 15)
     return fail(TDP_EINVAL, "%s: dweight must be 16-byte aligned", fn);
-  const ProductShape si = rows_shape(*seqs, in_features, out_features, dtype);
+  const ProductShape si = rows_shape(*seqs, in_features, out_features, dtype, kNarrowDx);
   const ProductShape sw = weight_shape(*seqs, num_weights, in_features, out_features, dtype);
   if (dx) st = check_workspace(fn, si, workspace);
   if (st == TDP_OK && dweight) st = check_workspace(fn, sw, workspace);
