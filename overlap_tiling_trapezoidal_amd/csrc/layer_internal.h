@@ -1,0 +1,93 @@
+// Launch shapes and workspace sizes of the layer operators (layer norm, grouped
+// products), shared by the host side (tokens.cpp) and the kernels.
+#pragma once
+
+#include "token_internal.h"
+
+namespace tdp {
+
+// Layer norm: lanes per row (the power of two that holds it in eight elements
+// each, up to a wave; wider rows take four passes of a wave, then the workgroup).
+inline int norm_rows_per_block(int32_t channels) {
+  const int chunks = channels / 8;
+  return chunks <= 8 ? 32 : chunks <= 16 ? 16 : chunks <= 32 ? 8 : chunks <= 256 ? 4 : 1;
+}
+inline int64_t norm_blocks(int32_t max_rows, int32_t channels) {
+  const int r = norm_rows_per_block(channels);
+  return ((int64_t)max_rows + r - 1) / r;
+}
+// Workgroups per set of weights in the backward launch; each leaves two partial
+// rows of sums, so more of them cost the join and fewer leave CUs idle (35840 rows
+// of 2048 bf16: 81 us with 512, 86 with 384, 84 with 256).
+constexpr int kLayerNormParts = 512;
+inline int64_t layer_norm_parts(const tdp_seqs& s, int32_t channels, int32_t sets) {
+  const int64_t blocks = norm_blocks(s.max_rows, channels) * ((s.num_seqs + sets - 1) / sets);
+  int64_t n = (kLayerNormParts + sets - 1) / sets;
+  return n < blocks ? n : blocks;
+}
+
+// Grouped products.  Blocks of `rows` rows that the sequences may have in all:
+// exactly where they are uniform, else at most one unfinished block each.
+inline int64_t row_blocks(const tdp_seqs& s, int rows) {
+  if (!s.row_range) return seq_blocks(s, rows);
+  return s.total_rows / rows + (s.num_seqs < s.total_rows ? s.num_seqs : s.total_rows);
+}
+struct ProductShape {
+  int rows;    // of the output tile: 256 (by 256 features), 128 (by 128) or 32 (by kNarrowY or kNarrowDx)
+  int splits;  // of the contraction
+};
+constexpr int kNarrowY = 64, kNarrowDx = 128;
+constexpr int kJoinRows = 8;
+constexpr int kProductMaxSplits = 16;
+// Splits of the contraction where the tiles are too few for the places that the
+// GPU has for them, none shorter than `least` of its `steps`.
+inline int product_splits(int64_t tiles, int64_t places, int64_t steps, int64_t least) {
+  int64_t n = places / tiles;
+  if (n > steps / least) n = steps / least;
+  if (n > kProductMaxSplits) n = kProductMaxSplits;
+  return n < 2 ? 1 : (int)n;
+}
+inline int64_t tiles_across(int64_t n, int64_t tile) { return (n + tile - 1) / tile; }
+// y (features = N, inner = K) and dx (the other way round).
+inline ProductShape rows_shape(const tdp_seqs& s, int32_t features, int32_t inner, int32_t dtype, int narrow) {
+  const int64_t mean = s.row_range ? s.total_rows / s.num_seqs : s.max_rows;
+  const int64_t big = row_blocks(s, 256) * tiles_across(features, 256);
+  ProductShape sh = {mean <= 48 ? 32 : 128, 1};
+  if (dtype == TDP_BF16 && mean >= 192 && big >= 192) sh.rows = 256;
+  const int64_t tiles = row_blocks(s, sh.rows) * tiles_across(features, sh.rows == 32 ? narrow : sh.rows);
+  const int64_t places = sh.rows == 256 ? 256 : sh.rows == 128 ? 512 : 131072 / narrow;
+  sh.splits = product_splits(tiles, places, inner * dtype_bytes(dtype) / 128, 4);
+  return sh;
+}
+// dW: its tile of W's rows is `rows` too, the contraction the rows of a weight's
+// sequences.  How many rows a weight has is known on the device only, so `splits`
+// says in how many parts the rows of all weights are cut where one has them all
+// (parts of less than kWeightSteps steps are not worth a slot).
+constexpr int kWeightSteps = 8;
+constexpr int kWeightMaxPlaces = 64;
+inline ProductShape weight_shape(const tdp_seqs& s, int32_t weights, int32_t in_features, int32_t out_features,
+                                 int32_t dtype) {
+  const int64_t big = weights * tiles_across(in_features, 256) * tiles_across(out_features, 256);
+  ProductShape sh = {dtype == TDP_BF16 && big >= 192 ? 256 : 128, 1};
+  if (weights > 64) return sh;
+  const int64_t tiles = tiles_across(in_features, sh.rows) * tiles_across(out_features, sh.rows);
+  int64_t n = (sh.rows == 256 ? 256 : 512) / tiles;
+  const int64_t steps = s.total_rows * dtype_bytes(dtype) / 128;
+  if (n > steps / kWeightSteps) n = steps / kWeightSteps;
+  if (n > kWeightMaxPlaces) n = kWeightMaxPlaces;
+  sh.splits = n < 2 ? 1 : (int)n;
+  return sh;
+}
+inline int64_t rows_workspace(const tdp_seqs& s, int32_t features, int32_t inner, int32_t dtype, int narrow) {
+  const ProductShape sh = rows_shape(s, features, inner, dtype, narrow);
+  return sh.splits == 1 ? 0 : align256(sh.splits * s.total_rows * features * 4);
+}
+inline int64_t weight_workspace(const tdp_seqs& s, int32_t weights, int32_t in_features, int32_t out_features,
+                                int32_t dtype) {
+  const ProductShape sh = weight_shape(s, weights, in_features, out_features, dtype);
+  return sh.splits == 1 ? 0 : align256((int64_t)2 * sh.splits * in_features * out_features * 4);
+}
+int check_product(const char* fn, const tdp_seqs* seqs, int32_t num_weights, int32_t in_features,
+                  int32_t out_features);
+
+}  // namespace tdp

@@ -15,6 +15,7 @@
 #include <math.h>
 #include <stdint.h>
 
+#include "layer_internal.h"
 #include "token_device.h"
 
 namespace tdp {

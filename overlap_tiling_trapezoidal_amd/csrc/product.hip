@@ -21,6 +21,7 @@
 #include <initializer_list>
 #include <type_traits>
 
+#include "layer_internal.h"
 #include "token_device.h"
 
 namespace tdp {

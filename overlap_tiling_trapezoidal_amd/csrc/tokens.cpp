@@ -8,7 +8,7 @@
 #include <initializer_list>
 #include <new>
 
-#include "token_internal.h"
+#include "layer_internal.h"
 
 namespace tdp {
 
