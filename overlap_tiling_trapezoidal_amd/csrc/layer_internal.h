@@ -39,25 +39,42 @@ struct ProductShape {
 constexpr int kNarrowY = 64, kNarrowDx = 128;
 constexpr int kJoinRows = 8;
 constexpr int kProductMaxSplits = 16;
-// Splits of the contraction where the tiles are too few for the places that the
-// GPU has for them, none shorter than `least` of its `steps`.
-inline int product_splits(int64_t tiles, int64_t places, int64_t steps, int64_t least) {
-  int64_t n = places / tiles;
-  if (n > steps / least) n = steps / least;
-  if (n > kProductMaxSplits) n = kProductMaxSplits;
-  return n < 2 ? 1 : (int)n;
-}
 inline int64_t tiles_across(int64_t n, int64_t tile) { return (n + tile - 1) / tile; }
-// y (features = N, inner = K) and dx (the other way round).
+// y (features = N, inner = K) and dx (the other way round): the tile and the
+// splits of the contraction that a model of the time expects to be fastest.  A
+// step of 128 bytes of the contraction takes a tile `wait` ns on its own and `busy`
+// of a CU that is full of them; splitting costs a launch and the parts' traffic.
+// Measured, bf16, with tiles of 32, 128 and 256 rows: 64 x 2048 -> 2048 12, 18 and
+// 39 us (128 in 8 splits 14); 8 x 256 x 1024 -> 1024 12, 15 and 24; 4 x 2240 x 512
+// -> 512 15, 12 and 17; 32 x 150 x 2048 -> 4096 267, 178 and 149; 200 x 4096 -> 4096
+// 34, 45 and 71 (128 in 8 splits 23).  fp32, 32 and 128 rows: 64 x 2048 -> 2048 49
+// and 140 (32 in splits 17); 4 x 2240 x 512 -> 512 53 and 68.
 inline ProductShape rows_shape(const tdp_seqs& s, int32_t features, int32_t inner, int32_t dtype, int narrow) {
-  const int64_t mean = s.row_range ? s.total_rows / s.num_seqs : s.max_rows;
-  const int64_t big = row_blocks(s, 256) * tiles_across(features, 256);
-  ProductShape sh = {mean <= 48 ? 32 : 128, 1};
-  if (dtype == TDP_BF16 && mean >= 192 && big >= 192) sh.rows = 256;
-  const int64_t tiles = row_blocks(s, sh.rows) * tiles_across(features, sh.rows == 32 ? narrow : sh.rows);
-  const int64_t places = sh.rows == 256 ? 256 : sh.rows == 128 ? 512 : 131072 / narrow;
-  sh.splits = product_splits(tiles, places, inner * dtype_bytes(dtype) / 128, 4);
-  return sh;
+  struct Tile {
+    int rows;
+    int64_t wait, busy;
+  };
+  const bool bf16 = dtype == TDP_BF16;
+  const Tile tiles[3] = {{32, bf16 ? 300 : 750, (bf16 ? 210 : 280) * narrow / 64},
+                         {128, bf16 ? 500 : 2100, bf16 ? 580 : 2000},
+                         {256, 1100, 1700}};
+  const int64_t all = inner * dtype_bytes(dtype), total = (all + 127) / 128;
+  ProductShape best = {32, 1};
+  int64_t least = INT64_MAX;
+  for (int i = 0; i < (bf16 ? 3 : 2); ++i) {
+    const int width = i == 0 ? narrow : tiles[i].rows;
+    const int64_t n = row_blocks(s, tiles[i].rows) * tiles_across(features, width);
+    for (int sp = 1; sp <= kProductMaxSplits && (sp == 1 || total >= 4 * sp); sp *= 2) {
+      const int64_t steps = (total + sp - 1) / sp, rounds = (n * sp + 255) / 256;
+      int64_t ns = rounds * tiles[i].busy > tiles[i].wait ? rounds * tiles[i].busy : tiles[i].wait;
+      ns = ns * steps + (sp == 1 ? 0 : 9000 + sp * s.total_rows * features / 500);  // 8 bytes at 4 TB/s
+      if (ns < least) {
+        least = ns;
+        best = {tiles[i].rows, sp};
+      }
+    }
+  }
+  return best;
 }
 // dW: its tile of W's rows is `rows` too, the contraction the rows of a weight's
 // sequences.  How many rows a weight has is known on the device only, so `splits`

@@ -191,10 +191,10 @@ def test_grouped_product_refusals(call):
                        (dict(n=0), tdp.TDP_EINVAL), (dict(n=5), tdp.TDP_EINVAL), (dict(dtype=2), tdp.TDP_EINVAL),
                        (dict(x=rows(row_stride=(1 << 21) + 4)), tdp.TDP_ESHAPE)]:
         assert call(**kw) == status, kw
-    # few rows of wide features: the contraction is split, so a workspace is needed
-    few = dict(s=seqs(max_rows=2, total_rows=8), K=4096, N=4096)
+    # few tiles of a long contraction: it is split, so a workspace is needed
+    long = dict(s=seqs(num_seqs=1, max_rows=200, total_rows=200), K=4096, N=4096)
     for ws in (None, P + 8):
-        assert call(**few, ws=ws) == tdp.TDP_EINVAL and "workspace" in tdp.tdp_last_error()
+        assert call(**long, ws=ws) == tdp.TDP_EINVAL and "workspace" in tdp.tdp_last_error()
     # 2^24 rows of 65536 features: more tiles than a launch holds
     many = seqs(num_seqs=100, max_rows=1 << 24, total_rows=100 << 24)
     assert call(s=many, K=65536, N=65536) == tdp.TDP_ESHAPE and "work-items" in tdp.tdp_last_error()
@@ -208,10 +208,11 @@ def test_grouped_product_workspace():
     bwd = lambda s, n, K, N, dt=tdp.TDP_BF16: lib.tdp_grouped_product_backward_workspace(  # noqa: E731
         ctypes.byref(s), n, K, N, dt)
     few, many = seqs(max_rows=2, total_rows=8), seqs(max_rows=20000, total_rows=80000)
-    assert fwd(few, 1, 4096, 4096) % (8 * 4096 * 4) == 0 and fwd(few, 1, 4096, 4096) > 0
+    long = seqs(num_seqs=1, max_rows=200, total_rows=200)    # few tiles of a long contraction: split
+    assert fwd(long, 1, 4096, 4096) % (200 * 4096 * 4) == 0 and fwd(long, 1, 4096, 4096) > 0
     assert fwd(many, 1, 4096, 4096) == 0 and bwd(many, 1, 4096, 4096) == 0
     assert bwd(many, 1, 128, 128) >= 2 * 128 * 128 * 4     # one tile of weights, its rows split
-    assert bwd(few, 1, 4096, 4096) >= fwd(few, 1, 4096, 4096)
+    assert bwd(long, 1, 4096, 4096) >= fwd(long, 1, 4096, 4096)
     for args in ((0, 128, 128), (5, 128, 128), (1, 0, 128), (1, 128, 12), (1, 128, tdp.TDP_MAX_FEATURES + 8)):
         assert fwd(few, *args) == 0 and bwd(few, *args) == 0
     assert fwd(few, 1, 4096, 4096, 7) == 0
