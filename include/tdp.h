@@ -747,7 +747,8 @@ typedef struct {
  * sequence s takes row s mod num_weights, so one row serves all, and B rows
  * give each batch element of a plan's slots its own (modulation by the
  * timestep).  channels is a multiple of 8, at most TDP_MAX_CHANNELS;
- * 1 <= num_weights <= num_seqs.  y may be x (same strides).  Sums are fp32: the
+ * 1 <= num_weights <= num_seqs.  y may be x (same strides); otherwise they must
+ * not overlap.  Sums are fp32: the
  * squares of a row's differences from its mean have to stay in its range.  With
  * eps 0 a row of equal values has no norm, as in the formula.  One launch. */
 #define TDP_MAX_CHANNELS 8192

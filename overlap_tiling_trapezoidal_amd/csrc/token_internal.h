@@ -182,10 +182,13 @@ inline DkvSplit dkv_split(const tdp_window* w, const tdp_seqs& q, const tdp_seqs
   }
   DkvSplit sp = {dkv_splits(k, w && w->sinks ? q.max_rows : seen, q_heads, k_heads), all, k.max_rows};
   if (sp.n == 1 && w && w->sinks) {
-    const int64_t part = seen > kDkvSplitRows ? seen : kDkvSplitRows, n = (q.max_rows + part - 1) / part;
-    sp.n = (int)(n < kAttnMaxSplits ? n : kAttnMaxSplits);
-    const int64_t lead = ((int64_t)w->sinks + kAttnBlockQ - 1) / kAttnBlockQ;
-    if (sp.n > 1 && lead < all) {
+    const int64_t lead = ((int64_t)w->sinks + kAttnBlockQ - 1) / kAttnBlockQ, heavy = lead * k.num_seqs * k_heads;
+    const int64_t part = seen > kDkvSplitRows ? seen : kDkvSplitRows;
+    int64_t n = (q.max_rows + part - 1) / part;
+    if (n > 2 * kAttnSplitBlocks / heavy) n = 2 * kAttnSplitBlocks / heavy;  // many blocks fill the GPU unsplit
+    if (n > kAttnMaxSplits) n = kAttnMaxSplits;
+    if (n > 1 && lead < all) {
+      sp.n = (int)n;
       sp.blocks = lead;
       sp.rows = lead * kAttnBlockQ;
     }
