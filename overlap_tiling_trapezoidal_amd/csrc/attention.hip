@@ -388,14 +388,15 @@ __device__ inline void mask_scores(f32x16& st, const float* bl, float c, int j0,
 
 // What the rows of a query block see of the keys: rows [row0, row1] of a sequence,
 // and per lane its own row.  Keys [0, first) and [lo, hi) cover all that any of the
-// rows sees; `at(t)` is the t-th of the `n` key blocks that hold them.
+// rows sees, in `n` blocks of keys, the t-th from key0(t) on: first rows in blocks
+// from key 0, then the window from its own first key.
 template <int KB>
 struct Seen {
   int lo, hi, first;        // of all rows
   int lo_max, hi_min;       // keys [lo_max, hi_min) and below first_min are seen by every row
   int first_min;
   int my_lo, my_hi, sinks;  // the lane's row
-  int lead, skip, n;        // blocks of first rows; blocks passed over behind them
+  int lead, skip, n;        // blocks of first rows; keys passed over behind them
   __device__ inline void init(const WindowDev& w, int qlen, int klen, int row0, int row1, int row) {
     const int off = klen - qlen;
     sinks = w.sinks;
@@ -410,11 +411,11 @@ struct Seen {
     my_lo = c.lo;
     my_hi = c.hi;
     lead = ((first < lo ? first : lo) + KB - 1) / KB;
-    const int w0 = lo / KB > lead ? lo / KB : lead, w1 = (hi + KB - 1) / KB;
-    skip = w0 - lead;
-    n = lead + (w1 > w0 ? w1 - w0 : 0);
+    skip = lo > lead * KB ? lo - lead * KB : 0;
+    const int left = hi - lead * KB - skip;
+    n = lead + (left > 0 ? (left + KB - 1) / KB : 0);
   }
-  __device__ inline int at(int t) const { return t < lead ? t : t + skip; }
+  __device__ inline int key0(int t) const { return t < lead ? t * KB : t * KB + skip; }
   // some row does not see some key of the 64 from j0 on
   __device__ inline bool edge(int j0, int keys) const {
     return !((j0 >= lo_max && j0 + keys <= hi_min) || j0 + keys <= first_min);
@@ -535,7 +536,7 @@ __global__ __launch_bounds__(kTok, T != TDP_BF16 ? 1 : DP == 64 ? 3 : 2) void at
     }
   };
   // block b of the walk begins with this key
-  auto key0 = [&](int b) __attribute__((always_inline)) { return (WIN ? seen.at(b) : b) * kAttnBlockK; };
+  auto key0 = [&](int b) __attribute__((always_inline)) { return WIN ? seen.key0(b) : b * kAttnBlockK; };
   // take block b's scores over: mask them, and move the maximum if they exceed it
   auto take = [&](int b, f32x16* sn) __attribute__((always_inline)) {
     if constexpr (WIN) {
@@ -788,7 +789,7 @@ __global__ __launch_bounds__(kTok, T == TDP_BF16 && !(BIAS && DP == 128) ? 2 : 1
   }
   const int klen = WIN ? seen.hi : kr.len;
   const int nb = m0 >= mlen ? 0 : WIN ? seen.n : (kr.len + kDqKeys - 1) / kDqKeys;
-  auto key0 = [&](int b) __attribute__((always_inline)) { return (WIN ? seen.at(b) : b) * kDqKeys; };
+  auto key0 = [&](int b) __attribute__((always_inline)) { return WIN ? seen.key0(b) : b * kDqKeys; };
 
   Direct<T, DP, kDqKeys> kd, vd;
   kd.init((uint32_t)krow, d_bytes);

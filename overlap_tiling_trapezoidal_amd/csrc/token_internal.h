@@ -184,7 +184,7 @@ inline DkvSplit dkv_split(const tdp_window* w, const tdp_seqs& q, const tdp_seqs
   if (sp.n == 1 && w && w->sinks) {
     const int64_t lead = ((int64_t)w->sinks + kAttnBlockQ - 1) / kAttnBlockQ, heavy = lead * k.num_seqs * k_heads;
     const int64_t part = seen > kDkvSplitRows ? seen : kDkvSplitRows;
-    int64_t n = (q.max_rows + part - 1) / part;
+    int64_t n = q.max_rows / part;
     if (n > 2 * kAttnSplitBlocks / heavy) n = 2 * kAttnSplitBlocks / heavy;  // many blocks fill the GPU unsplit
     if (n > kAttnMaxSplits) n = kAttnMaxSplits;
     if (n > 1 && lead < all) {
