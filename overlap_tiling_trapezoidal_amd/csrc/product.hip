@@ -34,6 +34,18 @@ typedef float f32x16 __attribute__((ext_vector_type(16)));
 #define TDP_LDS __attribute__((address_space(3)))
 
 enum Kind { kForward, kInput, kWeight };  // y, dx, dW
+enum Pass { kAll, kRounds, kRest };
+
+// Tiles of 256 by 256 run one to a CU, and a last round of few of them takes as
+// long as a full one.  Up to kRestTiles tiles beyond whole rounds of 256 are left to
+// a second launch, in quarters of 128 by 128 that all CUs share (8 960 rows of 2048
+// -> 6144, 864 tiles: 19x us against 207; 24576 rows for 8 weights of 2048 x 2048,
+// about 800 tiles: 19x us against 237).
+constexpr uint32_t kRestTiles = 128;
+__host__ __device__ inline uint32_t rest_tiles(uint32_t tiles) {
+  const uint32_t rest = tiles % 256;
+  return rest <= kRestTiles ? rest : 0;
+}
 
 template <int T>
 struct Mat;
@@ -66,6 +78,7 @@ struct ProductArgs {
   int32_t splits;     // y, dx: of the contraction; dW: weight_places
   uint32_t np;        // tiles of output features
   uint32_t nq;        // dW: tiles of W's rows
+  int32_t pass;       // y, dx: kAll, kRounds or kRest
   FastDiv by_np;
 };
 
@@ -258,14 +271,17 @@ struct RowBlocks {
 // contiguous range of the tiles.  Runs of eight tiles along q share one of p, and
 // the tiles that an XCD's 32 CUs hold at a time are eight by four: they read
 // twelve panels of operands through its L2 instead of 64.
-__device__ inline bool tile_of(uint32_t nq, uint32_t np, uint32_t b, uint32_t& q, uint32_t& p) {
-  const uint32_t tiles = nq * np, per = (tiles + 7) / 8, slot = b >> 3, item = (b & 7) * per + slot;
-  if (slot >= per || item >= tiles) return false;
+// The workgroup's item of `count`, or false.
+__device__ inline bool xcd_item(uint32_t count, uint32_t b, uint32_t& item) {
+  const uint32_t per = (count + 7) / 8, slot = b >> 3;
+  item = (b & 7) * per + slot;
+  return slot < per && item < count;
+}
+__device__ inline void tile_at(uint32_t nq, uint32_t np, uint32_t item, uint32_t& q, uint32_t& p) {
   const uint32_t group = item / (8 * np), first = group * 8, rest = item - first * np;
   const uint32_t n = nq - first < 8 ? nq - first : 8;
   p = rest / n;
   q = first + (rest - p * n);
-  return true;
 }
 
 __device__ inline f32x16 zero16() {
@@ -402,18 +418,33 @@ __global__ __launch_bounds__(64 * WP * WQ) void product_kernel(const ProductArgs
   SeqRows sr = {};
   const int split = KIND == kWeight ? 0 : blockIdx.y;
   int w_part = 0, w_parts = 1, w_steps = 0, w_slot = -1;  // dW
+  int f0, r0;
   if constexpr (KIND != kWeight) {
-    const RowBlocks rb = {A.seqs, BQ, lane};
-    if (!tile_of((uint32_t)rb.total(), A.np, blockIdx.x, tq, tp)) return;
+    const bool quarters = BQ == 128 && A.pass == kRest;  // of the tiles of 256 that are left
+    const RowBlocks rb = {A.seqs, quarters ? 256 : BQ, lane};
+    const uint32_t nq = (uint32_t)rb.total(), all = nq * A.np, rest = A.pass == kAll ? 0 : rest_tiles(all);
+    uint32_t item;
+    if (!xcd_item(quarters ? 4 * rest : all - rest, blockIdx.x, item)) return;
+    tile_at(nq, A.np, quarters ? all - rest + item / 4 : item, tq, tp);
     blk = (int)tq;
     s = rb.find(blk);
     sr = seq_rows(A.seqs, s);
     e = s % A.E;
+    f0 = (int)tp * (quarters ? 256 : BP);
+    r0 = blk * (quarters ? 256 : BQ);
+    if (quarters) {
+      r0 += (item & 1) * 128;
+      f0 += (item >> 1 & 1) * 128;
+      if (r0 >= sr.cap || f0 >= (KIND == kForward ? A.N : A.K)) return;
+    }
   } else {
     const uint32_t grid = (A.nq * A.np + 7) / 8 * 8;
     const int part = blockIdx.x / grid;
-    if (!tile_of(A.nq, A.np, blockIdx.x - part * grid, tq, tp)) return;
-    blk = (int)tq;
+    uint32_t item;
+    if (!xcd_item(A.nq * A.np, blockIdx.x - part * grid, item)) return;
+    tile_at(A.nq, A.np, item, tq, tp);
+    f0 = (int)tp * BP;
+    r0 = (int)tq * BQ;
     if (A.E <= 64) {
       WeightParts wp;
       wp.count(A, kStep, lane, reinterpret_cast<int*>(lds_p));
@@ -433,7 +464,6 @@ __global__ __launch_bounds__(64 * WP * WQ) void product_kernel(const ProductArgs
       }
     }
   }
-  const int f0 = (int)tp * BP, r0 = blk * BQ;
   const char* w = A.w + (int64_t)e * A.N * A.K * eb;
   const int features = KIND == kForward ? A.N : A.K;   // of the output
   const int inner = KIND == kForward ? A.K : A.N;      // y and dx: the contraction's length
@@ -772,8 +802,18 @@ int launch_rows(const char* fn, ProductArgs A, const tdp_seqs& seqs, const Produ
   int rc = check_items(fn, tiles * sh.splits, 64 * WP * WQ);
   if (rc == TDP_OK && sh.splits > 1) rc = check_items(fn, join_x * join_y, kJoin);
   if (rc != TDP_OK || !enqueue) return rc;
+  if constexpr (BQ == 256) {
+    // where the sequences are uniform, the tiles are known here
+    if (sh.splits == 1 && (seqs.row_range || rest_tiles((uint32_t)(blocks * A.np)))) A.pass = kRounds;
+  }
   hipLaunchKernelGGL((product_kernel<T, KIND, BP, BQ, WP, WQ, STAGES>), dim3((unsigned)tiles, (unsigned)sh.splits),
                      dim3(64 * WP * WQ), 0, st, A);
+  if constexpr (BQ == 256) {
+    if (A.pass == kRounds) {
+      A.pass = kRest;
+      hipLaunchKernelGGL((product_kernel<T, KIND, 128, 128, 2, 2, 2>), dim3(4 * kRestTiles), dim3(256), 0, st, A);
+    }
+  }
   if (sh.splits > 1)
     hipLaunchKernelGGL((product_join_kernel<T>), dim3((unsigned)join_x, (unsigned)join_y), dim3(kJoin), 0, st, A,
                        KIND == kForward ? A.y : A.dx, features, kJoinRows);
