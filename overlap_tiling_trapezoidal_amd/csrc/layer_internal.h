@@ -35,6 +35,7 @@ inline int64_t row_blocks(const tdp_seqs& s, int rows) {
 struct ProductShape {
   int rows;    // of the output tile: 256 (by 256 features), 128 (by 128) or 32 (by kNarrowY or kNarrowDx)
   int splits;  // of the contraction
+  bool deep;   // 128 rows: four stages on their way instead of two, one workgroup per CU
 };
 constexpr int kNarrowY = 64, kNarrowDx = 128;
 constexpr int kJoinRows = 8;
@@ -44,11 +45,13 @@ inline int64_t tiles_across(int64_t n, int64_t tile) { return (n + tile - 1) / t
 // splits of the contraction that a model of the time expects to be fastest.  A
 // step of 128 bytes of the contraction takes a tile `wait` ns on its own and `busy`
 // of a CU that is full of them; splitting costs a launch and the parts' traffic.
-// Measured, bf16, with tiles of 32, 128 and 256 rows: 64 x 2048 -> 2048 12, 18 and
-// 39 us (128 in 8 splits 14); 8 x 256 x 1024 -> 1024 12, 15 and 24; 4 x 2240 x 512
-// -> 512 15, 12 and 17; 32 x 150 x 2048 -> 4096 267, 178 and 149; 200 x 4096 -> 4096
-// 34, 45 and 71 (128 in 8 splits 23).  fp32, 32 and 128 rows: 64 x 2048 -> 2048 49
-// and 140 (32 in splits 17); 4 x 2240 x 512 -> 512 53 and 68.
+// Where all tiles of 128 have a CU to themselves, they keep four stages on their
+// way instead of two (8 x 100 x 2048 -> 2048: 19 us against 27).  Measured, bf16, with
+// tiles of 32, 128 and 256 rows: 64 x 2048 -> 2048 12, 18 and 39 us (128 in 8 splits
+// 14); 8 x 256 x 1024 -> 1024 12, 12 and 24; 4 x 2240 x 512 -> 512 14, 13 and 17; 32 x
+// 150 x 2048 -> 4096 270, 180 and 149; 200 x 4096 -> 4096 35, 30 and 71 (128 in 4 splits
+// 20).  fp32, 32 and 128 rows: 64 x 2048 -> 2048 48 and 132 (32 in splits 18); 4 x 2240
+// x 512 -> 512 54 and 69.
 inline ProductShape rows_shape(const tdp_seqs& s, int32_t features, int32_t inner, int32_t dtype, int narrow) {
   struct Tile {
     int rows;
@@ -56,10 +59,10 @@ inline ProductShape rows_shape(const tdp_seqs& s, int32_t features, int32_t inne
   };
   const bool bf16 = dtype == TDP_BF16;
   const Tile tiles[3] = {{32, bf16 ? 300 : 750, (bf16 ? 210 : 280) * narrow / 64},
-                         {128, bf16 ? 500 : 2100, bf16 ? 580 : 2000},
+                         {128, bf16 ? 430 : 1900, bf16 ? 580 : 2000},
                          {256, 1100, 1700}};
   const int64_t all = inner * dtype_bytes(dtype), total = (all + 127) / 128;
-  ProductShape best = {32, 1};
+  ProductShape best = {32, 1, false};
   int64_t least = INT64_MAX;
   for (int i = 0; i < (bf16 ? 3 : 2); ++i) {
     const int width = i == 0 ? narrow : tiles[i].rows;
@@ -70,7 +73,7 @@ inline ProductShape rows_shape(const tdp_seqs& s, int32_t features, int32_t inne
       ns = ns * steps + (sp == 1 ? 0 : 9000 + sp * s.total_rows * features / 500);  // 8 bytes at 4 TB/s
       if (ns < least) {
         least = ns;
-        best = {tiles[i].rows, sp};
+        best = {tiles[i].rows, sp, i == 1 && n * sp <= 256};
       }
     }
   }
@@ -85,7 +88,7 @@ constexpr int kWeightMaxPlaces = 64;
 inline ProductShape weight_shape(const tdp_seqs& s, int32_t weights, int32_t in_features, int32_t out_features,
                                  int32_t dtype) {
   const int64_t big = weights * tiles_across(in_features, 256) * tiles_across(out_features, 256);
-  ProductShape sh = {dtype == TDP_BF16 && big >= 192 ? 256 : 128, 1};
+  ProductShape sh = {dtype == TDP_BF16 && big >= 192 ? 256 : 128, 1, false};
   if (weights > 64) return sh;
   const int64_t tiles = tiles_across(in_features, sh.rows) * tiles_across(out_features, sh.rows);
   int64_t n = (sh.rows == 256 ? 256 : 512) / tiles;

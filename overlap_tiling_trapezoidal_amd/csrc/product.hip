@@ -38,10 +38,10 @@ enum Pass { kAll, kRounds, kRest };
 
 // Tiles of 256 by 256 run one to a CU, and a last round of few of them takes as
 // long as a full one.  Up to kRestTiles tiles beyond whole rounds of 256 are left to
-// a second launch, in quarters of 128 by 128 that all CUs share (8 960 rows of 2048
-// -> 6144, 864 tiles: 19x us against 207; 24576 rows for 8 weights of 2048 x 2048,
-// about 800 tiles: 19x us against 237).
-constexpr uint32_t kRestTiles = 128;
+// a second launch, in quarters of 128 by 128 that have a CU each (gradients of
+// 24576 rows for 8 weights of 2048 x 2048, about 800 tiles of dx: 415 us against
+// 427).  With twice as many it gains nothing.
+constexpr uint32_t kRestTiles = 64;
 __host__ __device__ inline uint32_t rest_tiles(uint32_t tiles) {
   const uint32_t rest = tiles % 256;
   return rest <= kRestTiles ? rest : 0;
@@ -680,8 +680,10 @@ __global__ __launch_bounds__(64 * WP * WQ) void product_kernel(const ProductArgs
         if (++t >= t1) break;
         stage(1);
         if (++t >= t1) break;
-        if constexpr (STAGES == 3) {
+        if constexpr (STAGES == 4) {
           stage(2);
+          if (++t >= t1) break;
+          stage(3);
           if (++t >= t1) break;
         }
       }
@@ -811,7 +813,7 @@ int launch_rows(const char* fn, ProductArgs A, const tdp_seqs& seqs, const Produ
   if constexpr (BQ == 256) {
     if (A.pass == kRounds) {
       A.pass = kRest;
-      hipLaunchKernelGGL((product_kernel<T, KIND, 128, 128, 2, 2, 2>), dim3(4 * kRestTiles), dim3(256), 0, st, A);
+      hipLaunchKernelGGL((product_kernel<T, KIND, 128, 128, 2, 2, 4>), dim3(4 * kRestTiles), dim3(256), 0, st, A);
     }
   }
   if (sh.splits > 1)
@@ -846,9 +848,11 @@ int run_rows(const char* fn, const ProductArgs& A, const tdp_seqs& seqs, const P
   constexpr int NB = KIND == kForward ? kNarrowY : kNarrowDx;
   if (dtype == TDP_BF16) {
     if (sh.rows == 256) return launch_rows<TDP_BF16, KIND, 256, 256, 4, 2, 2>(fn, A, seqs, sh, enqueue, st);
+    if (sh.rows == 128 && sh.deep) return launch_rows<TDP_BF16, KIND, 128, 128, 2, 2, 4>(fn, A, seqs, sh, enqueue, st);
     if (sh.rows == 128) return launch_rows<TDP_BF16, KIND, 128, 128, 2, 2, 2>(fn, A, seqs, sh, enqueue, st);
     return launch_rows<TDP_BF16, KIND, NB, 32, NB / 32, 1, 2>(fn, A, seqs, sh, enqueue, st);
   }
+  if (sh.rows == 128 && sh.deep) return launch_rows<TDP_F32, KIND, 128, 128, 2, 2, 4>(fn, A, seqs, sh, enqueue, st);
   if (sh.rows == 128) return launch_rows<TDP_F32, KIND, 128, 128, 2, 2, 2>(fn, A, seqs, sh, enqueue, st);
   return launch_rows<TDP_F32, KIND, NB, 32, NB / 32, 1, 2>(fn, A, seqs, sh, enqueue, st);
 }
