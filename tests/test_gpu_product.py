@@ -36,7 +36,18 @@ BIG = [
     (72, 4104, (1500, 900, 700), (1500, 899, 1), True, 3, "wide"),
     (328, 4096, (3400,), (3333,), False, 1, "rows"),
 ]
-BIG_IDS = [f"{c[0]}to{c[1]}" for c in BIG]
+BIG += [   # a few tiles beyond a whole round of 256
+    (72, 4096, (4300,), (4290,), False, 1, "rows"),
+    (72, 4104, (2100, 1100, 1000), (2100, 1090, 1000), True, 3, "wide"),
+]
+BIG_IDS = [f"{c[0]}to{c[1]}-{len(c[2])}" for c in BIG]
+# in, out features, sequences, rows, weights: every tile and form of the launch, split and whole, of y or of dx
+TILES = [
+    (136, 72, 12, 2500, 1), (136, 72, 40, 300, 40), (72, 2056, 12, 520, 3), (72, 72, 12, 5000, 1), (72, 72, 12, 2500, 2),
+    (2056, 72, 3, 2500, 1), (8200, 72, 5, 33, 5), (136, 2056, 12, 33, 1), (72, 1032, 40, 33, 4), (72, 72, 40, 200, 1),
+    (4104, 72, 12, 33, 2), (8200, 72, 40, 33, 1), (72, 1032, 40, 130, 1), (8200, 264, 12, 130, 1), (72, 8200, 5, 130, 1),
+    (72, 72, 70, 40, 70),
+]
 
 
 def setup(case, dtype, cuda, seed):
@@ -117,6 +128,15 @@ def test_grouped_product(case, dtype, cuda):
 @pytest.mark.parametrize("case", CASES, ids=IDS)
 def test_grouped_product_backward(case, dtype, cuda):
     check_backward(case, dtype, cuda, 42)
+
+
+@pytest.mark.parametrize("dtype", list(DT))
+@pytest.mark.parametrize("case", TILES, ids=["x".join(map(str, c)) for c in TILES])
+def test_grouped_product_tiles(case, dtype, cuda):
+    K, N, S, n, E = case
+    full = (K, N, (n,) * S, tuple(n - 3 * (i % 5) for i in range(S)), False, E, "rows")
+    check_forward(full, dtype, cuda, 47)
+    check_backward(full, dtype, cuda, 48)
 
 
 @pytest.mark.parametrize("case", BIG, ids=BIG_IDS)
