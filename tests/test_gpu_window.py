@@ -36,6 +36,9 @@ CASES = [
     ((64,), (64,), (400,), (390,), 2, 1, 64, (32, 3, 0, 32), True, "heads"),              # newest frames over a cache
     ((90,), (90,), (77,), (77,), 2, 2, 32, (8, 2, 1, 200), False, "rows"),                # sinks past the end
     ((2,), (2,), (9,), (9,), 1, 1, 64, (1 << 24, ALL, ALL, ALL), False, "rows"),          # the largest values
+    ((600,) * 28, tuple(600 - 20 * i for i in range(28)), None, None, 8, 8, 32, (1, ALL, 0, 0), False, "rows"),  # chunks
+    ((1300,) * 2, (1300, 1200), None, None, 16, 16, 32, (1, 100, 0, 130), False, "rows"),  # first rows' blocks split
+    ((1300,) * 2, (1300, 1200), None, None, 16, 16, 32, (50, 3, 1, 50), False, "packed"),
 ]
 IDS = [f"{'x'.join(map(str, c[0]))}-h{c[4]}.{c[5]}-d{c[6]}-{'.'.join(map(str, c[7]))}" for c in CASES]
 
