@@ -23,7 +23,8 @@
  * imbalance), a streaming blend that takes one tile at a time, the blend
  * of decoded pixel tiles for a tiled VAE decode, and what a denoiser's
  * layer computes on a plan's slots (three-axis rotation, per-head norms,
- * attention, layer norm, and their gradients).
+ * attention, also within a window of frames, layer norm, projections and
+ * experts' products, and their gradients).
  *
  * Conventions
  *   - Every function returns TDP_OK (0) or a negative status; the message of
