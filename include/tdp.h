@@ -36,7 +36,7 @@
  *     arguments are validated before anything is enqueued, so an error
  *     leaves every output untouched.
  *   - Results are deterministic: every output element has one writer and
- *     sums run in a fixed order; there are no atomics.
+ *     sums run in a fixed order; no floating-point value is added by atomics.
  *
  * Token and position layout (caller's tensors)
  *   latent    (B, N + Nc, C) row-major, dtype in_dtype; N = F*H*W generated
