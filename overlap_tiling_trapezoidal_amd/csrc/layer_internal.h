@@ -26,9 +26,20 @@ inline int64_t layer_norm_parts(const tdp_seqs& s, int32_t channels, int32_t set
   return n < blocks ? n : blocks;
 }
 
-// Grouped products.  Blocks of `rows` rows that the sequences may have in all:
-// exactly where they are uniform, else at most one unfinished block each.
-inline int64_t row_blocks(const tdp_seqs& s, int rows) {
+// Grouped products.  With one weight for all sequences the rows need not be told
+// apart before they are stored, so tiles may be of the tensors' rows, across the
+// ends of sequences.  Taken where these are short and their last tiles are a large
+// part of all (bf16, y and dx: 24 x 46 rows of 1632 -> 5696 34 and 41 us against 76
+// and 74 with tiles of their own, 48 x 100 of 2048 -> 2048 50 and 49 against 58 and
+// 60, but 48 x 200 95 and 99 against 92 and 88); looking the rows up costs long
+// sequences 3 %.
+inline bool flat_rows(const tdp_seqs& s, int32_t weights) {
+  return weights == 1 && s.num_seqs > 1 && s.total_rows < (int64_t)s.num_seqs * 192;
+}
+// Blocks of `rows` rows of the tensors if flat, else of the sequences: exactly
+// where these are uniform, else at most one unfinished block each.
+inline int64_t row_blocks(const tdp_seqs& s, int rows, bool flat = false) {
+  if (flat) return (s.total_rows + rows - 1) / rows;
   if (!s.row_range) return seq_blocks(s, rows);
   return s.total_rows / rows + (s.num_seqs < s.total_rows ? s.num_seqs : s.total_rows);
 }
@@ -52,7 +63,8 @@ inline int64_t tiles_across(int64_t n, int64_t tile) { return (n + tile - 1) / t
 // 150 x 2048 -> 4096 270, 180 and 149; 200 x 4096 -> 4096 35, 30 and 71 (128 in 4 splits
 // 20).  fp32, 32 and 128 rows: 64 x 2048 -> 2048 48 and 132 (32 in splits 18); 4 x 2240
 // x 512 -> 512 54 and 69.
-inline ProductShape rows_shape(const tdp_seqs& s, int32_t features, int32_t inner, int32_t dtype, int narrow) {
+inline ProductShape rows_shape(const tdp_seqs& s, int32_t features, int32_t inner, int32_t dtype, int narrow,
+                               bool flat) {
   struct Tile {
     int rows;
     int64_t wait, busy;
@@ -66,7 +78,7 @@ inline ProductShape rows_shape(const tdp_seqs& s, int32_t features, int32_t inne
   int64_t least = INT64_MAX;
   for (int i = 0; i < (bf16 ? 3 : 2); ++i) {
     const int width = i == 0 ? narrow : tiles[i].rows;
-    const int64_t n = row_blocks(s, tiles[i].rows) * tiles_across(features, width);
+    const int64_t n = row_blocks(s, tiles[i].rows, flat) * tiles_across(features, width);
     for (int sp = 1; sp <= kProductMaxSplits && (sp == 1 || total >= 4 * sp); sp *= 2) {
       const int64_t steps = (total + sp - 1) / sp, rounds = (n * sp + 255) / 256;
       int64_t ns = rounds * tiles[i].busy > tiles[i].wait ? rounds * tiles[i].busy : tiles[i].wait;
@@ -98,8 +110,9 @@ inline ProductShape weight_shape(const tdp_seqs& s, int32_t weights, int32_t in_
   sh.splits = n < 2 ? 1 : (int)n;
   return sh;
 }
-inline int64_t rows_workspace(const tdp_seqs& s, int32_t features, int32_t inner, int32_t dtype, int narrow) {
-  const ProductShape sh = rows_shape(s, features, inner, dtype, narrow);
+inline int64_t rows_workspace(const tdp_seqs& s, int32_t features, int32_t inner, int32_t dtype, int narrow,
+                              bool flat) {
+  const ProductShape sh = rows_shape(s, features, inner, dtype, narrow, flat);
   return sh.splits == 1 ? 0 : align256(sh.splits * s.total_rows * features * 4);
 }
 inline int64_t weight_workspace(const tdp_seqs& s, int32_t weights, int32_t in_features, int32_t out_features,

@@ -79,6 +79,7 @@ struct ProductArgs {
   uint32_t np;        // tiles of output features
   uint32_t nq;        // dW: tiles of W's rows
   int32_t pass;       // y, dx: kAll, kRounds or kRest
+  bool flat;          // y, dx: one weight for all, blocks of the tensors' rows
   FastDiv by_np;
 };
 
@@ -232,15 +233,18 @@ __device__ inline int wave_prefix(int v, int lane) {  // inclusive
 
 __device__ inline int last_lane(int v) { return __builtin_amdgcn_readlane(v, 63); }
 
-// Blocks of `rows` rows of every sequence in order, found by whole waves.
+// Blocks of `rows` rows of every sequence in order, found by whole waves; of
+// the tensors' rows, whatever sequences they are, if flat.
 struct RowBlocks {
   const SeqsDev& q;
   int rows, lane;
+  bool flat;
   __device__ inline int count(int s) const {
     if (s >= q.S) return 0;
     return (seq_rows(q, s).cap + rows - 1) / rows;
   }
   __device__ inline int total() const {
+    if (flat) return (int)((q.total + rows - 1) / rows);
     if (!q.range) return q.S * ((q.max_rows + rows - 1) / rows);
     int n = 0;
     for (int s = 0; s < q.S; s += 64) n += last_lane(wave_prefix(count(s + lane), lane));
@@ -248,6 +252,7 @@ struct RowBlocks {
   }
   // the sequence of block t, which becomes the block's number in it
   __device__ inline int find(int& t) const {
+    if (flat) return 0;
     if (!q.range) {
       const int per = (q.max_rows + rows - 1) / rows, s = t / per;
       t -= s * per;
@@ -267,11 +272,53 @@ struct RowBlocks {
   }
 };
 
+// Which rows of a block of the tensors' rows some sequence owns and uses: the
+// sequences that reach into it are listed in LDS (as many as the block has rows at
+// most, since written ranges do not overlap), and each lane looks its rows up.
+template <int BQ, int THREADS>
+struct BlockRows {
+  static constexpr int kBytes = (1 + 3 * BQ) * 4;
+  int n;
+  const int* list;
+  __device__ inline void find(const SeqsDev& q, int r0, int* lds) {
+    if (threadIdx.x == 0) lds[0] = 0;
+    __syncthreads();
+    for (int s = threadIdx.x; s < q.S; s += THREADS) {
+      const SeqRows r = seq_rows(q, s);
+      const int a = (int)(r.row0 - r0);
+      if (r.cap > 0 && a < BQ && a + r.cap > 0) {
+        const int i = atomicAdd(lds, 1);  // any order: the entries exclude each other
+        if (i < BQ) {
+          lds[1 + 3 * i] = a;
+          lds[2 + 3 * i] = a + r.len;
+          lds[3 + 3 * i] = a + r.cap;
+        }
+      }
+    }
+    __syncthreads();
+    n = lds[0] < BQ ? lds[0] : BQ;
+    list = lds + 1;
+  }
+  __device__ inline bool any_used() const {
+    bool any = false;
+    for (int i = 0; i < n; ++i) any |= list[3 * i + 1] > 0 && list[3 * i + 1] > list[3 * i];
+    return any;
+  }
+  __device__ inline void look_up(int row, bool& used, bool& owned) const {
+    used = owned = false;
+    for (int i = 0; i < n; ++i) {
+      const bool in = row >= list[3 * i];
+      used |= in && row < list[3 * i + 1];
+      owned |= in && row < list[3 * i + 2];
+    }
+  }
+};
+
 // Workgroups are dealt round-robin to the eight XCDs, each of which takes a
 // contiguous range of the tiles.  Runs of eight tiles along q share one of p, and
 // the tiles that an XCD's 32 CUs hold at a time are eight by four: they read
 // twelve panels of operands through its L2 instead of 64.
-// The workgroup's item of `count`, or false.
+// xcd_item: the workgroup's item of `count`, or false.
 __device__ inline bool xcd_item(uint32_t count, uint32_t b, uint32_t& item) {
   const uint32_t per = (count + 7) / 8, slot = b >> 3;
   item = (b & 7) * per + slot;
@@ -292,11 +339,10 @@ __device__ inline f32x16 zero16() {
 }
 
 // The wave's 32 rows of TP tiles of features, through 4 KB of LDS of its own so
-// that whole runs of features leave at once.  OUT: type written.  Rows at and
-// past `len` become zero, those past `cap` and features past `left` are not
-// written.
+// that whole runs of features leave at once.  OUT: type written.  Row lane % 32
+// becomes zero unless `used`, and is written if `owned`; features past `left` are not.
 template <int OUT, int TP>
-__device__ inline void store_tile(char* out, int64_t row_bytes, int len, int cap, int left, const f32x16* acc,
+__device__ inline void store_tile(char* out, int64_t row_bytes, bool used, bool owned, int left, const f32x16* acc,
                                   int lane, char* lds) {
   constexpr int eb = OUT == TDP_BF16 ? 2 : 4;
   constexpr int U = OUT == TDP_BF16 && TP > 1 ? 2 : 1;  // tiles side by side in a row of 128 bytes at most
@@ -310,7 +356,7 @@ __device__ inline void store_tile(char* out, int64_t row_bytes, int len, int cap
       for (int r4 = 0; r4 < 4; ++r4) {
         float x[4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) x[e] = r < len ? acc[u0 + u][r4 * 4 + e] : 0.0f;
+        for (int e = 0; e < 4; ++e) x[e] = used ? acc[u0 + u][r4 * 4 + e] : 0.0f;
         const int f = u * 32 + r4 * 8 + h * 4, c = f * eb / 16;
         char* at = lds + r * 128 + ((c ^ (r >> 1 & (kChunks - 1))) << 4) + f * eb % 16;
         if constexpr (OUT == TDP_BF16) {
@@ -329,7 +375,8 @@ __device__ inline void store_tile(char* out, int64_t row_bytes, int len, int cap
       const int row = i + lane / kChunks, c = lane % kChunks;
       const u32x4 v = *reinterpret_cast<const u32x4*>(lds + row * 128 + ((c ^ (row >> 1 & (kChunks - 1))) << 4));
       const int f = u0 * 32 + c * (16 / eb);
-      if (row < cap && f < left) *reinterpret_cast<u32x4*>(out + row * row_bytes + f * eb) = v;
+      const bool write = __shfl((int)owned, row);
+      if (write && f < left) *reinterpret_cast<u32x4*>(out + row * row_bytes + f * eb) = v;
     }
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     __builtin_amdgcn_wave_barrier();
@@ -396,9 +443,10 @@ struct RowCursor {
 //
 // Four waves: STAGES buffers of both, each 16 of the contraction read while the
 // 16 before are multiplied; two workgroups or more share a CU and fill each
-// other's waits.
+// other's waits, so the 128 by 128 tile is held to the registers of two waves per
+// SIMD (fp32, 40 x 300 x 512 -> 2048: 208 us against 258 with one).
 template <int T, int KIND, int BP, int BQ, int WP, int WQ, int STAGES>
-__global__ __launch_bounds__(64 * WP * WQ) void product_kernel(const ProductArgs A) {
+__global__ __launch_bounds__(64 * WP * WQ, BQ == 128 && STAGES == 2 ? 2 : 1) void product_kernel(const ProductArgs A) {
   constexpr int THREADS = 64 * WP * WQ, eb = Mat<T>::kBytes, kStep = kStageBytes / eb, KK = kStep / 16;
   constexpr int TP = BP / WP / 32, TQ = BQ / WQ / 32;
   constexpr bool kTurns = WP * WQ == 8;
@@ -419,16 +467,21 @@ __global__ __launch_bounds__(64 * WP * WQ) void product_kernel(const ProductArgs
   const int split = KIND == kWeight ? 0 : blockIdx.y;
   int w_part = 0, w_parts = 1, w_steps = 0, w_slot = -1;  // dW
   int f0, r0;
+  bool some = false, used[TQ], owned[TQ];  // some row of the tile; the lane's
   if constexpr (KIND != kWeight) {
     const bool quarters = BQ == 128 && A.pass == kRest;  // of the tiles of 256 that are left
-    const RowBlocks rb = {A.seqs, quarters ? 256 : BQ, lane};
+    const RowBlocks rb = {A.seqs, quarters ? 256 : BQ, lane, A.flat};
     const uint32_t nq = (uint32_t)rb.total(), all = nq * A.np, rest = A.pass == kAll ? 0 : rest_tiles(all);
     uint32_t item;
     if (!xcd_item(quarters ? 4 * rest : all - rest, blockIdx.x, item)) return;
     tile_at(nq, A.np, quarters ? all - rest + item / 4 : item, tq, tp);
     blk = (int)tq;
     s = rb.find(blk);
-    sr = seq_rows(A.seqs, s);
+    if (A.flat) {
+      sr.span = sr.cap = sr.len = (int)A.seqs.total;
+    } else {
+      sr = seq_rows(A.seqs, s);
+    }
     e = s % A.E;
     f0 = (int)tp * (quarters ? 256 : BP);
     r0 = blk * (quarters ? 256 : BQ);
@@ -436,6 +489,23 @@ __global__ __launch_bounds__(64 * WP * WQ) void product_kernel(const ProductArgs
       r0 += (item & 1) * 128;
       f0 += (item >> 1 & 1) * 128;
       if (r0 >= sr.cap || f0 >= (KIND == kForward ? A.N : A.K)) return;
+    }
+    some = r0 < sr.len;
+    if (A.flat) {
+      static_assert(kP * OpP::kBytes >= BlockRows<BQ, THREADS>::kBytes, "room for the list");
+      BlockRows<BQ, THREADS> br;
+      br.find(A.seqs, r0, reinterpret_cast<int*>(lds_p));
+      some = br.any_used();
+#pragma unroll
+      for (int j = 0; j < TQ; ++j) br.look_up((wq * TQ + j) * 32 + (lane & 31), used[j], owned[j]);
+      __syncthreads();
+    } else {
+#pragma unroll
+      for (int j = 0; j < TQ; ++j) {
+        const int row = r0 + (wq * TQ + j) * 32 + (lane & 31);
+        used[j] = row < sr.len;
+        owned[j] = row < sr.cap;
+      }
     }
   } else {
     const uint32_t grid = (A.nq * A.np + 7) / 8 * 8;
@@ -445,6 +515,8 @@ __global__ __launch_bounds__(64 * WP * WQ) void product_kernel(const ProductArgs
     tile_at(A.nq, A.np, item, tq, tp);
     f0 = (int)tp * BP;
     r0 = (int)tq * BQ;
+#pragma unroll
+    for (int j = 0; j < TQ; ++j) used[j] = owned[j] = r0 + (wq * TQ + j) * 32 + (lane & 31) < A.N;
     if (A.E <= 64) {
       WeightParts wp;
       wp.count(A, kStep, lane, reinterpret_cast<int*>(lds_p));
@@ -482,12 +554,13 @@ __global__ __launch_bounds__(64 * WP * WQ) void product_kernel(const ProductArgs
   int t0, t1;  // steps
   RowCursor pc, qc;  // dW; y and dx use `at` alone
   if constexpr (KIND != kWeight) {
-    const int steps = r0 < sr.len ? (inner + kStep - 1) / kStep : 0, per = (steps + A.splits - 1) / A.splits;
+    const int steps = some ? (inner + kStep - 1) / kStep : 0, per = (steps + A.splits - 1) / A.splits;
     t0 = split * per;
     t1 = t0 + per < steps ? t0 + per : steps;
     const HeadsDev& in = KIND == kForward ? A.x : A.y;
     qrow = (uint32_t)(in.row_stride * eb);
-    qc.at = in.data + eb * (seq_base(A.seqs, in, s, sr) + r0 * in.row_stride) + (int64_t)t0 * kStageBytes;
+    qc.at = in.data + eb * ((A.flat ? 0 : seq_base(A.seqs, in, s, sr)) + r0 * in.row_stride) +
+            (int64_t)t0 * kStageBytes;
     prow = (uint32_t)A.K * eb;
     pc.at = KIND == kForward ? w + (int64_t)f0 * prow + (int64_t)t0 * kStageBytes
                              : w + (int64_t)t0 * kStep * prow + f0 * eb;
@@ -699,17 +772,17 @@ __global__ __launch_bounds__(64 * WP * WQ) void product_kernel(const ProductArgs
     if constexpr (KIND == kWeight) {
       float* out = (w_slot >= 0 ? A.ws + (int64_t)w_slot * A.N * A.K : A.dw + (int64_t)e * A.N * A.K) +
                    (int64_t)row * A.K + wf;
-      store_tile<TDP_F32, TP>(reinterpret_cast<char*>(out), (int64_t)A.K * 4, A.N - row, A.N - row, A.K - wf, acc[j],
-                              lane, lds);
+      store_tile<TDP_F32, TP>(reinterpret_cast<char*>(out), (int64_t)A.K * 4, used[j], owned[j], A.K - wf, acc[j], lane,
+                              lds);
     } else if (A.splits > 1) {
       // parts lie by the tensor's rows: (splits, total rows, features)
       float* out = A.ws + ((int64_t)split * A.seqs.total + sr.row0 + row) * features + wf;
-      store_tile<TDP_F32, TP>(reinterpret_cast<char*>(out), (int64_t)features * 4, sr.len - row, sr.cap - row,
-                              features - wf, acc[j], lane, lds);
+      store_tile<TDP_F32, TP>(reinterpret_cast<char*>(out), (int64_t)features * 4, used[j], owned[j], features - wf,
+                              acc[j], lane, lds);
     } else {
       const HeadsDev& o = KIND == kForward ? A.y : A.dx;
-      char* out = o.data + eb * (seq_base(A.seqs, o, s, sr) + row * o.row_stride + wf);
-      store_tile<T, TP>(out, o.row_stride * eb, sr.len - row, sr.cap - row, features - wf, acc[j], lane, lds);
+      char* out = o.data + eb * ((A.flat ? 0 : seq_base(A.seqs, o, s, sr)) + row * o.row_stride + wf);
+      store_tile<T, TP>(out, o.row_stride * eb, used[j], owned[j], features - wf, acc[j], lane, lds);
     }
   }
 }
@@ -720,7 +793,7 @@ constexpr int kJoin = 256;
 template <int T>
 __global__ __launch_bounds__(kJoin) void product_join_kernel(const ProductArgs A, HeadsDev o, int features, int rows) {
   const int lane = threadIdx.x & 63;
-  const RowBlocks rb = {A.seqs, rows, lane};
+  const RowBlocks rb = {A.seqs, rows, lane, false};
   int blk = blockIdx.x;
   if (blk >= rb.total()) return;
   const int s = rb.find(blk);
@@ -799,14 +872,17 @@ int launch_rows(const char* fn, ProductArgs A, const tdp_seqs& seqs, const Produ
   const int features = KIND == kForward ? A.N : A.K;
   A.np = (uint32_t)((features + BP - 1) / BP);
   A.splits = sh.splits;
-  const int64_t blocks = row_blocks(seqs, BQ), tiles = (blocks * A.np + 7) / 8 * 8;
+  const HeadsDev &in = KIND == kForward ? A.x : A.y, &out = KIND == kForward ? A.y : A.dx;
+  auto one_matrix = [&](const HeadsDev& t) { return seqs.row_range || t.seq_stride == seqs.max_rows * t.row_stride; };
+  A.flat = flat_rows(seqs, A.E) && one_matrix(in) && one_matrix(out);
+  const int64_t blocks = row_blocks(seqs, BQ, A.flat), tiles = (blocks * A.np + 7) / 8 * 8;
   const int64_t join_y = ((int64_t)kJoinRows * (features / 4) + kJoin - 1) / kJoin, join_x = row_blocks(seqs, kJoinRows);
   int rc = check_items(fn, tiles * sh.splits, 64 * WP * WQ);
   if (rc == TDP_OK && sh.splits > 1) rc = check_items(fn, join_x * join_y, kJoin);
   if (rc != TDP_OK || !enqueue) return rc;
   if constexpr (BQ == 256) {
-    // where the sequences are uniform, the tiles are known here
-    if (sh.splits == 1 && (seqs.row_range || rest_tiles((uint32_t)(blocks * A.np)))) A.pass = kRounds;
+    // except for ragged sequences the tiles are known here
+    if (sh.splits == 1 && ((seqs.row_range && !A.flat) || rest_tiles((uint32_t)(blocks * A.np)))) A.pass = kRounds;
   }
   hipLaunchKernelGGL((product_kernel<T, KIND, BP, BQ, WP, WQ, STAGES>), dim3((unsigned)tiles, (unsigned)sh.splits),
                      dim3(64 * WP * WQ), 0, st, A);
@@ -817,8 +893,8 @@ int launch_rows(const char* fn, ProductArgs A, const tdp_seqs& seqs, const Produ
     }
   }
   if (sh.splits > 1)
-    hipLaunchKernelGGL((product_join_kernel<T>), dim3((unsigned)join_x, (unsigned)join_y), dim3(kJoin), 0, st, A,
-                       KIND == kForward ? A.y : A.dx, features, kJoinRows);
+    hipLaunchKernelGGL((product_join_kernel<T>), dim3((unsigned)join_x, (unsigned)join_y), dim3(kJoin), 0, st, A, out,
+                       features, kJoinRows);
   return TDP_OK;
 }
 
@@ -884,7 +960,7 @@ int tdp_grouped_product(const tdp_seqs* seqs, const tdp_rows* x, const void* wei
   ProductArgs A = {};
   int st = begin(fn, seqs, x, weight, num_weights, y, in_features, out_features, dtype, &A);
   if (st != TDP_OK) return st;
-  const ProductShape sh = rows_shape(*seqs, out_features, in_features, dtype, kNarrowY);
+  const ProductShape sh = rows_shape(*seqs, out_features, in_features, dtype, kNarrowY, flat_rows(*seqs, num_weights));
   st = check_workspace(fn, sh, workspace);
   if (st != TDP_OK) return st;
   A.ws = static_cast<float*>(workspace);
@@ -905,7 +981,7 @@ int tdp_grouped_product_backward(const tdp_seqs* seqs, const tdp_rows* x, const 
   if (st != TDP_OK) return st;
   if (reinterpret_cast<uintptr_t>(dweight) & 15)
     return fail(TDP_EINVAL, "%s: dweight must be 16-byte aligned", fn);
-  const ProductShape si = rows_shape(*seqs, in_features, out_features, dtype, kNarrowDx);
+  const ProductShape si = rows_shape(*seqs, in_features, out_features, dtype, kNarrowDx, flat_rows(*seqs, num_weights));
   const ProductShape sw = weight_shape(*seqs, num_weights, in_features, out_features, dtype);
   if (dx) st = check_workspace(fn, si, workspace);
   if (st == TDP_OK && dweight) st = check_workspace(fn, sw, workspace);

@@ -228,14 +228,14 @@ int64_t tdp_grouped_product_workspace(const tdp_seqs* seqs, int32_t num_weights,
                                       int32_t out_features, int32_t dtype) {
   const char* fn = "tdp_grouped_product_workspace";
   if (check_product(fn, seqs, num_weights, in_features, out_features) != TDP_OK || !dtype_bytes(dtype)) return 0;
-  return rows_workspace(*seqs, out_features, in_features, dtype, kNarrowY);
+  return rows_workspace(*seqs, out_features, in_features, dtype, kNarrowY, flat_rows(*seqs, num_weights));
 }
 
 int64_t tdp_grouped_product_backward_workspace(const tdp_seqs* seqs, int32_t num_weights, int32_t in_features,
                                                int32_t out_features, int32_t dtype) {
   const char* fn = "tdp_grouped_product_backward_workspace";
   if (check_product(fn, seqs, num_weights, in_features, out_features) != TDP_OK || !dtype_bytes(dtype)) return 0;
-  const int64_t a = rows_workspace(*seqs, in_features, out_features, dtype, kNarrowDx);
+  const int64_t a = rows_workspace(*seqs, in_features, out_features, dtype, kNarrowDx, flat_rows(*seqs, num_weights));
   const int64_t b = weight_workspace(*seqs, num_weights, in_features, out_features, dtype);
   return a > b ? a : b;  // dx and dW take turns
 }

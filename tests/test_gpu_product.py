@@ -49,6 +49,23 @@ TILES = [
     (72, 72, 70, 40, 70),
 ]
 
+# as those with one weight, whose tiles are of the tensors' rows, with several
+TILES += [
+    (136, 72, 12, 2500, 2), (72, 72, 12, 5000, 2), (2056, 72, 3, 2500, 2), (136, 2056, 12, 33, 3), (72, 72, 40, 200, 3),
+    (8200, 72, 40, 33, 3), (72, 1032, 40, 130, 3), (8200, 264, 12, 130, 3), (72, 8200, 5, 130, 2),
+]
+# one weight for sequences that end anywhere in a tile
+SHARED = [
+    (136, 264, (46,) * 24, tuple(46 - 5 * (i % 3) for i in range(24)), True, 1, "wide"),
+    (72, 2056, tuple(i % 5 for i in range(600)), tuple(max(0, i % 5 - i % 2) for i in range(600)), True, 1, "rows"),
+    (136, 264, (1,) * 700, (1, 0) * 350, True, 1, "rows"),
+    (264, 136, (46,) * 50, (0,) * 30 + tuple(range(20)), False, 1, "rows"),        # whole tiles without a used row
+    (264, 136, (46,) * 50, (0,) * 30 + tuple(range(20)), False, 1, "seqs"),        # rows apart: tiles of sequences
+    (2056, 72, (20,) * 7, (20, 0, 3, 20, 20, 1, 20), True, 1, "wide"),             # few rows: the contraction split
+    (72, 4104, (150,) * 30, tuple(150 - i for i in range(30)), True, 1, "wide"),   # large tiles and some beyond a round
+    (4104, 72, (150,) * 30, tuple(150 - i for i in range(30)), True, 1, "wide"),   # the same of dx
+]
+
 
 def setup(case, dtype, cuda, seed):
     K, N, caps, lens, ragged, E, kind = case
@@ -173,3 +190,44 @@ def test_broadcast_rows(dtype, cuda):
         assert (got[n - 2:] == 0).all()
     one = dy.double().T @ x.double()
     check("dw", dw, (n - 2) * one, (n + 24) * U32 * n * one.abs())
+
+
+@pytest.mark.parametrize("dtype", list(DT))
+@pytest.mark.parametrize("case", SHARED, ids=[f"{c[0]}to{c[1]}-{len(c[2])}x{c[2][0]}-{c[6]}" for c in SHARED])
+def test_grouped_product_shared_weight(case, dtype, cuda):
+    check_forward(case, dtype, cuda, 49)
+    check_backward(case, dtype, cuda, 50)
+
+
+@pytest.mark.parametrize("dtype", list(DT))
+@pytest.mark.parametrize("E", [1, 2])
+def test_grouped_product_row_limit(E, dtype, cuda):
+    """Ranges longer than max_rows: rows past it are left alone."""
+    K, N, limit = 72, 136, 30
+    ranges = [(3, 48), (48, 78), (80, 80), (80, 200), (200, 201), (201, 290)]
+    lens = (45, 29, 0, 30, 1, 12)
+    rows = [(a, min(b - a, limit), min(b - a, n, limit)) for (a, b), n in zip(ranges, lens)]
+    seqs = tdp.Sequences(len(ranges), limit, row_range=torch.tensor(ranges, dtype=torch.int64, device=cuda), total_rows=300,
+                         seq_len=torch.tensor(lens, dtype=torch.int32, device=cuda))
+    gen = torch.Generator().manual_seed(51)
+    x, dy = (torch.full((300, k), NAN).to(DT[dtype]) for k in (K, N))
+    for a, _, n in rows:
+        x[a:a + n], dy[a:a + n] = torch.randn(n, K, generator=gen), torch.randn(n, N, generator=gen)
+    w = (torch.randn(E, N, K, generator=gen) * K ** -0.5).to(DT[dtype])
+    xd, gd, wd = x.to(cuda), dy.to(cuda), w.to(cuda)
+    y, dx, dw = torch.full_like(gd, NAN), torch.full_like(xd, NAN), torch.empty(E, N, K, device=cuda)
+    note(f"row limit {E} {dtype}")
+    ws = tdp.allocate_grouped_product_workspace(seqs, E, N, K, DT[dtype], cuda)
+    tdp.tdp_grouped_product(seqs, xd, wd, y, workspace=ws)
+    ws = tdp.allocate_grouped_product_backward_workspace(seqs, E, N, K, DT[dtype], cuda)
+    tdp.tdp_grouped_product_backward(seqs, xd, wd, gd, dx, dw, ws)
+    torch.cuda.synchronize()
+    check_rest("y", y, rows)
+    check_rest("dx", dx, rows)
+    want, bound = torch.zeros(E, N, K, dtype=torch.float64), torch.zeros(E, N, K, dtype=torch.float64)
+    for s, (a, _, n) in enumerate(rows):
+        check("y", y[a:a + n], *L.product(x[a:a + n], w[s % E], DT[dtype]))
+        check("dx", dx[a:a + n], *L.product(dy[a:a + n], w[s % E].T, DT[dtype]))
+        want[s % E] += dy[a:a + n].double().T @ x[a:a + n].double()
+        bound[s % E] += dy[a:a + n].double().abs().T @ x[a:a + n].double().abs()
+    check("dw", dw, want, (sum(n for _, _, n in rows) + 24) * U32 * bound)
