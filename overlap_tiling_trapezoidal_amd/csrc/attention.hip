@@ -693,6 +693,62 @@ __global__ __launch_bounds__(kTok) void attn_join_kernel(const AttnArgs A, float
     A.lse[(int64_t)head * A.qs.total + qr.row0 + row] = live ? mx * unit + logf(l) : -INFINITY;
 }
 
+// The same sums in the same order with a wave per query entry, for launches of many
+// entries, which then wait for fewer workgroups (bf16, causal, with the products: 3 x
+// 710 rows, 6 heads of 96 in two parts 23 us against 31; 32 new rows of 4 sequences
+// over 8192 keys, 16 heads of 128, 25 against 26).
+template <int T, int DP>
+__global__ __launch_bounds__(kTok) void attn_join_rows_kernel(const AttnArgs A, float c, float unit) {
+  constexpr int E = DP < 64 ? 1 : DP / 64;
+  static_assert(kAttnMaxSplits <= 64, "a part per lane");
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+  const int64_t g = (int64_t)blockIdx.x * 4 + wave;  // ((s, hk), m)
+  const int64_t n1 = (int64_t)A.qs.S * A.k.heads * A.m_max;
+  if (g >= n1) return;
+  const int64_t sh = g / A.m_max;
+  const int m = (int)(g - sh * A.m_max), s = (int)(sh / A.k.heads), hk = (int)(sh - (int64_t)s * A.k.heads);
+  const SeqRows qr = seq_rows(A.qs, s);
+  if (m >= qr.cap * A.group) return;
+  f32x2 ml = {-INFINITY, 0.0f};
+  if (lane < A.splits) ml = reinterpret_cast<const f32x2*>(A.ws + n1 * A.splits * DP)[lane * n1 + g];
+  float mx = -INFINITY, l = 0.0f;
+  for (int i = 0; i < A.splits; ++i) mx = fmaxf(mx, __shfl(ml.x, i));
+  const float mine = mx == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f((ml.x - mx) * c);
+  float x[4][E];
+#pragma unroll
+  for (int u = 0; u < 4; ++u)
+#pragma unroll
+    for (int e = 0; e < E; ++e) x[u][e] = 0.0f;
+  for (int i = 0; i < A.splits; i += 4) {
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      if (i + u >= A.splits) break;
+      const float f = __shfl(mine, i + u);
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        const int d = e * 64 + lane;
+        if (d < DP) x[u][e] = fmaf(A.ws[((i + u) * n1 + g) * DP + d], f, x[u][e]);
+      }
+    }
+  }
+  for (int i = 0; i < A.splits; ++i) l = fmaf(__shfl(ml.y, i), __shfl(mine, i), l);
+  const int row = (int)fastdiv((uint32_t)m, A.by_group), head = hk * A.group + (m - row * A.group);
+  const bool live = row < qr.len && l != 0.0f;
+  char* op = A.o.data + Mat<T>::kBytes * (seq_base(A.qs, A.o, s, qr) + row * A.o.row_stride + head * A.o.head_stride);
+#pragma unroll
+  for (int e = 0; e < E; ++e) {
+    const int d = e * 64 + lane;
+    if (d >= A.D) continue;
+    const float y = live ? ((x[0][e] + x[1][e]) + (x[2][e] + x[3][e])) / l : 0.0f;
+    if constexpr (T == TDP_BF16)
+      reinterpret_cast<__bf16*>(op)[d] = (__bf16)y;
+    else
+      reinterpret_cast<float*>(op)[d] = y;
+  }
+  if (A.lse && lane == 0)
+    A.lse[(int64_t)head * A.qs.total + qr.row0 + row] = live ? mx * unit + logf(l) : -INFINITY;
+}
+
 // A weight again from its score: exp(s - lse) in powers of two, nl = -lse log2(e),
 // -infinity for rows without keys.  No weight exceeds one, but lse and its change
 // of unit are rounded by up to 2^-22 of it altogether, so past |lse| = 10^8 the
@@ -1212,13 +1268,18 @@ dim3 grid_of(const AttnArgs& A) {
   return dim3(WIN ? chunk_grid(A.tiles, A.chunk) : xcd_grid(A.tiles));
 }
 
+constexpr int64_t kJoinRowsFrom = 2048;  // entries: one wave each fills every SIMD twice
 template <int T, int DP, bool BIAS, bool WIN>
 void launch_forward(AttnArgs A, hipStream_t st) {
   if (WIN) A.chunk = window_chunk(A.tiles, A.uneven);
   hipLaunchKernelGGL((attn_forward_kernel<T, DP, BIAS, WIN>), grid_of<WIN>(A), dim3(kTok), 0, st, A);
-  if (A.splits > 1)
-    hipLaunchKernelGGL((attn_join_kernel<T, DP>), dim3((unsigned)(A.qs.S * A.k.heads * A.m_max)), dim3(kTok), 0, st, A,
-                       BIAS ? 1.0f : A.scale * kLog2e, BIAS ? kLn2 : A.scale);
+  if (A.splits == 1) return;
+  const int64_t entries = (int64_t)A.qs.S * A.k.heads * A.m_max;
+  const float c = BIAS ? 1.0f : A.scale * kLog2e, unit = BIAS ? kLn2 : A.scale;
+  if (entries >= kJoinRowsFrom)
+    hipLaunchKernelGGL((attn_join_rows_kernel<T, DP>), dim3((unsigned)((entries + 3) / 4)), dim3(kTok), 0, st, A, c, unit);
+  else
+    hipLaunchKernelGGL((attn_join_kernel<T, DP>), dim3((unsigned)entries), dim3(kTok), 0, st, A, c, unit);
 }
 
 template <int T, int DP, bool BIAS, bool WIN>

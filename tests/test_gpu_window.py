@@ -13,6 +13,7 @@ import torch
 import layer_reference as L
 import overlap_tiling_trapezoidal_amd as tdp
 from harness import note
+import test_gpu_tokens as tokens
 from test_gpu_tokens import DT, NAN, check, check_rest, layout, poisoned, to_device
 
 pytestmark = pytest.mark.gpu
@@ -39,6 +40,8 @@ CASES = [
     ((600,) * 28, tuple(600 - 20 * i for i in range(28)), None, None, 8, 8, 32, (1, ALL, 0, 0), False, "rows"),  # chunks
     ((1300,) * 2, (1300, 1200), None, None, 16, 16, 32, (1, 100, 0, 130), False, "rows"),  # first rows' blocks split
     ((1300,) * 2, (1300, 1200), None, None, 16, 16, 32, (50, 3, 1, 50), False, "packed"),
+    ((700,) * 2, (700, 611), None, None, 4, 2, 96, (1, ALL, 0, 0), False, "rows"),         # parts of many rows joined
+    ((300, 211), (300, 17), (2100, 2000), (2099, 40), 8, 2, 40, (1, 1500, 0, 64), True, "packed"),
 ]
 IDS = [f"{'x'.join(map(str, c[0]))}-h{c[4]}.{c[5]}-d{c[6]}-{'.'.join(map(str, c[7]))}" for c in CASES]
 
@@ -173,3 +176,9 @@ def test_window_prompt_and_token_by_token_agree(cuda):
     mag = v.abs().max().float()
     # weights of one row rounded at different maxima: 2^-8 of them each, and the outputs' roundings
     assert ((whole.float() - one.float()).abs() <= 4 * 2.0 ** -8 * mag).all()
+
+
+@pytest.mark.parametrize("dtype", list(DT))
+@pytest.mark.parametrize("bias", [None, "pad", "lowest"])
+def test_attention_parts_of_many_rows(bias, dtype, cuda):
+    tokens.test_attention(((330,) * 2, (330, 301), (1100,) * 2, (1099, 530), 4, 1, 72, bias, False, "rows"), dtype, cuda)
