@@ -4,13 +4,19 @@
 //   with n = (x - mean) r and g = dy w:
 //   dx = r (g - mean(g) - n mean(g n)),  dw = sum of dy n,  db = sum of dy
 //
-// Bound by HBM bandwidth: a row is read once, stays in registers for both sums
-// (the squares are of the differences from the mean, so an offset of the row
-// costs no digits), and is written once.  G lanes share a row, eight elements of
-// it per lane NV times; rows wider than one wave holds take the workgroup.  A
-// workgroup takes several blocks of rows, the next one's loads in flight while
-// this one is worked on, and keeps the weights in registers.  247296 rows of 2048
-// bf16 (2.03 GB) take 357 us, 5.7 TB/s of the 5.96 that a plain copy reaches.
+// Bound by HBM bandwidth: a row is read once, stays in registers for its three
+// sums, and is written once.  The sum of the elements alone leaves the mean off by
+// a few 2^-24 of the row's offset, which every difference would carry (rows around
+// 10^4 with a spread of 1: up to 10^-3).  The mean of the differences is that
+// error, so they are lowered by it before their squares are summed, and an offset
+// of the row costs no digits (taken from the squares' sum instead, it would cancel
+// in rows of nearly one value).  The third sum costs up to 2 % in bf16 and 5 % in
+// fp32 rows of 2048 and more (35840 of them 114 us against 109).  G lanes share a
+// row, eight elements of it per lane NV times; rows wider than one wave holds take
+// the workgroup.  A workgroup takes several blocks of rows, the next one's loads in
+// flight while this one is worked on, and keeps the weights in registers.  247296
+// rows of 2048 bf16 (2.03 GB) take 358 us, 5.7 TB/s of the 5.96 that a plain copy
+// reaches.
 #include <hip/hip_runtime.h>
 #include <math.h>
 #include <stdint.h>
@@ -94,6 +100,22 @@ struct Lane {
     for (int v = 0; v < NV; ++v)
       if (on[v]) Raw<T>::store(p + v * G * 16, half, y[v]);
   }
+  // a row's differences from its mean: from the sum's, then from what that left
+  __device__ inline void center(float (*x)[8], float m, float inv_c, float* red) const {
+    float left = 0.0f;
+#pragma unroll
+    for (int v = 0; v < NV; ++v)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        x[v][e] = on[v] ? x[v][e] - m : 0.0f;
+        left += x[v][e];
+      }
+    left = row_sum<G>(left, red) * inv_c;
+#pragma unroll
+    for (int v = 0; v < NV; ++v)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) x[v][e] = on[v] ? x[v][e] - left : 0.0f;
+  }
   // a vector of weights (null: all `value`)
   __device__ inline void weights(const float* w, float value, float (*out)[8]) const {
 #pragma unroll
@@ -120,7 +142,7 @@ struct RowOf {
 template <int T, int G, int NV>
 __global__ __launch_bounds__(kTok) void layer_norm_kernel(const NormArgs A) {
   typedef Lane<T, G, NV> L;
-  __shared__ float red[2][4];
+  __shared__ float red[3][4];
   const L ln(A.C);
   const float inv_c = 1.0f / (float)A.C;
   const uint32_t n = A.blocks * (uint32_t)A.seqs.S;
@@ -153,14 +175,12 @@ __global__ __launch_bounds__(kTok) void layer_norm_kernel(const NormArgs A) {
 #pragma unroll
       for (int e = 0; e < 8; ++e) m += x[v][e];
     m = row_sum<G>(m, red[0]) * inv_c;
+    ln.center(x, m, inv_c, red[1]);
 #pragma unroll
     for (int v = 0; v < NV; ++v)
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        x[v][e] = ln.on[v] ? x[v][e] - m : 0.0f;
-        q = fmaf(x[v][e], x[v][e], q);
-      }
-    const float r = __builtin_amdgcn_rsqf(fmaf(row_sum<G>(q, red[1]), inv_c, A.eps));
+      for (int e = 0; e < 8; ++e) q = fmaf(x[v][e], x[v][e], q);
+    const float r = __builtin_amdgcn_rsqf(fmaf(row_sum<G>(q, red[2]), inv_c, A.eps));
     const bool live = at.live();
 #pragma unroll
     for (int v = 0; v < NV; ++v)
@@ -172,12 +192,12 @@ __global__ __launch_bounds__(kTok) void layer_norm_kernel(const NormArgs A) {
 
 // dx, and each workgroup's sums of dw and db over its rows, fp32 in a fixed
 // order.  A workgroup keeps to one set of weights.  On 35840 rows of 2048 bf16
-// (440 MB) 81 us with the join, 5.4 TB/s; a workgroup per row, whose eight elements
+// (440 MB) 82 us with the join, 5.4 TB/s; a workgroup per row, whose eight elements
 // per lane need fewer registers, takes 99 for the barriers of its sums.
 template <int T, int G, int NV>
 __global__ __launch_bounds__(kTok) void layer_norm_backward_kernel(const NormArgs A) {
   typedef Lane<T, G, NV> L;
-  __shared__ float red[2][8];
+  __shared__ float red[3][8];
   __shared__ float join[G < 256 ? 4 : 1][G < 256 ? 8 * 64 : 1];
   const L ln(A.C);
   const float inv_c = 1.0f / (float)A.C;
@@ -217,17 +237,16 @@ __global__ __launch_bounds__(kTok) void layer_norm_backward_kernel(const NormArg
         mg = fmaf(g[v][e], w[v][e], mg);
       }
     row_sums<G>(m, mg, red[0]);
-    m *= inv_c;
     mg *= inv_c;
+    ln.center(x, m * inv_c, inv_c, red[1]);
 #pragma unroll
     for (int v = 0; v < NV; ++v)
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        x[v][e] = ln.on[v] ? x[v][e] - m : 0.0f;
         q = fmaf(x[v][e], x[v][e], q);
         gx = fmaf(g[v][e] * w[v][e], x[v][e], gx);
       }
-    row_sums<G>(q, gx, red[1]);
+    row_sums<G>(q, gx, red[2]);
     const bool live = at.live();
     // a row past the end holds zeros, whose r is infinite when eps is 0
     const float r = live ? __builtin_amdgcn_rsqf(fmaf(q, inv_c, A.eps)) : 0.0f;

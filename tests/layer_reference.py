@@ -22,18 +22,34 @@ def _norm_parts(x, eps):
     return d, dd, r, 0.5 * dvar / (var + eps) + 3 * U32
 
 
-def layer_norm(x, w, b, eps, dtype):
+def far_parts(x, eps):
+    """The same where the mean's own error is taken out again: what is left of it scales with the row's spread,
+    not with its offset."""
+    mean = x.mean(1, keepdim=True)
+    d = x - mean
+    var = d.square().mean(1, keepdim=True)
+    r = 1.0 / torch.sqrt(var + eps)
+    first = 48 * U32 * x.abs().mean(1, keepdim=True)
+    # differences from the first mean are no larger than |d| + first; their mean is a sum like the first
+    dm = 48 * U32 * (d.abs().mean(1, keepdim=True) + first)
+    dd = dm + U32 * (2 * d.abs() + first)
+    ddm = dd.mean(1, keepdim=True)
+    dvar = 50 * U32 * var + 2 * (d.abs() * dd).mean(1, keepdim=True) + ddm * ddm + dd.square().mean(1, keepdim=True)
+    return d, dd, r, 0.5 * dvar / (var + eps) + 3 * U32
+
+
+def layer_norm(x, w, b, eps, dtype, parts=_norm_parts):
     x, w, b = x.double(), w.double(), b.double()
-    d, dd, r, dr = _norm_parts(x, eps)
+    d, dd, r, dr = parts(x, eps)
     n = d * r * w
     y = n + b
     return y, dd * r * w.abs() + n.abs() * (dr + 3 * U32) + U32 * y.abs() + half_step(dtype) * y.abs()
 
 
-def layer_norm_backward(x, w, dy, eps, dtype):
+def layer_norm_backward(x, w, dy, eps, dtype, parts=_norm_parts):
     """(dx, bound, dw, bound, db, bound); the sums over these rows alone."""
     x, w, dy = x.double(), w.double(), dy.double()
-    d, dd, r, dr = _norm_parts(x, eps)
+    d, dd, r, dr = parts(x, eps)
     n, g = d * r, dy * w
     mg, c = g.mean(1, keepdim=True), (g * d).mean(1, keepdim=True) * r * r
     dx = r * (g - mg - d * c)

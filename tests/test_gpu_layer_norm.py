@@ -168,3 +168,29 @@ def test_layer_norm_values(cuda):
     assert torch.isnan(y[2]).all() and torch.isnan(y[3]).all()
     for i in (1, 4, 5):
         check(f"row {i}", y[i:i + 1], *L.layer_norm(x[i:i + 1], torch.ones(C), b, 1e-5, torch.float32))
+
+
+@pytest.mark.parametrize("dtype", list(DT))
+@pytest.mark.parametrize("offset", [100.0, 1e3, -1e4, 1e6])
+@pytest.mark.parametrize("C", [8, 136, 520, 2048, 4104, 8192])
+def test_layer_norm_far_rows(C, offset, dtype, cuda):
+    """Rows far from zero: the error scales with their spread, not with their offset, in outputs and gradients."""
+    gen, rows = torch.Generator().manual_seed(C), 5
+    seqs = tdp.Sequences(1, rows)
+    x = (offset + torch.randn(rows, C, generator=gen)).to(DT[dtype])
+    x[1] = offset + 100 * torch.randn(C, generator=gen)
+    x[2, C // 2] = -offset   # an element far from the others
+    dy = torch.randn(rows, C, generator=gen).to(DT[dtype])
+    w, b = 1.0 + 0.3 * torch.randn(C, generator=gen), 0.5 * torch.randn(C, generator=gen)
+    xd, wd, y, dx = x.to(cuda), w.to(cuda), torch.empty_like(x, device=cuda), torch.empty_like(x, device=cuda)
+    dw, db = torch.empty(C, device=cuda), torch.empty(C, device=cuda)
+    note(f"layer norm far rows {C} {offset} {dtype}")
+    tdp.tdp_layer_norm(seqs, xd, wd, b.to(cuda), y, eps=1e-5)
+    tdp.tdp_layer_norm_backward(seqs, xd, wd, dy.to(cuda), dx, dw, db, tdp.allocate_layer_norm_workspace(seqs, C, 1, cuda),
+                                eps=1e-5)
+    torch.cuda.synchronize()
+    check("y", y, *L.layer_norm(x, w, b, 1e-5, DT[dtype], L.far_parts))
+    g, gb, w1, w1b, b1, b1b = L.layer_norm_backward(x, w, dy, 1e-5, DT[dtype], L.far_parts)
+    check("dx", dx, g, gb)
+    check("dw", dw, w1, w1b)
+    check("db", db, b1, b1b)
