@@ -94,7 +94,8 @@ inline ProductShape rows_shape(const tdp_seqs& s, int32_t features, int32_t inne
 // dW: its tile of W's rows is `rows` too, the contraction the rows of a weight's
 // sequences.  How many rows a weight has is known on the device only, so `splits`
 // says in how many parts the rows of all weights are cut where one has them all
-// (parts of less than kWeightSteps steps are not worth a slot).
+// (parts of less than kWeightSteps steps are not worth a slot).  A step does not
+// reach across the end of a sequence, so many short ones are many steps of few rows.
 constexpr int kWeightSteps = 8;
 constexpr int kWeightMaxPlaces = 64;
 inline ProductShape weight_shape(const tdp_seqs& s, int32_t weights, int32_t in_features, int32_t out_features,
@@ -104,7 +105,7 @@ inline ProductShape weight_shape(const tdp_seqs& s, int32_t weights, int32_t in_
   if (weights > 64) return sh;
   const int64_t tiles = tiles_across(in_features, sh.rows) * tiles_across(out_features, sh.rows);
   int64_t n = (sh.rows == 256 ? 256 : 512) / tiles;
-  const int64_t steps = s.total_rows * dtype_bytes(dtype) / 128;
+  const int64_t steps = row_blocks(s, 128 / dtype_bytes(dtype));
   if (n > steps / kWeightSteps) n = steps / kWeightSteps;
   if (n > kWeightMaxPlaces) n = kWeightMaxPlaces;
   sh.splits = n < 2 ? 1 : (int)n;

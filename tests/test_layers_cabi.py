@@ -216,3 +216,16 @@ def test_grouped_product_workspace():
     for args in ((0, 128, 128), (5, 128, 128), (1, 0, 128), (1, 128, 12), (1, 128, tdp.TDP_MAX_FEATURES + 8)):
         assert fwd(few, *args) == 0 and bwd(few, *args) == 0
     assert fwd(few, 1, 4096, 4096, 7) == 0
+
+
+def test_grouped_product_workspace_of_short_sequences():
+    """The gradient of a weight takes a step at least per sequence, so many short ones are split like a long one."""
+    lib = tdp.load_library()
+    bwd = lambda s, K, N, dt: lib.tdp_grouped_product_backward_workspace(ctypes.byref(s), 1, K, N, dt)  # noqa: E731
+    for dt in (tdp.TDP_BF16, tdp.TDP_F32):
+        for n, rows in ((700, 1), (600, 2), (250, 3)):
+            short = seqs(num_seqs=n, max_rows=rows, total_rows=n * rows, len_group=1)
+            slots = bwd(short, 136, 264, dt) // (136 * 264 * 4)   # two per part; dx needs less
+            assert slots >= 2 * (n // 8 if n < 512 else 64), (dt, n, rows, slots)
+        few = seqs(num_seqs=7, max_rows=1, total_rows=7, len_group=1)
+        assert bwd(few, 136, 264, dt) == 0
