@@ -154,8 +154,11 @@ struct Along {
 
 // An operand whose contraction runs across its rows, which hold COLS elements,
 // chunk c of row r at c ^ 4 (r % 4): the four rows that a transposing read touches
-// lie in different quarters of the banks.
-template <int T, int COLS, int THREADS>
+// lie in different quarters of the banks.  ANEW: fp32 columns' places are made anew
+// for each fragment.  Kept over the loop, those of both operands of dW take the
+// registers of two waves per SIMD and more, and reading them back from memory waits
+// for the operands' loads too (4096 x 4096 x 4096: 1214 us, 1083 anew).
+template <int T, int COLS, int THREADS, bool ANEW>
 struct Across {
   typedef typename Mat<T>::Frag Frag;
   static constexpr int kRow = COLS * Mat<T>::kBytes, kChunks = kRow / 16, kRows = kStageBytes / Mat<T>::kBytes;
@@ -190,13 +193,12 @@ struct Across {
       const bf16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4bf16((P)(TDP_LDS char*)(lds + at + 4 * kRow));
       return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
     } else {
-      const int c = c0 + (lane & 31);
+      int at = 8 * h * kRow + 4 * (c0 + (lane & 31));
+      if (ANEW) asm volatile("" : "+v"(at));
       f32x8 v;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const int r = 16 * kk + 8 * h + e;
-        v[e] = *reinterpret_cast<const float*>(lds + r * kRow + (((c >> 2) ^ ((r & 3) << 2)) << 4) + (c & 3) * 4);
-      }
+      for (int e = 0; e < 8; ++e)
+        v[e] = *reinterpret_cast<const float*>(lds + (16 * kk + e) * kRow + (at ^ ((e & 3) << 6)));
       return v;
     }
   }
@@ -444,15 +446,16 @@ struct RowCursor {
 // Four waves: STAGES buffers of both, each 16 of the contraction read while the
 // 16 before are multiplied; two workgroups or more share a CU and fill each
 // other's waits, so the 128 by 128 tile is held to the registers of two waves per
-// SIMD (fp32, 40 x 300 x 512 -> 2048: 208 us against 258 with one).
+// SIMD (against one, 4096 x 4096 x 4096 fp32: y 1015 us and 1211, dW 1083 and 1338;
+// 8 x 1000 rows, 1024 -> 2048 bf16: dx 38 and 58).
 template <int T, int KIND, int BP, int BQ, int WP, int WQ, int STAGES>
 __global__ __launch_bounds__(64 * WP * WQ, BQ == 128 && STAGES == 2 ? 2 : 1) void product_kernel(const ProductArgs A) {
   constexpr int THREADS = 64 * WP * WQ, eb = Mat<T>::kBytes, kStep = kStageBytes / eb, KK = kStep / 16;
   constexpr int TP = BP / WP / 32, TQ = BQ / WQ / 32;
   constexpr bool kTurns = WP * WQ == 8;
   typedef typename Mat<T>::Frag Frag;
-  typedef std::conditional_t<KIND == kForward, Along<T, BP, THREADS>, Across<T, BP, THREADS>> OpP;
-  typedef std::conditional_t<KIND == kWeight, Across<T, BQ, THREADS>, Along<T, BQ, THREADS>> OpQ;
+  typedef std::conditional_t<KIND == kForward, Along<T, BP, THREADS>, Across<T, BP, THREADS, KIND == kWeight>> OpP;
+  typedef std::conditional_t<KIND == kWeight, Across<T, BQ, THREADS, true>, Along<T, BQ, THREADS>> OpQ;
   constexpr int kP = kTurns ? 3 : STAGES, kQ = kTurns ? 2 : STAGES;  // buffers
   __shared__ __align__(1024) char lds_p[kP * OpP::kBytes];
   __shared__ __align__(1024) char lds_q[kQ * OpQ::kBytes];
