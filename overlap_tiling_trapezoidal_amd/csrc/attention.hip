@@ -191,7 +191,7 @@ __device__ inline uint32_t chunk_item(uint32_t chunk) {
   const uint32_t slot = blockIdx.x >> 3, c = slot / chunk;
   return (c * 8 + ((blockIdx.x + c) & 7)) * chunk + (slot - c * chunk);
 }
-inline uint32_t chunk_grid(uint32_t tiles, uint32_t chunk) { return (tiles + 8 * chunk - 1) / (8 * chunk) * 8 * chunk; }
+inline int64_t chunk_grid(int64_t tiles, int64_t chunk) { return (tiles + 8 * chunk - 1) / (8 * chunk) * 8 * chunk; }
 inline uint32_t window_chunk(int64_t tiles, bool uneven) {
   return uneven && tiles >= 1024 ? 16 : (uint32_t)((tiles + 7) / 8);
 }
@@ -1265,7 +1265,7 @@ __global__ __launch_bounds__(kTok) void attn_sum_kernel(const AttnArgs A) {
 
 template <bool WIN>
 dim3 grid_of(const AttnArgs& A) {
-  return dim3(WIN ? chunk_grid(A.tiles, A.chunk) : xcd_grid(A.tiles));
+  return dim3(WIN ? (uint32_t)chunk_grid(A.tiles, A.chunk) : xcd_grid(A.tiles));
 }
 
 constexpr int64_t kJoinRowsFrom = 2048;  // entries: one wave each fills every SIMD twice
@@ -1351,6 +1351,12 @@ int begin(const char* fn, const tdp_seqs* q_seqs, const tdp_seqs* k_seqs, const 
   return TDP_OK;
 }
 
+// Whole chunks are launched: up to 127 workgroups more than tiles, where ranges of
+// eight stay within the margin of check_items.
+int64_t tile_items(const AttnArgs& A, int64_t tiles) {
+  return A.win.step && tiles <= UINT32_MAX ? chunk_grid(tiles, window_chunk(tiles, A.uneven)) : tiles;
+}
+
 int check_items(const char* fn, int64_t workgroups) {
   if (workgroups * kTok > 0xffffffffLL - 8 * kTok)
     return fail(TDP_ESHAPE, "%s: %lld workgroups, more work-items than one HIP launch holds", fn, (long long)workgroups);
@@ -1400,7 +1406,8 @@ int forward(const char* fn, const tdp_seqs* q_seqs, const tdp_seqs* k_seqs, cons
   A.ws = static_cast<float*>(workspace);
   const int64_t tiles = (int64_t)A.blocks * q_seqs->num_seqs * k->heads * A.splits;
   const int64_t join = A.splits > 1 ? (int64_t)q_seqs->num_seqs * k->heads * A.m_max : 0;
-  st = check_items(fn, tiles > join ? tiles : join);
+  const int64_t grid = tile_items(A, tiles);
+  st = check_items(fn, grid > join ? grid : join);
   if (st != TDP_OK) return st;
   A.tiles = (uint32_t)tiles;
   hipStream_t hs = reinterpret_cast<hipStream_t>(stream);
@@ -1442,7 +1449,8 @@ int backward(const char* fn, const tdp_seqs* q_seqs, const tdp_seqs* k_seqs, con
   const int64_t qt = A.blocks * heads;
   const int64_t kt = dkv_blocks(*k_seqs, k->heads) + sp.blocks * heads * (sp.n - 1);
   const int64_t sum = sp.n > 1 ? (heads * sp.rows * 32 + kTok - 1) / kTok : 0;
-  st = check_items(fn, qt > kt ? (qt > sum ? qt : sum) : (kt > sum ? kt : sum));
+  for (const int64_t n : {tile_items(A, qt), tile_items(A, kt), sum})
+    if (st == TDP_OK) st = check_items(fn, n);
   if (st != TDP_OK) return st;
   A.tiles = (uint32_t)qt;
   hipStream_t hs = reinterpret_cast<hipStream_t>(stream);

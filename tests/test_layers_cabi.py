@@ -229,3 +229,16 @@ def test_grouped_product_workspace_of_short_sequences():
             assert slots >= 2 * (n // 8 if n < 512 else 64), (dt, n, rows, slots)
         few = seqs(num_seqs=7, max_rows=1, total_rows=7, len_group=1)
         assert bwd(few, 136, 264, dt) == 0
+
+
+@pytest.mark.device_abi
+@pytest.mark.parametrize("call", [window_call, window_backward_call], ids=["forward", "backward"])
+def test_window_attention_counts_what_it_launches(call):
+    """Work is dealt in whole chunks, which may take a launch past its limit where the work alone does not."""
+    n = (1 << 24) - 16
+    few = seqs(num_seqs=n, max_rows=1, total_rows=n)
+    one = {name: heads32(1) for name in ("q", "k", "v", "out")}
+    if call is window_backward_call:
+        one.update({name: heads32(1) for name in ("dout", "dq", "dk", "dv")})
+    assert call(qs=few, ks=few, w=window(back=tdp.TDP_WINDOW_ALL), **one) == tdp.TDP_ESHAPE
+    assert "work-items" in tdp.tdp_last_error()
