@@ -1404,7 +1404,7 @@ int forward(const char* fn, const tdp_seqs* q_seqs, const tdp_seqs* k_seqs, cons
   if (A.splits > 1 && (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 15)))
     return fail(TDP_EINVAL, "%s: workspace must be a 16-byte aligned device pointer (%s_workspace)", fn, fn);
   A.ws = static_cast<float*>(workspace);
-  const int64_t tiles = (int64_t)A.blocks * q_seqs->num_seqs * k->heads * A.splits;
+  const int64_t tiles = attention_blocks(*q_seqs, q->heads, k->heads) * A.splits;
   const int64_t join = A.splits > 1 ? (int64_t)q_seqs->num_seqs * k->heads * A.m_max : 0;
   const int64_t grid = tile_items(A, tiles);
   st = check_items(fn, grid > join ? grid : join);
@@ -1446,8 +1446,8 @@ int backward(const char* fn, const tdp_seqs* q_seqs, const tdp_seqs* k_seqs, con
   const DkvSplit sp = dkv_split(window, *q_seqs, *k_seqs, q->heads, k->heads);
   A.split_blocks = (uint32_t)sp.blocks;
   const int64_t heads = (int64_t)k_seqs->num_seqs * k->heads;
-  const int64_t qt = A.blocks * heads;
-  const int64_t kt = dkv_blocks(*k_seqs, k->heads) + sp.blocks * heads * (sp.n - 1);
+  const int64_t qt = attention_blocks(*q_seqs, q->heads, k->heads);
+  const int64_t kt = dkv_blocks(*k_seqs, k->heads) + (sp.n > 1 ? sp.blocks * heads * (sp.n - 1) : 0);
   const int64_t sum = sp.n > 1 ? (heads * sp.rows * 32 + kTok - 1) / kTok : 0;
   for (const int64_t n : {tile_items(A, qt), tile_items(A, kt), sum})
     if (st == TDP_OK) st = check_items(fn, n);

@@ -80,6 +80,8 @@ int check_seqs(const char* fn, const char* name, const tdp_seqs* s, SeqsDev* out
 int check_heads(const char* fn, const char* name, const tdp_heads* t, const tdp_seqs* s, int32_t head_dim,
                 int32_t dtype, HeadsDev* out);
 int check_rows(const char* fn, const char* name, const tdp_rows* t, int32_t dtype, HeadsDev* out);
+constexpr int32_t kMaxHeads = 65536;
+int check_head_counts(const char* fn, int32_t q_heads, int32_t k_heads, int32_t head_dim);
 // Workgroups of `rows`-row blocks over every sequence: S * ceil(max_rows / rows).
 inline int64_t seq_blocks(const tdp_seqs& s, int rows) {
   return (int64_t)s.num_seqs * ((s.max_rows + rows - 1) / rows);
@@ -116,9 +118,15 @@ constexpr int kAttnBlockK = 64;   // keys per step
 constexpr int kAttnSplitBlocks = 512;
 constexpr int kAttnSplitKeys = 256;
 constexpr int kAttnMaxSplits = 64;
+// `per` blocks for each head of each sequence.  More of these than any launch holds
+// are returned as they are, which is refused too and keeps products in 64 bits.
+inline int64_t head_blocks(const tdp_seqs& s, int32_t heads, int64_t per) {
+  const int64_t n = (int64_t)s.num_seqs * heads;
+  return n > (1 << 24) ? n : n * per;
+}
 inline int64_t attention_blocks(const tdp_seqs& q, int32_t q_heads, int32_t k_heads) {
   const int64_t m = (int64_t)q.max_rows * (q_heads / k_heads);
-  return (int64_t)q.num_seqs * k_heads * ((m + kAttnBlockQ - 1) / kAttnBlockQ);
+  return head_blocks(q, k_heads, (m + kAttnBlockQ - 1) / kAttnBlockQ);
 }
 // Keys that a block of queries walks at most.
 inline int64_t window_keys(const tdp_window* w, const tdp_seqs& q, const tdp_seqs& k) {
@@ -153,7 +161,7 @@ inline int64_t attention_workspace(const tdp_seqs& q, const tdp_seqs& k, const t
 // of 4 x 8960 rows, 16 heads on 4 of 64, a 77-token prompt: 130 us against 708).
 constexpr int kDkvSplitRows = 512;
 inline int64_t dkv_blocks(const tdp_seqs& k, int32_t k_heads) {
-  return (int64_t)k.num_seqs * k_heads * ((k.max_rows + kAttnBlockQ - 1) / kAttnBlockQ);
+  return head_blocks(k, k_heads, (k.max_rows + kAttnBlockQ - 1) / kAttnBlockQ);
 }
 inline int dkv_splits(const tdp_seqs& k, int64_t rows, int32_t q_heads, int32_t k_heads) {
   const int64_t blocks = dkv_blocks(k, k_heads);
@@ -182,7 +190,7 @@ inline DkvSplit dkv_split(const tdp_window* w, const tdp_seqs& q, const tdp_seqs
   }
   DkvSplit sp = {dkv_splits(k, w && w->sinks ? q.max_rows : seen, q_heads, k_heads), all, k.max_rows};
   if (sp.n == 1 && w && w->sinks) {
-    const int64_t lead = ((int64_t)w->sinks + kAttnBlockQ - 1) / kAttnBlockQ, heavy = lead * k.num_seqs * k_heads;
+    const int64_t lead = ((int64_t)w->sinks + kAttnBlockQ - 1) / kAttnBlockQ, heavy = head_blocks(k, k_heads, lead);
     const int64_t part = seen > kDkvSplitRows ? seen : kDkvSplitRows;
     int64_t n = q.max_rows / part;
     if (n > 2 * kAttnSplitBlocks / heavy) n = 2 * kAttnSplitBlocks / heavy;  // many blocks fill the GPU unsplit

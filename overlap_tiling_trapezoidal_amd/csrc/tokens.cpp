@@ -41,8 +41,8 @@ int check_heads(const char* fn, const char* name, const tdp_heads* t, const tdp_
                 int32_t dtype, HeadsDev* out) {
   if (!t || !t->data) return fail(TDP_EINVAL, "%s: null %s", fn, name);
   if (reinterpret_cast<uintptr_t>(t->data) & 15) return fail(TDP_EINVAL, "%s: %s must be 16-byte aligned", fn, name);
-  if (t->heads < 1 || t->heads > 65536)
-    return fail(TDP_ESHAPE, "%s: %s.heads %d outside [1, 65536]", fn, name, t->heads);
+  if (t->heads < 1 || t->heads > kMaxHeads)
+    return fail(TDP_ESHAPE, "%s: %s.heads %d outside [1, %d]", fn, name, t->heads, kMaxHeads);
   const int64_t unit = 16 / dtype_bytes(dtype);
   const int64_t st[3] = {t->seq_stride, t->row_stride, t->head_stride};
   for (int i = 0; i < 3; ++i)
@@ -54,6 +54,13 @@ int check_heads(const char* fn, const char* name, const tdp_heads* t, const tdp_
   out->row_stride = t->row_stride;
   out->head_stride = t->head_stride;
   out->heads = t->heads;
+  return TDP_OK;
+}
+
+int check_head_counts(const char* fn, int32_t q_heads, int32_t k_heads, int32_t head_dim) {
+  if (q_heads < 1 || k_heads < 1 || q_heads > kMaxHeads || q_heads % k_heads != 0 || head_dim < 8)
+    return fail(TDP_ESHAPE, "%s: needs heads in [1, %d], q's a multiple of k's, and head_dim >= 8 (got %d, %d, %d)", fn,
+                kMaxHeads, q_heads, k_heads, head_dim);
   return TDP_OK;
 }
 
@@ -176,18 +183,18 @@ int64_t tdp_qk_norm_rope_workspace(const tdp_rope* rope, const tdp_seqs* seqs, i
 
 int64_t tdp_attention_workspace(const tdp_seqs* q_seqs, const tdp_seqs* k_seqs, int32_t q_heads, int32_t k_heads,
                                 int32_t head_dim) {
-  if (check_seqs("tdp_attention_workspace", "q_seqs", q_seqs, nullptr) != TDP_OK ||
-      check_seqs("tdp_attention_workspace", "k_seqs", k_seqs, nullptr) != TDP_OK || q_heads < 1 || k_heads < 1 ||
-      q_heads % k_heads != 0 || head_dim < 8)
+  const char* fn = "tdp_attention_workspace";
+  if (check_seqs(fn, "q_seqs", q_seqs, nullptr) != TDP_OK || check_seqs(fn, "k_seqs", k_seqs, nullptr) != TDP_OK ||
+      check_head_counts(fn, q_heads, k_heads, head_dim) != TDP_OK)
     return 0;
   return attention_workspace(*q_seqs, *k_seqs, nullptr, q_heads, k_heads, head_dim);
 }
 
 int64_t tdp_attention_backward_workspace(const tdp_seqs* q_seqs, const tdp_seqs* k_seqs, int32_t q_heads,
                                          int32_t k_heads, int32_t head_dim) {
-  if (check_seqs("tdp_attention_backward_workspace", "q_seqs", q_seqs, nullptr) != TDP_OK ||
-      check_seqs("tdp_attention_backward_workspace", "k_seqs", k_seqs, nullptr) != TDP_OK || q_heads < 1 ||
-      k_heads < 1 || q_heads % k_heads != 0 || head_dim < 8)
+  const char* fn = "tdp_attention_backward_workspace";
+  if (check_seqs(fn, "q_seqs", q_seqs, nullptr) != TDP_OK || check_seqs(fn, "k_seqs", k_seqs, nullptr) != TDP_OK ||
+      check_head_counts(fn, q_heads, k_heads, head_dim) != TDP_OK)
     return 0;
   return backward_workspace(*q_seqs, *k_seqs, nullptr, q_heads, k_heads, head_dim);
 }
@@ -196,8 +203,8 @@ int64_t tdp_window_attention_workspace(const tdp_seqs* q_seqs, const tdp_seqs* k
                                        int32_t q_heads, int32_t k_heads, int32_t head_dim) {
   const char* fn = "tdp_window_attention_workspace";
   if (check_window(fn, window) != TDP_OK || check_seqs(fn, "q_seqs", q_seqs, nullptr) != TDP_OK ||
-      check_seqs(fn, "k_seqs", k_seqs, nullptr) != TDP_OK || q_heads < 1 || k_heads < 1 || q_heads % k_heads != 0 ||
-      head_dim < 8)
+      check_seqs(fn, "k_seqs", k_seqs, nullptr) != TDP_OK ||
+      check_head_counts(fn, q_heads, k_heads, head_dim) != TDP_OK)
     return 0;
   return attention_workspace(*q_seqs, *k_seqs, window, q_heads, k_heads, head_dim);
 }
@@ -207,8 +214,8 @@ int64_t tdp_window_attention_backward_workspace(const tdp_seqs* q_seqs, const td
                                                 int32_t head_dim) {
   const char* fn = "tdp_window_attention_backward_workspace";
   if (check_window(fn, window) != TDP_OK || check_seqs(fn, "q_seqs", q_seqs, nullptr) != TDP_OK ||
-      check_seqs(fn, "k_seqs", k_seqs, nullptr) != TDP_OK || q_heads < 1 || k_heads < 1 || q_heads % k_heads != 0 ||
-      head_dim < 8)
+      check_seqs(fn, "k_seqs", k_seqs, nullptr) != TDP_OK ||
+      check_head_counts(fn, q_heads, k_heads, head_dim) != TDP_OK)
     return 0;
   return backward_workspace(*q_seqs, *k_seqs, window, q_heads, k_heads, head_dim);
 }

@@ -242,3 +242,37 @@ def test_window_attention_counts_what_it_launches(call):
         one.update({name: heads32(1) for name in ("dout", "dq", "dk", "dv")})
     assert call(qs=few, ks=few, w=window(back=tdp.TDP_WINDOW_ALL), **one) == tdp.TDP_ESHAPE
     assert "work-items" in tdp.tdp_last_error()
+
+
+ENORMOUS = dict(num_seqs=1 << 30, max_rows=1 << 24, total_rows=2 ** 31 - 1, row_range=P)
+
+
+@pytest.mark.parametrize("sinks", [0, 2, (1 << 24) - 200, 1 << 25])
+def test_attention_workspaces_of_enormous_counts(sinks):
+    """Counts whose products pass 64 bits end in a size or a refusal, not in a division by zero."""
+    lib, s, r = tdp.load_library(), seqs(**ENORMOUS), ctypes.byref
+    w = window(back=5, sinks=sinks)
+    for heads in (1, 4, 65535, 65536):
+        rows = heads * s.total_rows * 8
+        assert lib.tdp_window_attention_workspace(r(s), r(s), r(w), heads, heads, 64) == 0
+        assert lib.tdp_attention_workspace(r(s), r(s), heads, heads, 64) == 0
+        for got in (lib.tdp_window_attention_backward_workspace(r(s), r(s), r(w), heads, heads, 64),
+                    lib.tdp_attention_backward_workspace(r(s), r(s), heads, heads, 64)):
+            assert rows <= got < rows + 256
+    for q, k in ((65537, 65537), (1 << 18, 1 << 18), (1 << 30, 1)):
+        for got in (lib.tdp_window_attention_workspace(r(s), r(s), r(w), q, k, 64),
+                    lib.tdp_window_attention_backward_workspace(r(s), r(s), r(w), q, k, 64),
+                    lib.tdp_attention_workspace(r(s), r(s), q, k, 64),
+                    lib.tdp_attention_backward_workspace(r(s), r(s), q, k, 64)):
+            assert got == 0 and "heads" in tdp.tdp_last_error()
+
+
+@pytest.mark.device_abi
+@pytest.mark.parametrize("heads", [1, 4, 65536])
+@pytest.mark.parametrize("call", [window_call, window_backward_call], ids=["forward", "backward"])
+def test_window_attention_refuses_enormous_counts(call, heads):
+    s, h = seqs(**ENORMOUS), heads32(heads, head_stride=0, row_stride=64, seq_stride=64)
+    ts = ("q", "k", "v", "out") + (("dout", "dq", "dk", "dv") if call is window_backward_call else ())
+    for w in (window(back=5), window(back=tdp.TDP_WINDOW_ALL, sinks=(1 << 24) - 200)):
+        assert call(qs=s, ks=s, w=w, **{name: h for name in ts}) == tdp.TDP_ESHAPE
+        assert "work-items" in tdp.tdp_last_error()
