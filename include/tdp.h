@@ -732,7 +732,8 @@ int tdp_window_attention_backward(const tdp_seqs* q_seqs, const tdp_seqs* k_seqs
 /* What a denoising transformer's layer computes on the same rows before and
  * after its attention.  The calls below take (rows, features) tensors over
  * sequences as above: unused rows may hold anything in inputs and are 0 in
- * outputs, rows outside every range are left alone.  Errors as tdp_rope_apply. */
+ * outputs, rows outside every range are left alone.  num_seqs is at most 2^30
+ * here.  Errors as tdp_rope_apply. */
 
 /* A (rows, features) tensor: element strides, features contiguous, placed as
  * tdp_heads' rows.  data is 16-byte aligned and both strides are multiples of

@@ -121,6 +121,9 @@ inline int64_t weight_workspace(const tdp_seqs& s, int32_t weights, int32_t in_f
   const ProductShape sh = weight_shape(s, weights, in_features, out_features, dtype);
   return sh.splits == 1 ? 0 : align256((int64_t)2 * sh.splits * in_features * out_features * 4);
 }
+// Sequences and the weights that they share: at most 2^30, so that sums of two such
+// numbers stay in 32 bits, here and in the kernels.
+int check_weights(const char* fn, const tdp_seqs* seqs, int32_t num_weights);
 int check_product(const char* fn, const tdp_seqs* seqs, int32_t num_weights, int32_t in_features,
                   int32_t out_features);
 

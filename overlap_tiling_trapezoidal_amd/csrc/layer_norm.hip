@@ -337,9 +337,8 @@ int begin(const char* fn, const tdp_seqs* seqs, const tdp_rows* x, const float* 
   int st = check_seqs(fn, "seqs", seqs, &A->seqs);
   if (st == TDP_OK) st = check_rows(fn, "x", x, dtype, &A->x);
   if (st != TDP_OK) return st;
-  if (num_weights < 1 || num_weights > seqs->num_seqs)
-    return fail(TDP_EINVAL, "%s: num_weights must be in [1, num_seqs] (got %d of %d)", fn, num_weights,
-                seqs->num_seqs);
+  st = check_weights(fn, seqs, num_weights);
+  if (st != TDP_OK) return st;
   if (reinterpret_cast<uintptr_t>(weight) & 3) return fail(TDP_EINVAL, "%s: weight must be 4-byte aligned", fn);
   A->w = weight;
   A->C = channels;

@@ -64,6 +64,15 @@ int check_head_counts(const char* fn, int32_t q_heads, int32_t k_heads, int32_t 
   return TDP_OK;
 }
 
+int check_weights(const char* fn, const tdp_seqs* seqs, int32_t num_weights) {
+  if (seqs->num_seqs > (1 << 30))
+    return fail(TDP_ESHAPE, "%s: num_seqs %d exceeds 2^30", fn, seqs->num_seqs);
+  if (num_weights < 1 || num_weights > seqs->num_seqs)
+    return fail(TDP_EINVAL, "%s: num_weights must be in [1, num_seqs] (got %d of %d)", fn, num_weights,
+                seqs->num_seqs);
+  return TDP_OK;
+}
+
 int check_product(const char* fn, const tdp_seqs* seqs, int32_t num_weights, int32_t in_features,
                   int32_t out_features) {
   const int st = check_seqs(fn, "seqs", seqs, nullptr);
@@ -72,10 +81,7 @@ int check_product(const char* fn, const tdp_seqs* seqs, int32_t num_weights, int
     if (f < 8 || f % 8 != 0 || f > TDP_MAX_FEATURES)
       return fail(TDP_ESHAPE, "%s: features must be multiples of 8 in [8, %d] (got %d and %d)", fn, TDP_MAX_FEATURES,
                   in_features, out_features);
-  if (num_weights < 1 || num_weights > seqs->num_seqs)
-    return fail(TDP_EINVAL, "%s: num_weights must be in [1, num_seqs] (got %d of %d)", fn, num_weights,
-                seqs->num_seqs);
-  return TDP_OK;
+  return check_weights(fn, seqs, num_weights);
 }
 
 int check_window(const char* fn, const tdp_window* w) {
@@ -223,11 +229,11 @@ int64_t tdp_window_attention_backward_workspace(const tdp_seqs* q_seqs, const td
 int64_t tdp_layer_norm_workspace(const tdp_seqs* seqs, int32_t channels, int32_t num_weights) {
   const char* fn = "tdp_layer_norm_workspace";
   if (check_seqs(fn, "seqs", seqs, nullptr) != TDP_OK) return 0;
-  if (channels < 8 || channels % 8 != 0 || channels > TDP_MAX_CHANNELS || num_weights < 1 ||
-      num_weights > seqs->num_seqs) {
-    fail(TDP_ESHAPE, "%s: channels %d or num_weights %d out of range", fn, channels, num_weights);
+  if (channels < 8 || channels % 8 != 0 || channels > TDP_MAX_CHANNELS) {
+    fail(TDP_ESHAPE, "%s: channels %d out of range", fn, channels);
     return 0;
   }
+  if (check_weights(fn, seqs, num_weights) != TDP_OK) return 0;
   return align256(layer_norm_parts(*seqs, channels, num_weights) * num_weights * 2 * channels * 4);
 }
 

@@ -276,3 +276,20 @@ def test_window_attention_refuses_enormous_counts(call, heads):
     for w in (window(back=5), window(back=tdp.TDP_WINDOW_ALL, sinks=(1 << 24) - 200)):
         assert call(qs=s, ks=s, w=w, **{name: h for name in ts}) == tdp.TDP_ESHAPE
         assert "work-items" in tdp.tdp_last_error()
+
+
+@pytest.mark.device_abi
+@pytest.mark.parametrize("call", [norm_call, norm_backward_call, product_call, product_backward_call])
+def test_layers_refuse_enormous_counts(call):
+    """Past 2^30 sequences sums of counts would leave 32 bits; up to there the launch's limit is met or sizes hold."""
+    lib, r = tdp.load_library(), ctypes.byref
+    past = seqs(num_seqs=(1 << 30) + 1, max_rows=1, total_rows=1000, row_range=P)
+    for n in (1, 1 << 20, (1 << 30) + 1):
+        assert call(s=past, n=n) == tdp.TDP_ESHAPE and "2^30" in tdp.tdp_last_error()
+        assert lib.tdp_layer_norm_workspace(r(past), 128, n) == 0
+        for size in (lib.tdp_grouped_product_workspace, lib.tdp_grouped_product_backward_workspace):
+            assert size(r(past), n, 128, 128, tdp.TDP_F32) == 0
+    s = seqs(**ENORMOUS)
+    for n in (1, 513, 1 << 30):
+        assert call(s=s, n=n) == tdp.TDP_ESHAPE
+        assert lib.tdp_layer_norm_workspace(r(s), 8192, n) == -(-512 // n) * n * 2 * 8192 * 4
