@@ -80,7 +80,6 @@ struct ProductArgs {
   uint32_t nq;        // dW: tiles of W's rows
   int32_t pass;       // y, dx: kAll, kRounds or kRest
   bool flat;          // y, dx: one weight for all, blocks of the tensors' rows
-  FastDiv by_np;
 };
 
 // 16 bytes per lane from a buffer straight into 1 KB of LDS.  Written out because
