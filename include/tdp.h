@@ -32,9 +32,10 @@
  *   - The library owns only the host plan.  Every device buffer is allocated
  *     and freed by the caller; the library never allocates device memory.
  *   - The device operations only enqueue work on `stream` (a hipStream_t,
- *     NULL = the null stream) and return without synchronizing.  All
- *     arguments are validated before anything is enqueued, so an error
- *     leaves every output untouched.
+ *     NULL = the null stream) and return without synchronizing.  The buffers
+ *     and the stream belong to the device that is current.  All arguments are
+ *     validated before anything is enqueued, so an error leaves every output
+ *     untouched.
  *   - Results are deterministic: every output element has one writer and
  *     sums run in a fixed order; no floating-point value is added by atomics.
  *

@@ -979,6 +979,15 @@ def _heads(t, name, seqs: Sequences, head_dim, like, written=False):
     return tdp_heads(t.data_ptr(), *lay)
 
 
+def _on(device, call, *args):
+    """A library call with `device` current, as its launches need."""
+    import torch
+    if device.index is None or device.index == torch.cuda.current_device():
+        return _check(call(*args))
+    with torch.cuda.device(device):
+        return _check(call(*args))
+
+
 def _vec(t, name, dtype, numel, device):
     return ctypes.c_void_p(None) if t is None else _ptr(t, name, dtype, numel, device)
 
@@ -995,21 +1004,21 @@ def tdp_rope_apply(rope: Rope, seqs: Sequences, pos, x, y, inverse=False, stream
     ``inverse`` turns back, which is also the gradient.  y may be x."""
     ref = ctypes.byref
     D = rope.cfg.head_dim
-    _check(load_library().tdp_rope_apply(
+    _on(x.device, load_library().tdp_rope_apply,
         rope.handle, ref(seqs.c), _pos_ptr(rope, seqs, pos, x.device), ref(_heads(x, "x", seqs, D, x)),
         ref(_heads(y, "y", seqs, D, x, True)), _dtype_code(x, "x"), int(bool(inverse)),
-        _stream_handle(stream, x.device)))
+        _stream_handle(stream, x.device))
 
 
 def tdp_qk_norm_rope(rope: Rope, seqs: Sequences, pos, q, k, q_weight, k_weight, q_out, k_out, eps=1e-6, stream=None):
     """Enqueue the norm of every query and key head (times fp32 weights, None: ones) and its rotation."""
     import torch
     ref, D, dev = ctypes.byref, rope.cfg.head_dim, q.device
-    _check(load_library().tdp_qk_norm_rope(
+    _on(dev, load_library().tdp_qk_norm_rope,
         rope.handle, ref(seqs.c), _pos_ptr(rope, seqs, pos, dev), ref(_heads(q, "q", seqs, D, q)),
         ref(_heads(k, "k", seqs, D, q)), _vec(q_weight, "q_weight", torch.float32, D, dev),
         _vec(k_weight, "k_weight", torch.float32, D, dev), ref(_heads(q_out, "q_out", seqs, D, q, True)),
-        ref(_heads(k_out, "k_out", seqs, D, q, True)), eps, _dtype_code(q, "q"), _stream_handle(stream, dev)))
+        ref(_heads(k_out, "k_out", seqs, D, q, True)), eps, _dtype_code(q, "q"), _stream_handle(stream, dev))
 
 
 def allocate_qk_norm_rope_workspace(rope: Rope, seqs: Sequences, q_heads: int, k_heads: int, device="cuda"):
@@ -1027,13 +1036,13 @@ def tdp_qk_norm_rope_backward(rope: Rope, seqs: Sequences, pos, q, k, q_weight, 
     ref, D, dev = ctypes.byref, rope.cfg.head_dim, q.device
     sq, sk = _heads(q, "q", seqs, D, q), _heads(k, "k", seqs, D, q)
     need = load_library().tdp_qk_norm_rope_workspace(rope.handle, ref(seqs.c), sq.heads, sk.heads)
-    _check(load_library().tdp_qk_norm_rope_backward(
+    _on(dev, load_library().tdp_qk_norm_rope_backward,
         rope.handle, ref(seqs.c), _pos_ptr(rope, seqs, pos, dev), ref(sq), ref(sk),
         _vec(q_weight, "q_weight", torch.float32, D, dev), _vec(k_weight, "k_weight", torch.float32, D, dev),
         ref(_heads(dq_out, "dq_out", seqs, D, q)), ref(_heads(dk_out, "dk_out", seqs, D, q)),
         ref(_heads(dq, "dq", seqs, D, q, True)), ref(_heads(dk, "dk", seqs, D, q, True)),
         _vec(dq_weight, "dq_weight", torch.float32, D, dev), _vec(dk_weight, "dk_weight", torch.float32, D, dev),
-        eps, _dtype_code(q, "q"), _ptr(workspace, "workspace", torch.uint8, need, dev), _stream_handle(stream, dev)))
+        eps, _dtype_code(q, "q"), _ptr(workspace, "workspace", torch.uint8, need, dev), _stream_handle(stream, dev))
 
 
 def allocate_attention_workspace(q_seqs: Sequences, k_seqs: Sequences, q_heads: int, k_heads: int, head_dim: int,
@@ -1063,13 +1072,13 @@ def tdp_attention(q_seqs: Sequences, k_seqs: Sequences, q, k, v, out, lse=None, 
     ref, D, dev = ctypes.byref, q.shape[-1], q.device
     sq, sk = _heads(q, "q", q_seqs, D, q), _heads(k, "k", k_seqs, D, q)
     need = load_library().tdp_attention_workspace(ref(q_seqs.c), ref(k_seqs.c), sq.heads, sk.heads, D)
-    _check(load_library().tdp_attention(
+    _on(dev, load_library().tdp_attention,
         ref(q_seqs.c), ref(k_seqs.c), ref(sq), ref(sk), ref(_heads(v, "v", k_seqs, D, q)),
         _vec(key_bias, "key_bias", torch.float32, k_seqs.total_rows, dev),
         ref(_heads(out, "out", q_seqs, D, q, True)),
         _vec(lse, "lse", torch.float32, sq.heads * q_seqs.total_rows, dev), D ** -0.5 if scale is None else scale, D,
         _dtype_code(q, "q"), _ptr(workspace, "workspace", torch.uint8, need, dev) if need else ctypes.c_void_p(None),
-        _stream_handle(stream, dev)))
+        _stream_handle(stream, dev))
 
 
 def tdp_attention_backward(q_seqs: Sequences, k_seqs: Sequences, q, k, v, out, lse, dout, dq, dk, dv, workspace,
@@ -1079,14 +1088,14 @@ def tdp_attention_backward(q_seqs: Sequences, k_seqs: Sequences, q, k, v, out, l
     ref, D, dev = ctypes.byref, q.shape[-1], q.device
     sq, sk = _heads(q, "q", q_seqs, D, q), _heads(k, "k", k_seqs, D, q)
     need = load_library().tdp_attention_backward_workspace(ref(q_seqs.c), ref(k_seqs.c), sq.heads, sk.heads, D)
-    _check(load_library().tdp_attention_backward(
+    _on(dev, load_library().tdp_attention_backward,
         ref(q_seqs.c), ref(k_seqs.c), ref(sq), ref(sk), ref(_heads(v, "v", k_seqs, D, q)),
         _vec(key_bias, "key_bias", torch.float32, k_seqs.total_rows, dev), ref(_heads(out, "out", q_seqs, D, q)),
         _ptr(lse, "lse", torch.float32, sq.heads * q_seqs.total_rows, dev),
         ref(_heads(dout, "dout", q_seqs, D, q)), ref(_heads(dq, "dq", q_seqs, D, q, True)),
         ref(_heads(dk, "dk", k_seqs, D, q, True)), ref(_heads(dv, "dv", k_seqs, D, q, True)),
         D ** -0.5 if scale is None else scale, D, _dtype_code(q, "q"),
-        _ptr(workspace, "workspace", torch.uint8, need, dev), _stream_handle(stream, dev)))
+        _ptr(workspace, "workspace", torch.uint8, need, dev), _stream_handle(stream, dev))
 
 
 def make_window(step=1, back=None, ahead=0, sinks=0) -> tdp_window:
@@ -1094,15 +1103,6 @@ def make_window(step=1, back=None, ahead=0, sinks=0) -> tdp_window:
     (None: all of them), the first ``sinks`` rows always."""
     every = lambda n: TDP_WINDOW_ALL if n is None else n  # noqa: E731
     return tdp_window(step, every(back), every(ahead), sinks)
-
-
-def _on(device, call, *args):
-    """A library call with `device` current, as its launches need."""
-    import torch
-    if device.index is None or device.index == torch.cuda.current_device():
-        return _check(call(*args))
-    with torch.cuda.device(device):
-        return _check(call(*args))
 
 
 def allocate_window_attention_workspace(q_seqs: Sequences, k_seqs: Sequences, window: tdp_window, q_heads: int,
