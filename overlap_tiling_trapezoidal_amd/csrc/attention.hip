@@ -181,12 +181,13 @@ inline uint32_t xcd_grid(uint32_t tiles) { return (tiles + 7) / 8 * 8; }
 // the keys (causal ones) make ranges of unequal work, and items far apart share no
 // keys: chunks of 16 neighbours are dealt in turn, one XCD further each round, so
 // that none gets the ends of all sequences (8 prompts of 2048 to 4096 tokens, 16
-// heads on 4 of 64: causal 233 us against 280, gradients 741 against 890; window of
-// 1024 159 against 171).  Equal work keeps equal ranges (frames of the 24576-token
-// latent: 1283 us against 1308), and so do few items, whose chunks would end at
-// different times (gradients of 8192 causal tokens, 8 heads of 128: 579 us against
-// 706).  Queries go last rows first: early ones see less (window of 1024: 151 us
-// against 158).
+// heads on 4 of 64: causal 286 us against 298, gradients 791 against 969; window of
+// 1024 145 and 471 either way).  Equal work keeps equal ranges (24 frames of 1024
+// rows, four in view, 16 heads of 128: 884 us against 922), and so do few items,
+// whose chunks would end at different times (gradients of 8192 causal tokens, 8
+// heads of 128: 544 us against 689).  Queries go last rows first: early ones see
+// less (those tokens 184 us against 194, the frames 884 against 901; prompts in a
+// window of 1024 see as much anywhere and take 145 against 144).
 __device__ inline uint32_t chunk_item(uint32_t chunk) {
   const uint32_t slot = blockIdx.x >> 3, c = slot / chunk;
   return (c * 8 + ((blockIdx.x + c) & 7)) * chunk + (slot - c * chunk);
@@ -779,8 +780,9 @@ __device__ inline float neg_lse(float lse) {
 // 16 heads of 128: 280 us, 0.88 PFLOP/s of its three products (324 us when it ran
 // its third product one block behind the scores, as the forward does); its 1152
 // workgroups are 2.25 rounds of the 512 places, run as three, and at head_dim 128
-// it spills three registers.  Its keys are not split: few tiles of few heads leave
-// CUs idle (one of 2048 rows, 3 heads of 128: 48 workgroups).
+// it spills three registers (with a window 21, read back only where holes are
+// cleared and behind the loop).  Its keys are not split: few tiles of few heads
+// leave CUs idle (one of 2048 rows, 3 heads of 128: 48 workgroups).
 // The form with a bias takes one workgroup per CU at head_dim 128, where it would
 // spill in the loop (gradients of 8 x 480 rows on 343 keys, 9 heads of 96: 70 us
 // against 81; of 4 x 2240 rows on 512 keys, 16 heads of 128: 247 against 302).
@@ -965,8 +967,9 @@ __device__ inline void load_stats(const f32x2* from, int left, int wave, int lan
 // rows, the blocks are split over workgroups, whose sums are joined by
 // attn_sum_kernel.  On 4 x 2240 rows, 16 heads of 128: 443 us, 0.74 PFLOP/s of its
 // four products; K, V and the sums fill all 512 registers (11 spill, 22 with a
-// bias), so one wave per SIMD has nothing but its own instructions to cover its
-// waits, and the 1152 workgroups are 4.5 rounds of the 256 places, run as five.
+// bias, 7 with a window), so one wave per SIMD has nothing but its own instructions
+// to cover its waits, and the 1152 workgroups are 4.5 rounds of the 256 places, run
+// as five.
 constexpr int kDkvRows = 64;
 template <int T, int DP, bool BIAS, bool WIN>
 __global__ __launch_bounds__(kTok, T == TDP_BF16 && DP <= 64 ? 2 : 1) void attn_dkv_kernel(const AttnArgs A) {
